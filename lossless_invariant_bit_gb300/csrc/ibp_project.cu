@@ -36,13 +36,9 @@
 //
 // Every wait on an mbarrier gives up after about two seconds, records
 // IBP_ETIMEOUT and lets the CTA free its tensor memory and exit.
-#include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <mutex>
-
 #include "ibp_internal.cuh"
+#include "ibp_sm103.cuh"
+#include "ibp_tma.cuh"
 
 namespace ibp {
 namespace {
@@ -93,51 +89,6 @@ struct PjShape {
   static constexpr uint32_t TMEM = ACC * BN;             // accumulator columns (<= 512)
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ uint64_t global_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-
-__device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
-               : "memory");
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
-               "r"(bytes)
-               : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint32_t a, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(done)
-      : "r"(a), "r"(parity), "r"(1000000u)
-      : "memory");
-  return done != 0u;
-}
-
-// Wait for the phase of `parity` to complete, for at most ~2 s (the clock is
-// read only once the first test has failed).
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
-  const uint32_t a = smem_addr(bar);
-  if (mbar_try(a, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (true) {
-    if (mbar_try(a, parity)) return true;
-    if (global_ns() - t0 > 2000000000ull) return false;
-  }
-}
-
 // One TMA copy of a 3-D box {64 elements, rows, k-blocks} into shared memory
 // (coordinates: element 0, first row, first k-block), completing on `bar`.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
@@ -149,37 +100,10 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Shared-memory matrix descriptor of a K-major tile written by TMA with the
-// 128-byte swizzle: rows of 128 bytes, 8-row atoms 1024 bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);  // start address
-  d |= (uint64_t)1u << 16;                           // leading byte offset (unused here)
-  d |= (uint64_t)(1024u >> 4) << 32;                 // stride byte offset: one 8-row atom
-  d |= (uint64_t)1u << 46;                           // descriptor version
-  d |= (uint64_t)2u << 61;                           // 128-byte swizzle
-  return d;
-}
-
 // Instruction descriptor: kind::f16, fp32 accumulator, A and B of one 16-bit
 // type (fp16 or bf16), both K-major, M = 128, N = bn.
 __device__ __forceinline__ uint32_t mma_idesc(uint32_t bf16, uint32_t bn) {
   return (1u << 4) | (bf16 << 7) | (bf16 << 10) | ((bn >> 3) << 17) | ((kPjBM >> 4) << 24);
-}
-
-__device__ __forceinline__ void mma_f16(uint32_t tmem, uint64_t adesc, uint64_t bdesc,
-                                        uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
-      : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -195,24 +119,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         "=r"(r[31])
       : "r"(taddr));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi, uint32_t bf16) {
-  if (bf16) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float to_float(uint16_t v, uint32_t bf16) {
-  if (bf16) return __uint_as_float((uint32_t)v << 16);
-  return __half2float(__ushort_as_half(v));
-}
-
-__device__ __forceinline__ void set_status(uint32_t* st, uint32_t code) {
-  atomicCAS(st, 0u, code);
 }
 
 template <int kSeg, int kAR>
@@ -523,31 +429,6 @@ __global__ void __launch_bounds__(128) k_project_assemble(ProjectArgs a, uint32_
   }
 }
 
-// cuTensorMapEncodeTiled, looked up once through the runtime (the library
-// links no driver library).
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-std::mutex g_enc_mu;
-EncodeTiledFn g_encode = nullptr;
-
-EncodeTiledFn encode_fn() {
-  std::lock_guard<std::mutex> lock(g_enc_mu);
-  if (!g_encode) {
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess || fn == nullptr) {
-      cudaGetLastError();
-      return nullptr;
-    }
-    g_encode = reinterpret_cast<EncodeTiledFn>(fn);
-  }
-  return g_encode;
-}
-
 // A 3-D map of a row-major [rows, k] matrix of 16-bit values seen as
 // {64 elements, rows, k / 64 k-blocks} (the k-blocks 128 bytes apart), boxes
 // of {64, box_rows, box_kb} with the 128-byte swizzle: box_kb K-major tiles
@@ -555,7 +436,7 @@ EncodeTiledFn encode_fn() {
 // zero.
 bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t k, uint32_t box_rows,
               uint32_t box_kb, uint32_t bf16) {
-  EncodeTiledFn f = encode_fn();
+  const EncodeTiledFn f = encode_tiled();
   if (!f) return false;
   const cuuint64_t dims[3] = {kPjBK, rows, k / kPjBK};
   const cuuint64_t strides[2] = {k * 2u, kPjBK * 2u};
@@ -565,34 +446,6 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t k, uin
            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Raise a kernel's dynamic shared-memory limit to `smem` once per device (a
-// call being captured into a CUDA graph then sets nothing).
-cudaError_t smem_limit(const void* fn, size_t smem) {
-  struct Seen {
-    const void* fn;
-    int dev;
-    size_t smem;
-  };
-  static std::mutex mu;
-  static Seen seen[64];
-  static int n_seen = 0;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-  std::lock_guard<std::mutex> lock(mu);
-  for (int i = 0; i < n_seen; ++i)
-    if (seen[i].fn == fn && seen[i].dev == dev && seen[i].smem >= smem) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  for (int i = 0; i < n_seen; ++i)
-    if (seen[i].fn == fn && seen[i].dev == dev) {
-      seen[i].smem = smem;
-      return cudaSuccess;
-    }
-  if (n_seen < 64) seen[n_seen++] = Seen{fn, dev, smem};
-  return cudaSuccess;
 }
 
 template <int kSeg, int kAR>
