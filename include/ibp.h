@@ -445,6 +445,151 @@ IBP_API ibp_status ibp_project_compress(ibp_store* store, const void* x, uint64_
                                         void* workspace, uint64_t workspace_bytes,
                                         ibp_stream_t stream);
 
+/* ---------------------------------------------------------------- paged K/V
+ * A paged K/V cache in HBM: where a served model's keys and values live before
+ * they are compressed to host slots (ibp_compress) and after they have been
+ * fetched back (ibp_gather_decompress).  With token_stride = kv_heads *
+ * head_dim * 2 and head_stride = head_dim * 2 a token's keys are one IBP row.
+ *
+ * Position p of sequence s lives in page page_table[s][p / page_tokens], at
+ * token p % page_tokens.  A call works on a ragged batch: sequence s has
+ * kv_lens[s] tokens in the cache, of which the last q_starts[s + 1] -
+ * q_starts[s] are new; new token i (row q_starts[s] + i of the call's [n_tokens,
+ * heads, head_dim] arrays) sits at position kv_lens[s] - (number of new
+ * tokens) + i.  The arrays are read on the device, so a captured call follows
+ * their contents.  A handle knows the geometry and owns a status word; it may be
+ * used on several streams at once.
+ *
+ * Errors that a kernel finds set the handle's status word: IBP_ERANGE for
+ * q_starts that decrease or pass n_tokens or max_q_tokens (such a sequence is left out),
+ * kv_lens outside [0, max_pages * page_tokens] (taken as 0), and, where it is
+ * needed, a page id outside [0, n_pages): nothing is read or written there, and
+ * attention zero-fills the rows that had to read it. */
+typedef struct ibp_paged ibp_paged;
+
+typedef struct {
+  void* k;               /* device, 16-byte aligned: the key pages */
+  void* v;               /* device, 16-byte aligned: the value pages */
+  uint64_t page_stride;  /* bytes between pages, heads and tokens of both, */
+  uint64_t head_stride;  /* multiples of 16 */
+  uint64_t token_stride;
+  uint32_t n_pages;
+  uint32_t page_tokens;  /* a power of two, 8 to 256 */
+  uint32_t kv_heads;
+  uint32_t head_dim;     /* a multiple of 16, at most IBP_PAGED_MAX_HEAD_DIM */
+  uint32_t dtype;        /* 0: fp16, 1: bf16 */
+} ibp_paged_desc;
+
+typedef struct {
+  const int32_t* page_table;  /* device [n_seqs, table_stride] */
+  const int32_t* kv_lens;     /* device [n_seqs] */
+  const int32_t* q_starts;    /* device [n_seqs + 1] */
+  uint64_t table_stride;      /* entries between rows of the page table */
+  uint32_t n_seqs;
+  uint32_t max_pages;         /* columns of the page table */
+  uint32_t n_tokens;          /* rows of the new tokens' arrays */
+  uint32_t max_q_tokens;      /* most new tokens of one sequence */
+} ibp_paged_batch;
+
+#define IBP_PAGED_MAX_HEAD_DIM 128u
+#define IBP_PAGED_MAX_SELECTED 65536u
+/* device workspace bytes of ibp_paged_attention */
+#define IBP_PAGED_WORKSPACE_BYTES (96ull << 20)
+
+/* Create a handle on a cache (the descriptor is copied, the pages stay the
+ * caller's).  Allocates a status word on the current device.  Errors:
+ * IBP_EINVAL (geometry), IBP_EALIGN, IBP_ENOMEM, IBP_ECUDA. */
+IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc);
+
+/* Free a handle (synchronises the device; the pages are not touched).  NULL is a no-op. */
+IBP_API ibp_status ibp_paged_destroy(ibp_paged* cache);
+
+/* As ibp_stream_status, for a paged cache's status word. */
+IBP_API ibp_status ibp_paged_status(const ibp_paged* cache, ibp_stream_t stream, ibp_status* out,
+                                    int reset);
+
+/* Append: the new tokens' keys and values into their pages, and their queries
+ * beside them, normalised for each head and rotated by position on the way:
+ *   y = x * rsqrt(mean(x^2) + eps) * norm            (norm NULL: y = x)
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)     (cos_sin NULL: no rotation)
+ * for queries and keys; values go as they are.  Arithmetic in fp32, one
+ * rounding to the 16-bit type.
+ *   k, v        device [n_tokens, kv_heads, head_dim], token stride kv_token_stride bytes
+ *   q, q_out    NULL, or device [n_tokens, q_heads, head_dim] with token strides
+ *               q_token_stride and q_out_token_stride (may be the same memory)
+ *   q_norm, k_norm  NULL or device [head_dim] weights of the cache's type
+ *   cos_sin     NULL or device fp32 [n_positions, rot_dim]: rot_dim/2 cosines,
+ *               then rot_dim/2 sines, of each position
+ *   rot_dim     rotated channels of a head, a multiple of 16: channels i and
+ *               i + rot_dim/2 are a pair, or 2i and 2i + 1 (adjacent_pairs != 0)
+ * A token whose position lies outside the cache or the table sets IBP_ERANGE;
+ * its keys and values are not written, its queries are zero.  Errors:
+ * IBP_EINVAL, IBP_EALIGN (16 bytes), IBP_ECUDA. */
+IBP_API ibp_status ibp_paged_append(const ibp_paged* cache, const ibp_paged_batch* batch,
+                                    const void* k, const void* v, uint64_t kv_token_stride,
+                                    const void* q, uint64_t q_token_stride, void* q_out,
+                                    uint64_t q_out_token_stride, uint32_t q_heads,
+                                    const void* q_norm, const void* k_norm, float eps,
+                                    const float* cos_sin, uint32_t n_positions, uint32_t rot_dim,
+                                    uint32_t adjacent_pairs, ibp_stream_t stream);
+
+/* Attention of the new tokens over the pages: for each row i at position p and
+ * each query head (q_heads / kv_heads of them share a K/V head),
+ *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j
+ * over the keys j <= p (causal != 0) or all kv_lens[s] keys (causal = 0), with
+ * window > 0 only those with j > p - window (causal only).  A row that sees no
+ * key is zero, with lse = -inf.  Keys and values that no row may see have no part
+ * in the result, whatever they hold.
+ *   q    device [n_tokens, q_heads, head_dim], token stride q_token_stride bytes
+ *   out  device [n_tokens, q_heads, head_dim], contiguous, of the cache's type
+ *   lse  NULL or device fp32 [n_tokens, q_heads]: log sum_j exp(scale * q_i . k_j)
+ *   selected  NULL, or device int32 [n_tokens, kv_heads, n_selected]: row i of
+ *        K/V head h sees only the keys of the pages selected[i][h][...] (numbers
+ *        of the sequence's pages, no page twice; negative entries and those
+ *        beyond the row's position are passed over).  Causal, without window.
+ *   workspace  device, IBP_PAGED_WORKSPACE_BYTES, 16-byte aligned
+ * Scores, softmax and sums in fp32, the weights rounded to the 16-bit type
+ * before they multiply the values.  Errors: IBP_EINVAL, IBP_EALIGN,
+ * IBP_ECUDA; a device wait that gave up sets IBP_ETIMEOUT. */
+IBP_API ibp_status ibp_paged_attention(const ibp_paged* cache, const ibp_paged_batch* batch,
+                                       const void* q, uint64_t q_token_stride, uint32_t q_heads,
+                                       void* out, float* lse, float scale, uint32_t causal,
+                                       uint32_t window, const int32_t* selected,
+                                       uint32_t n_selected, void* workspace,
+                                       uint64_t workspace_bytes, ibp_stream_t stream);
+
+/* Bounds of the pages that the batch's new tokens went into, over all tokens
+ * they hold now: bounds [n_pages, kv_heads, 2, head_dim], contiguous, of the
+ * cache's type, 16-byte aligned; [..][0][d] the smallest and [..][1][d] the
+ * largest key of channel d (NaN if a key is NaN).  Other pages' bounds keep
+ * their values.  Errors: IBP_EINVAL, IBP_EALIGN, IBP_ECUDA. */
+IBP_API ibp_status ibp_paged_bounds(const ibp_paged* cache, const ibp_paged_batch* batch,
+                                    void* bounds, ibp_stream_t stream);
+
+/* Scores of the pages for each new token and K/V head: an upper bound of the
+ * products of any of the head's queries with any of the page's keys,
+ *   scores[i][h][c] = max_g sum_d max(q_d lo_d, q_d hi_d)
+ * over the q_heads / kv_heads queries g of K/V head h and the bounds of page c
+ * of the sequence, -inf for pages that begin beyond the token's position (and
+ * for a page id out of range).
+ *   q       as for ibp_paged_attention
+ *   scores  device fp32 [n_tokens, kv_heads, max_pages]
+ * Errors: IBP_EINVAL, IBP_EALIGN, IBP_ECUDA. */
+IBP_API ibp_status ibp_paged_scores(const ibp_paged* cache, const ibp_paged_batch* batch,
+                                    const void* q, uint64_t q_token_stride, uint32_t q_heads,
+                                    const void* bounds, float* scores, ibp_stream_t stream);
+
+/* The n_selected pages of largest score of each new token and K/V head: the
+ * page of the token's own position always, then by score, equal scores by the
+ * smaller number, NaN before all; in ascending order, -1 behind the last where
+ * fewer pages begin at or before the token's position.
+ *   scores    device fp32 [n_tokens, kv_heads, max_pages]
+ *   selected  device int32 [n_tokens, kv_heads, n_selected]
+ * Errors: IBP_EINVAL (n_selected 0 or above IBP_PAGED_MAX_SELECTED), IBP_EALIGN, IBP_ECUDA. */
+IBP_API ibp_status ibp_paged_select(const ibp_paged* cache, const ibp_paged_batch* batch,
+                                    const float* scores, uint32_t n_selected, int32_t* selected,
+                                    ibp_stream_t stream);
+
 /* Copy the store's Mask and Bitval (R/4 words each) to host arrays.  Synchronous. */
 IBP_API ibp_status ibp_meta_get(const ibp_store* store, uint32_t* mask_host, uint32_t* bitval_host);
 

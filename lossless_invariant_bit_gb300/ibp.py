@@ -36,10 +36,28 @@ class ibp_store_info(ctypes.Structure):
                 ("meta_valid", ctypes.c_uint32), ("max_runs", ctypes.c_uint32)]
 
 
+class ibp_paged_desc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("page_stride", ctypes.c_uint64), ("head_stride", ctypes.c_uint64),
+                ("token_stride", ctypes.c_uint64), ("n_pages", ctypes.c_uint32),
+                ("page_tokens", ctypes.c_uint32), ("kv_heads", ctypes.c_uint32),
+                ("head_dim", ctypes.c_uint32), ("dtype", ctypes.c_uint32)]
+
+
+class ibp_paged_batch(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("q_starts", ctypes.c_void_p), ("table_stride", ctypes.c_uint64),
+                ("n_seqs", ctypes.c_uint32), ("max_pages", ctypes.c_uint32),
+                ("n_tokens", ctypes.c_uint32), ("max_q_tokens", ctypes.c_uint32)]
+
+
+PAGED_WORKSPACE_BYTES = 96 << 20  # IBP_PAGED_WORKSPACE_BYTES of include/ibp.h
+
 _lib = None
 _P = ctypes.c_void_p
 _U32 = ctypes.c_uint32
 _U64 = ctypes.c_uint64
+_F32 = ctypes.c_float
 _ST = ctypes.c_int
 
 _SIGS = {
@@ -74,6 +92,16 @@ _SIGS = {
     "ibp_gather_copy_dma": [_P, _P, _U64, _U32, _P, _U64, _U64, _P],
     "ibp_gather_copy_staged": [_P, _P, _U64, _U32, _P, _U64, _U64, _P, _P],
     "ibp_project_compress": [_P, _P, _U64, _U64, _P, _P, _U32, _P, _P, _P, _P, _P, _U64, _P],
+    "ibp_paged_create": [ctypes.POINTER(ctypes.c_void_p), _P],
+    "ibp_paged_destroy": [_P],
+    "ibp_paged_status": [_P, _P, ctypes.POINTER(ctypes.c_int), ctypes.c_int],
+    "ibp_paged_append": [_P, _P, _P, _P, _U64, _P, _U64, _P, _U64, _U32, _P, _P, _F32, _P, _U32,
+                         _U32, _U32, _P],
+    "ibp_paged_attention": [_P, _P, _P, _U64, _U32, _P, _P, _F32, _U32, _U32, _P, _U32, _P, _U64,
+                            _P],
+    "ibp_paged_bounds": [_P, _P, _P, _P],
+    "ibp_paged_scores": [_P, _P, _P, _U64, _U32, _P, _P, _P],
+    "ibp_paged_select": [_P, _P, _P, _U32, _P, _P],
 }
 
 
@@ -358,6 +386,65 @@ def ibp_gather_copy_staged(dst, src, slot_bytes: int, row_bytes: int, ids_host, 
     _check(_lib_handle().ibp_gather_copy_staged(_ptr(dst), _ptr(src), slot_bytes, row_bytes,
                                                 _ptr(ids_host), n, n_rows, _ptr(staging_host),
                                                 _stream(stream)), "ibp_gather_copy_staged")
+
+
+def ibp_paged_create(desc: "ibp_paged_desc") -> int:
+    h = ctypes.c_void_p()
+    _check(_lib_handle().ibp_paged_create(ctypes.byref(h), ctypes.addressof(desc)),
+           "ibp_paged_create")
+    return h.value
+
+
+def ibp_paged_destroy(cache: int) -> None:
+    _check(_lib_handle().ibp_paged_destroy(cache), "ibp_paged_destroy")
+
+
+def ibp_paged_status(cache: int, stream=None, reset: bool = False) -> int:
+    out = ctypes.c_int(0)
+    _check(_lib_handle().ibp_paged_status(cache, _stream(stream), ctypes.byref(out),
+                                          int(bool(reset))), "ibp_paged_status")
+    return out.value
+
+
+def ibp_paged_append(cache: int, batch: "ibp_paged_batch", k, v, kv_token_stride: int, q,
+                     q_token_stride: int, q_out, q_out_token_stride: int, q_heads: int, q_norm,
+                     k_norm, eps: float, cos_sin, n_positions: int, rot_dim: int,
+                     adjacent_pairs: bool, stream=None) -> None:
+    _check(_lib_handle().ibp_paged_append(cache, ctypes.addressof(batch), _ptr(k), _ptr(v),
+                                          kv_token_stride, _ptr(q), q_token_stride, _ptr(q_out),
+                                          q_out_token_stride, q_heads, _ptr(q_norm), _ptr(k_norm),
+                                          eps, _ptr(cos_sin), n_positions, rot_dim,
+                                          int(bool(adjacent_pairs)), _stream(stream)),
+           "ibp_paged_append")
+
+
+def ibp_paged_attention(cache: int, batch: "ibp_paged_batch", q, q_token_stride: int,
+                        q_heads: int, out, lse, scale: float, causal: bool, window: int, selected,
+                        n_selected: int, workspace, workspace_bytes: int, stream=None) -> None:
+    _check(_lib_handle().ibp_paged_attention(cache, ctypes.addressof(batch), _ptr(q),
+                                             q_token_stride, q_heads, _ptr(out), _ptr(lse), scale,
+                                             int(bool(causal)), window, _ptr(selected),
+                                             n_selected, _ptr(workspace), workspace_bytes,
+                                             _stream(stream)), "ibp_paged_attention")
+
+
+def ibp_paged_bounds(cache: int, batch: "ibp_paged_batch", bounds, stream=None) -> None:
+    _check(_lib_handle().ibp_paged_bounds(cache, ctypes.addressof(batch), _ptr(bounds),
+                                          _stream(stream)), "ibp_paged_bounds")
+
+
+def ibp_paged_scores(cache: int, batch: "ibp_paged_batch", q, q_token_stride: int, q_heads: int,
+                     bounds, scores, stream=None) -> None:
+    _check(_lib_handle().ibp_paged_scores(cache, ctypes.addressof(batch), _ptr(q), q_token_stride,
+                                          q_heads, _ptr(bounds), _ptr(scores), _stream(stream)),
+           "ibp_paged_scores")
+
+
+def ibp_paged_select(cache: int, batch: "ibp_paged_batch", scores, n_selected: int, selected,
+                     stream=None) -> None:
+    _check(_lib_handle().ibp_paged_select(cache, ctypes.addressof(batch), _ptr(scores),
+                                          n_selected, _ptr(selected), _stream(stream)),
+           "ibp_paged_select")
 
 
 def ibp_status_str(status: int) -> str:
