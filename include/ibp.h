@@ -497,11 +497,13 @@ typedef struct {
 #define IBP_PAGED_WORKSPACE_BYTES (96ull << 20)
 
 /* Create a handle on a cache (the descriptor is copied, the pages stay the
- * caller's).  Allocates a status word on the current device.  Errors:
- * IBP_EINVAL (geometry), IBP_EALIGN, IBP_ENOMEM, IBP_ECUDA. */
+ * caller's) on the current device; its status word is one of 4096 that the
+ * library holds there from the first handle on.  Errors: IBP_EINVAL (geometry),
+ * IBP_EALIGN, IBP_ENOMEM, IBP_ECUDA. */
 IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc);
 
-/* Free a handle (synchronises the device; the pages are not touched).  NULL is a no-op. */
+/* Free a handle, once the work of its calls is done (the pages are not touched;
+ * work still in flight would report into a later handle's status word).  NULL is a no-op. */
 IBP_API ibp_status ibp_paged_destroy(ibp_paged* cache);
 
 /* As ibp_stream_status, for a paged cache's status word. */

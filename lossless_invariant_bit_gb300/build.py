@@ -20,7 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libibp.so")
 SOURCES = ["ibp_kernels.cu", "ibp_api.cu", "ibp_noalloc.cu", "ibp_transfer.cu", "ibp_project.cu",
-           "ibp_launch.cu", "ibp_paged.cu", "ibp_paged_step.cu", "ibp_paged_api.cu"]
+           "ibp_launch.cu", "ibp_paged.cu", "ibp_paged_step.cu",
+           "ibp_paged_chunk.cu", "ibp_paged_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

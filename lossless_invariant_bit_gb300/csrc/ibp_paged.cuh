@@ -41,7 +41,7 @@ struct PagedAttnArgs {
   uint32_t causal, window, G;
   const int32_t* selected;  // NULL or [n_tokens, H, n_sel]
   uint32_t n_sel;
-  uint32_t max_rows;        // the step kernel takes sequences with at most so many rows
+  uint32_t max_rows;        // rows of a sequence: the step kernel's most, one less than the chunk kernel's least
   uint8_t* ws;
 };
 
@@ -69,15 +69,16 @@ cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, con
                                 float* scores, int sm_count, cudaStream_t st);
 cudaError_t launch_paged_select(const PagedGeom& g, const PagedBatchView& b, const float* scores,
                                 uint32_t n_sel, int32_t* selected, cudaStream_t st);
-// Sequences with at most kStepRows rows (new tokens x query heads of a K/V
-// head), or with a page list per token.
+// Sequences with at most a.max_rows rows (new tokens x query heads of a K/V
+// head), or tokens with a page list each.
 constexpr uint32_t kStepRows = 16;
 cudaError_t launch_paged_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
                               cudaStream_t st);
 // Tokens of a page in one box of the maps of the step and the chunk kernel.
 constexpr uint32_t kStepBox = 32, kChunkBox = 128;
-cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const PagedMaps& m, uint32_t min_rows,
-                               int sm_count, cudaStream_t st);
+// Sequences with more than a.max_rows rows.
+cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
+                               cudaStream_t st);
 
 #ifdef __CUDACC__
 

@@ -1,13 +1,58 @@
 // C-ABI of the paged K/V cache: handles, argument checks, launches.
 #include <cmath>
-#include <cstdlib>
+#include <mutex>
 #include <new>
 
 #include "ibp_internal.cuh"
 #include "ibp_paged.cuh"
 #include "ibp_tma.cuh"
 
+// Status words of the handles of a device: one block per device, kept until the
+// process exits, so that a handle costs no device allocation (and freeing one no
+// synchronisation).
+namespace {
+
+constexpr int kDevices = 64, kWords = 4096;
+
+struct StatusPool {
+  uint32_t* words = nullptr;  // 32 bytes apart
+  bool used[kWords] = {};
+  int next = 0;
+};
+
+std::mutex g_pool_mu;
+StatusPool g_pool[kDevices];
+
+// A word that no handle uses, not yet cleared; -1: none left (or no memory).
+int take_status(int device, uint32_t** word) {
+  if (device < 0 || device >= kDevices) return -1;
+  std::lock_guard<std::mutex> lock(g_pool_mu);
+  StatusPool& p = g_pool[device];
+  if (!p.words && cudaMalloc(reinterpret_cast<void**>(&p.words), 32u * kWords) != cudaSuccess) {
+    cudaGetLastError();
+    p.words = nullptr;
+    return -1;
+  }
+  for (int i = 0; i < kWords; ++i) {
+    const int at = (p.next + i) % kWords;
+    if (p.used[at]) continue;
+    p.used[at] = true;
+    p.next = at + 1;
+    *word = p.words + 8 * at;
+    return at;
+  }
+  return -1;
+}
+
+void give_status(int device, int at) {
+  std::lock_guard<std::mutex> lock(g_pool_mu);
+  g_pool[device].used[at] = false;
+}
+
+}  // namespace
+
 struct ibp_paged {
+  int status_at;
   ibp::PagedGeom g;
   int device, sm_count;
   ibp::PagedMaps step, chunk;
@@ -109,13 +154,14 @@ ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
     delete c;
     return IBP_ECUDA;
   }
-  if (cudaMalloc(reinterpret_cast<void**>(&c->g.status), 256) != cudaSuccess) {
-    cudaGetLastError();
+  c->status_at = take_status(c->device, &c->g.status);
+  if (c->status_at < 0) {
     delete c;
     return IBP_ENOMEM;
   }
-  if (cudaMemset(c->g.status, 0, 256) != cudaSuccess) {
-    cudaFree(c->g.status);
+  if (cudaMemset(c->g.status, 0, 4) != cudaSuccess ||
+      cudaStreamSynchronize(nullptr) != cudaSuccess) {
+    give_status(c->device, c->status_at);
     delete c;
     return IBP_ECUDA;
   }
@@ -125,9 +171,9 @@ ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
 
 ibp_status ibp_paged_destroy(ibp_paged* c) {
   if (!c) return IBP_OK;
-  const cudaError_t e = cudaFree(c->g.status);
+  give_status(c->device, c->status_at);
   delete c;
-  return cu(e);
+  return IBP_OK;
 }
 
 ibp_status ibp_paged_status(const ibp_paged* c, ibp_stream_t stream, ibp_status* out, int reset) {
@@ -214,10 +260,19 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
   a.G = q_heads / c->g.H;
   a.selected = selected;
   a.n_sel = n_selected;
-  a.max_rows = 0xFFFFFFFFu;
   a.ws = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return cu(ibp::launch_paged_step(a, c->step, c->sm_count, st));
+  // Lists of pages, and sequences with one tile of 16 rows at most, go to the step
+  // kernel, the others to the chunk kernel; a batch may need both.
+  const bool few = selected || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
+  if (few || b->n_seqs > 1u) {
+    a.max_rows = ibp::kStepRows;
+    const cudaError_t ce = ibp::launch_paged_step(a, c->step, c->sm_count, st);
+    if (ce != cudaSuccess || few) return cu(ce);
+  } else {
+    a.max_rows = 0;
+  }
+  return cu(ibp::launch_paged_chunk(a, c->chunk, c->sm_count, st));
 }
 
 ibp_status ibp_paged_bounds(const ibp_paged* c, const ibp_paged_batch* b, void* bounds,
