@@ -12,12 +12,18 @@
 // query r % G of token r / G, so the queries that share K/V fill a tile however
 // few tokens a chunk has.  Two slots of 128 rows alternate: while the tensor
 // cores work for one, four warps take the other's exponentials.
-//   warp 0        TMA: keys and values of a block, a box per page, into a ring of 5 tiles
-//   warp 1        one thread issues tcgen05.mma: S = Q K^T (both from shared
-//                 memory) into 128 columns of tensor memory per slot, O += P V with P
-//                 from tensor memory, over S's columns, and V as the transposed operand
-//   warps 4 - 7   slot 0, warps 8 - 11 slot 1 (thread = row): queries into shared memory,
-//                 then per block S -> registers, mask, maximum, exponentials, P
+//   warps 0 - 3   slot 0, warps 4 - 7 slot 1 (thread = row): queries into shared memory,
+//                 then per block S -> registers, mask, exponentials, maximum, P in two
+//                 halves, so that P V begins while the second half is computed
+//   warp 8        walks the tiles and tells the others of each through shared
+//                 memory; TMA: keys and values of a block, a box per page, into a ring of
+//                 5 tiles
+//   warps 9, 10   issue tcgen05.mma, one for each slot, so that the tensor cores have the
+//                 other slot's products while one waits: S = Q K^T (both from shared
+//                 memory) into 128 columns of tensor memory, O += P V with P from tensor
+//                 memory, over S's columns, and V as the transposed operand
+//   warp 11       waits for keys and values in the issuing warp's place, and says so
+//                 with the weights' barrier: one wait less between two products
 // A tile of at most 128 rows gives both slots the same rows, slot 0 the even
 // blocks of keys and slot 1 the odd ones, and joins them at its end.
 //
@@ -37,7 +43,7 @@ constexpr uint64_t kWsBytes = IBP_PAGED_WORKSPACE_BYTES - kStepWsBytes;
 template <int kDP>
 struct Piece {
   float m[kTileRows], l[kTileRows];
-  float o[kTileRows][kDP];
+  float o[kDP][kTileRows];
 };
 
 struct Join {
@@ -134,6 +140,24 @@ struct Walk {
   bool fresh;
 };
 
+// What the other warps are told of a run of blocks; count 0: there is no more.  A
+// ring of 8: the walking warp is at most 3 tiles ahead, since each takes two of the
+// 5 places for keys and values and a tile's queries wait for the tile before.
+struct Info {
+  uint32_t count, two;    // blocks; the slots take alternate ones
+  uint32_t q0, head;
+  uint32_t row0, rows;
+  uint32_t n, L;
+  uint32_t lo, hi, key0;  // keys that any row sees, first key of the run
+  uint32_t whole;         // the run is the whole tile: write the result, not a piece
+  uint32_t place;         // which of the CTA's two pieces
+  uint32_t pad[3];
+};
+constexpr uint32_t kInfos = 8;
+// Keys whose weights are computed before the first half of them is handed over: what
+// waits for the first half's store is then hidden (64 to 112 measured alike).
+constexpr int kEarly = 80;
+
 __device__ __forceinline__ bool walk(const PagedAttnArgs& a, Walk& w) {
   if (w.u >= w.u1) return false;
   if (!w.fresh) {
@@ -159,36 +183,51 @@ __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map,
       : "memory");
 }
 
-// Descriptor of V as the transposed right operand: rows of 64 channels
-// (128 bytes, swizzled) for each key; 8 keys to an atom of 1024 bytes, the next 64
-// channels a half tile further.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr, uint32_t half_bytes) {
-  uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(half_bytes >> 4) << 16;  // leading: 64 channels on
-  d |= (uint64_t)(1024u >> 4) << 32;       // stride: 8 keys on
-  d |= (uint64_t)1u << 46;
-  d |= (uint64_t)2u << 61;
-  return d;
-}
+// The matrix instructions of a block, issued by the lane with `on` set while the
+// whole warp walks the same path (descriptors stay uniform values), as one run
+// of code: what lies between two of them counts, each works for 64 cycles only.
+#define IBP_MMA_SS(inc)                                                         \
+  " add.s64 a, a, " inc ";\n add.s64 b, b, " inc ";\n"                          \
+  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
+#define IBP_MMA_TS(col)                                                         \
+  " add.s64 b, b, 128;\n add.u32 c, %1, " col ";\n"                             \
+  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [c], b, %4, p;\n"
 
-// The matrix instructions, issued by the lane with `on` set: the whole warp walks
-// the same path, so that descriptors are uniform values.
-__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t tmem, uint64_t adesc,
-                                       uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// S = Q K^T over 64 channels: low descriptor words of both, their common high word;
+// accumulates from the start when `acc` is set.
+__device__ __forceinline__ void mma_qk(uint32_t on, uint32_t tmem, uint32_t qlo, uint32_t klo,
+                                       uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      "{\n .reg .pred p, q, e;\n .reg .b64 a, b;\n setp.ne.b32 e, %5, 0;\n"
+      " setp.ne.b32 q, %6, 0;\n setp.eq.b32 p, 0, 0;\n"
+      " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n" IBP_MMA_SS("2")
+          IBP_MMA_SS("2") IBP_MMA_SS("2") "}\n" ::"r"(tmem),
+      "r"(qlo), "r"(klo), "r"(hi), "r"(idesc), "r"(on), "r"(acc)
       : "memory");
 }
 
-// A from tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t tmem, uint32_t a, uint64_t bdesc,
-                                       uint32_t idesc, uint32_t accumulate) {
+// One step of it, for the head sizes between.
+__device__ __forceinline__ void mma_qk_step(uint32_t on, uint32_t tmem, uint32_t qlo,
+                                            uint32_t klo, uint32_t hi, uint32_t idesc,
+                                            uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 e, %5, 0;\n"
+      " setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(tmem),
+      "r"(qlo), "r"(klo), "r"(hi), "r"(idesc), "r"(on), "r"(acc)
+      : "memory");
+}
+
+// O (+)= P V over 64 keys, P in tensor memory; accumulates from the start when `acc` is set.
+__device__ __forceinline__ void mma_pv(uint32_t on, uint32_t tmem, uint32_t p, uint32_t vlo,
+                                       uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, q, e;\n .reg .b64 b;\n .reg .b32 c;\n setp.ne.b32 e, %5, 0;\n"
+      " setp.ne.b32 q, %6, 0;\n setp.eq.b32 p, 0, 0;\n mov.b64 b, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, q;\n" IBP_MMA_TS("8")
+          IBP_MMA_TS("16") IBP_MMA_TS("24") "}\n" ::"r"(tmem),
+      "r"(p), "r"(vlo), "r"(hi), "r"(idesc), "r"(on), "r"(acc)
       : "memory");
 }
 
@@ -262,6 +301,37 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The registers of the launch, shared out again: 8 warps of 208 and 4 of 88 are
+// the 12 of 168 that the launch came with.
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+static_assert(8 * 208 + 4 * 88 <= 12 * 168, "no more registers than the launch has");
+
+// Two fp32 values at a time.
+__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Whether both slots (256 threads) say so; every tile has one such vote, so that
 // neither waits for the other once one has given up.
 __device__ __forceinline__ bool both_slots(bool mine) {
@@ -275,11 +345,21 @@ __device__ __forceinline__ bool both_slots(bool mine) {
   return all != 0u;
 }
 
-// A wait of a whole warp that also gives up once another role has.
+// A wait of a whole warp.  One that has run out (about two seconds) sets *fail;
+// the waits that run after it give up at once if what they wait for is not there.
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, uint32_t* fail) {
-  const bool there = !*reinterpret_cast<volatile uint32_t*>(fail) && mbar_wait(bar, parity);
-  if (!there) atomicExch(fail, 1u);
-  return __all_sync(0xFFFFFFFFu, there);
+  const uint32_t at = smem_addr(bar);
+  if (__all_sync(0xFFFFFFFFu, mbar_try(at, parity))) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try(at, parity))) return true;
+    const bool late = global_ns() - t0 > 2000000000ull ||
+                      *reinterpret_cast<volatile uint32_t*>(fail) != 0u;
+    if (__any_sync(0xFFFFFFFFu, late)) {
+      atomicExch(fail, 1u);
+      return false;
+    }
+  }
 }
 
 template <int kDP, bool kBf16>
@@ -295,12 +375,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + (2u + kRing) * S::kTile);
   uint64_t* empty = full + kRing;
   uint64_t* s_full = empty + kRing;  // per slot: scores are there
-  uint64_t* p_full = s_full + 2;     // per slot: weights are there
-  uint64_t* q_full = p_full + 2;     // the tile's queries are there
+  uint64_t* p_full = s_full + 2;     // per slot: half the weights (values, the next keys) are there
+  uint64_t* p2_full = p_full + 2;    // per slot: the other half
+  uint64_t* turn = p2_full + 2;      // per slot: the other has issued its products
+  uint64_t* q_full = turn + 2;       // the tile's queries are there
   uint64_t* o_full = q_full + 1;     // every product of the tile is done
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(o_full + 1);
+  uint64_t* done = o_full + 1;       // per slot, after a failure: its products are done
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 2);
   uint32_t* s_fail = s_tmem + 1;
   uint32_t* s_bad = s_fail + 1;      // 8 blocks: bit per page with an id out of range
+  __shared__ Info s_info[kInfos];
+  __shared__ uint64_t info_full[kInfos];
   __shared__ uint64_t s_scan[kThreads / 32];
   __shared__ uint64_t s_found[3];
 
@@ -313,19 +398,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
     for (uint32_t i = 0; i < kRing; ++i) {
       mbar_init(full + i, 1);
-      mbar_init(empty + i, 1);
+      mbar_init(empty + i, 2);
     }
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 128);
+      mbar_init(p_full + i, 5);
+      mbar_init(p2_full + i, 4);
+      mbar_init(turn + i, 1);
+      mbar_init(done + i, 1);
     }
-    mbar_init(q_full, 256);
-    mbar_init(o_full, 1);
+    for (uint32_t i = 0; i < kInfos; ++i) mbar_init(info_full + i, 1);
+    mbar_init(q_full, 8);
+    mbar_init(o_full, 2);
     *s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 1) {
+  if (tid == 0) mbar_arrive(turn);  // slot 0 begins
+  if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(s_tmem)),
                  "r"(512u)
@@ -398,16 +488,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     w0.u = u0;
     w0.fresh = true;
   }
-  Join join{};
+  // the tile of number t, once its run is known; false: no more, or given up
+  auto info_of = [&](uint32_t t) -> const Info* {
+    const Info* x = s_info + t % kInfos;
+    if (!wait_or_fail(info_full + t % kInfos, (t / kInfos) & 1u, s_fail)) return nullptr;
+    return x->count ? x : nullptr;
+  };
 
-  if (warp == 0) {
-    // ---------------- producer: lane i loads page i of the block
+  if (warp == 8) {
+    reg_dec();
+    // ---------------- the walk, and loads: lane i loads page i of the block
     const uint32_t lg = a.g.page_lg, box_lg = lg < 7u ? lg : 7u;
     const uint32_t npg = kKeys >> box_lg;
-    uint32_t e = 0, blocks = 0;  // ring entries filled, blocks begun
+    uint32_t e = 0, blocks = 0, tiles = 0;  // ring entries filled, blocks and tiles begun
     bool go = true;
     Walk w = w0;
-    while (go && walk(a, w)) {
+    Join join{};
+    while (go) {
+      const bool more = walk(a, w);
+      if (lane == 0) {
+        Info* x = s_info + tiles % kInfos;
+        const uint64_t tile_u = w.u - w.count - w.blk;  // the tile's first block in the list
+        const bool whole = w.blk == 0 && w.count == w.t.nb;
+        x->count = more ? w.count : 0u;
+        x->two = w.t.two;
+        x->q0 = w.t.q0;
+        x->head = w.t.head;
+        x->row0 = w.t.row0;
+        x->rows = w.t.rows;
+        x->n = w.t.n;
+        x->L = w.t.L;
+        x->lo = w.t.lo;
+        x->hi = w.t.hi;
+        x->key0 = (w.t.b0 + w.blk) * kKeys;
+        x->whole = whole;
+        x->place = tile_u >= u0 ? 1u : 0u;
+        mbar_arrive(info_full + tiles % kInfos);
+        if (more && w.blk + w.count == w.t.nb && !whole) {
+          uint64_t f = tile_u * ctas / total;
+          while (f + 1 < ctas && total * (f + 1) / ctas <= tile_u) ++f;
+          while (f > 0 && total * f / ctas > tile_u) --f;
+          join.first = (uint32_t)f;
+          join.count = blockIdx.x - (uint32_t)f + 1u;
+          join.q0 = w.t.q0;
+          join.head = w.t.head;
+          join.row0 = w.t.row0;
+          join.rows = w.t.rows;
+        }
+      }
+      ++tiles;
+      __syncwarp();
+      if (!more) break;
       const int32_t* table = a.b.table + w.t.s * a.b.table_stride;
       auto page_at = [&](uint32_t b) {
         const uint32_t key = (w.t.b0 + b) * kKeys + (lane << box_lg);
@@ -443,90 +574,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    if (lane == 0) joins[blockIdx.x] = join;
     // after a failure: the copies in flight land (or their waits give up too)
     if (!go)
       for (uint32_t i = e > kRing ? e - kRing : 0u; i < e; ++i)
         mbar_wait(full + i % kRing, (i / kRing) & 1u);
-  } else if (warp == 1) {
-    // ---------------- matrix products
-    const uint32_t on = lane == 0 ? 1u : 0u;
+  } else if (warp == 9 || warp == 10) {
+    reg_dec();
+    // ---------------- a slot's matrix products
+    const uint32_t on = lane == 0 ? 1u : 0u, slot = warp - 9u;
     {
       const uint32_t base_desc = (1u << 4) | ((uint32_t)kBf16 << 7) | ((uint32_t)kBf16 << 10) |
                                  ((kRows >> 4) << 24);
       const uint32_t qk_desc = base_desc | ((kKeys >> 3) << 17);
       const uint32_t pv_desc = base_desc | ((a.g.D >> 3) << 17) | (1u << 16);
-      uint32_t e0 = 0, tiles = 0, pn[2] = {0, 0};
+      // Descriptors of 128-byte swizzled tiles.  Queries and keys: rows along the
+      // reduction, 8 to an atom of 1024 bytes.  Values, as the transposed operand: rows of
+      // 64 channels for each key, 8 keys to an atom, the next 64 channels half a tile on.
+      const uint32_t desc_hi = (uint32_t)(sw128_desc(0) >> 32);
+      const uint32_t q_lo = (uint32_t)sw128_desc(smem_addr(s_q));
+      const uint32_t kv_lo = (uint32_t)sw128_desc(smem_addr(s_kv));
+      const uint32_t v_lead = ((S::kHalf >> 4) << 16) - (1u << 16);
+      const uint32_t k_steps = a.g.D / 16u;
+      const uint32_t ts = tmem + slot * 128u, to = tmem + 256u + slot * 128u;
+      uint32_t e0 = 0, tiles = 0, pn = 0, tn = 0;
       bool go = true;
-      Walk w = w0;
-      auto k_entry = [&](uint32_t i) { return e0 + 2u * i; };
-      auto wait_entry = [&](uint32_t e) {
-        go = go && wait_or_fail(full + e % kRing, (e / kRing) & 1u, s_fail);
-        tc_after();
-      };
-      auto qk = [&](uint32_t slot, uint32_t qslot, uint32_t e) {
-        const uint32_t qa = smem_addr(s_q + qslot * S::kTile);
-        const uint32_t ka = smem_addr(s_kv + (e % kRing) * S::kTile);
-#pragma unroll
-        for (uint32_t k = 0; k < kDP / 16u; ++k) {
-          if (16u * k >= a.g.D) break;
-          const uint32_t off = (k >> 2) * S::kHalf + 32u * (k & 3u);
-          mma_ss(on, tmem + slot * 128u, sw128_desc(qa + off), sw128_desc(ka + off), qk_desc,
-                  k != 0u ? 1u : 0u);
+      // S = Q K^T; the other slot's turn begins with the last of it, since a turn takes
+      // as long to pass on as two products to run
+      auto qk = [&](uint32_t qslot, uint32_t e, bool pass) {
+        const uint32_t qa = q_lo + qslot * (S::kTile >> 4);
+        const uint32_t ka = kv_lo + (e % kRing) * (S::kTile >> 4);
+        if (k_steps == kDP / 16u) {
+          if (kDP == 128) mma_qk(on, ts, qa, ka, desc_hi, qk_desc, 0u);
+          if (pass && lane == 0) mbar_arrive(turn + (slot ^ 1u));
+          __syncwarp();
+          constexpr uint32_t kOff = kDP == 128 ? S::kHalf >> 4 : 0u;
+          mma_qk(on, ts, qa + kOff, ka + kOff, desc_hi, qk_desc, kDP == 128 ? 1u : 0u);
+        } else {
+          for (uint32_t k = 0; k < k_steps; ++k) {
+            const uint32_t off = (k >> 2) * (S::kHalf >> 4) + 2u * (k & 3u);
+            mma_qk_step(on, ts, qa + off, ka + off, desc_hi, qk_desc, k ? 1u : 0u);
+          }
+          if (pass && lane == 0) mbar_arrive(turn + (slot ^ 1u));
+          __syncwarp();
         }
         commit(on, s_full + slot);
       };
-      auto pv = [&](uint32_t slot, uint32_t e, bool first) {
-        go = go && wait_or_fail(p_full + slot, pn[slot]++ & 1u, s_fail);
-        tc_after();
-        if (!go) return;
-        const uint32_t va = smem_addr(s_kv + (e % kRing) * S::kTile);
-#pragma unroll
-        for (uint32_t k = 0; k < kKeys / 16u; ++k)
-          mma_ts(on, tmem + 256u + slot * 128u, tmem + slot * 128u + 8u * k,
-                     v_desc(va + 2048u * k, S::kHalf), pv_desc, first && k == 0u ? 0u : 1u);
-      };
-      while (go && walk(a, w)) {
+      while (go) {
+        const Info* x = info_of(tiles);
+        if (!x) break;
+        const uint32_t nb = x->count;
+        const bool two = x->two != 0u;
+        const uint32_t step = two ? 2u : 1u, qslot = two ? 0u : slot;
         go = wait_or_fail(q_full, tiles & 1u, s_fail);
         tc_after();
-        if (!go) break;
-        const uint32_t nb = w.count;
-        if (!w.t.two) {
-          wait_entry(k_entry(0));
+        uint32_t i = two ? slot : 0u;
+        if (go && i < nb) {
+          const uint32_t ek = e0 + 2u * i;
+          go = wait_or_fail(full + ek % kRing, (ek / kRing) & 1u, s_fail);
+          tc_after();
+          if (go) qk(qslot, ek, false);
+        }
+        // The slots take turns, so that one's products run while the other's weights are
+        // computed (left alone they fall into step, and both wait for both).
+        for (uint32_t b = 0; b < nb && go; b += step, i += step) {
+          const uint32_t ev = e0 + 2u * i + 1u, ek = e0 + 2u * (i + step);
+          const uint32_t va = kv_lo + v_lead + (ev % kRing) * (S::kTile >> 4);
+          // the weights, and with them these values and the next keys
+          const uint32_t parity = pn & 1u;
+          go = wait_or_fail(turn + slot, tn++ & 1u, s_fail);
+          if (i < nb) go = go && wait_or_fail(p_full + slot, parity, s_fail);
+          tc_after();
           if (!go) break;
-          qk(0, 0, k_entry(0));
-          qk(1, 1, k_entry(0));
-          commit(on, empty + k_entry(0) % kRing);
-          for (uint32_t i = 0; i < nb && go; ++i) {
-            const uint32_t ev = k_entry(i) + 1u, ek = k_entry(i + 1u);
-            wait_entry(ev);
-            pv(0, ev, i == 0u);
-            if (i + 1u < nb && go) {
-              wait_entry(ek);
-              if (go) qk(0, 0, ek);
-            }
-            pv(1, ev, i == 0u);
-            commit(on, empty + ev % kRing);
-            if (i + 1u < nb && go) {
-              qk(1, 1, ek);
-              commit(on, empty + ek % kRing);
-            }
+          if (i < nb) {
+            mma_pv(on, to, ts, va, desc_hi, pv_desc, b ? 1u : 0u);
+            go = wait_or_fail(p2_full + slot, parity, s_fail);
+            tc_after();
+            if (!go) break;
+            mma_pv(on, to, ts + 32u, va + 512u, desc_hi, pv_desc, 1u);
+            ++pn;
           }
-        } else {
-          for (uint32_t i = 0; i < 2u && i < nb && go; ++i) {
-            wait_entry(k_entry(i));
-            if (go) qk(i, 0, k_entry(i));
-            commit(on, empty + k_entry(i) % kRing);
-          }
-          for (uint32_t i = 0; i < nb && go; ++i) {
-            const uint32_t slot = i & 1u, ev = k_entry(i) + 1u, ek = k_entry(i + 2u);
-            wait_entry(ev);
-            pv(slot, ev, i < 2u);
-            commit(on, empty + ev % kRing);
-            if (i + 2u < nb && go) {
-              wait_entry(ek);
-              if (go) qk(slot, 0, ek);
-              commit(on, empty + ek % kRing);
-            }
+          if (i + step < nb) {
+            qk(qslot, ek, true);
+          } else {
+            if (lane == 0) mbar_arrive(turn + (slot ^ 1u));
+            __syncwarp();
           }
         }
         commit(on, o_full);
@@ -534,53 +666,112 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++tiles;
       }
       if (!go) {  // products in flight finish before the tensor memory goes
-        commit(on, o_full);
-        mbar_wait(o_full, tiles & 1u);
+        commit(on, done + slot);
+        mbar_wait(done + slot, 0);
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp == 11) {
+    reg_dec();
+    // ---------------- keys and values are there: one arrival with each block's weights
+    uint32_t e0 = 0, tiles = 0, pn[2] = {0, 0};
+    bool go = true;
+    auto entry = [&](uint32_t e) {
+      go = go && wait_or_fail(full + e % kRing, (e / kRing) & 1u, s_fail);
+    };
+    while (go) {
+      const Info* t = info_of(tiles++);
+      if (!t) break;
+      const uint32_t nb = t->count, two = t->two, step = two ? 2u : 1u;
+      for (uint32_t i = 0; i < nb && go; ++i) {
+        entry(e0 + 2u * i + 1u);                         // these values
+        if (i + step < nb) entry(e0 + 2u * (i + step));  // the slot's next keys
+        if (!go) break;
+        const uint32_t s0 = two ? i & 1u : 0u, s1 = two ? s0 : 1u;
+        if (lane == 0)
+          for (uint32_t x = s0; x <= s1; ++x) mbar_arrive(p_full + x);
+        // the next arrival belongs to the next phase
+        for (uint32_t x = s0; x <= s1 && go; ++x)
+          go = wait_or_fail(p_full + x, pn[x]++ & 1u, s_fail);
+      }
+      e0 += 2u * nb;
+    }
+  } else {
+    reg_inc();
     // ---------------- a slot's rows: thread = row
-    const uint32_t slot = (warp - 4u) >> 2, wq = warp & 3u, r = wq * 32u + lane;
+    const uint32_t slot = warp >> 2, wq = warp & 3u, r = wq * 32u + lane;
     const uint32_t lane_base = (wq * 32u) << 16;
     const uint32_t ts = tmem + lane_base + slot * 128u, to = tmem + lane_base + 256u + slot * 128u;
     const float c = a.scale_log2;
+    const uint32_t box_lg = a.g.page_lg < 7u ? a.g.page_lg : 7u;
+    // This warp's 32 rows of the slot's queries in shared memory, 16 bytes at a
+    // time; between two tiles they hold the rows of the output.
+    constexpr uint32_t kCh = kDP / 8u, kPer = 32u / kCh, kLd = 32u / kPer;
+    uint8_t* s_rows = s_q + slot * S::kTile + wq * 32u * 128u;
+    const uint32_t my_ch = lane % kCh, my_sub = lane / kCh;
+    auto chunk_at = [&](uint32_t row, uint32_t ch) {
+      return s_rows + (ch >> 3) * S::kHalf + row * 128u + (((ch & 7u) ^ (row & 7u)) << 4);
+    };
+    // The tile's queries: lane i knows where row i lies, 16 (or 8) lanes fetch a row.
+    auto load_q = [&](const Info* t) {
+      const uint32_t n = t->two ? (slot ? 0u : t->rows)
+                                : (t->rows > slot * kRows ? t->rows - slot * kRows : 0u);
+      if (!t->two || slot == 0) {
+        const uint32_t R = t->row0 + slot * kRows + (r < n ? r : 0u), tok = R / a.G;
+        const uint64_t p = reinterpret_cast<uint64_t>(
+            a.q + (uint64_t)(t->q0 + tok) * a.q_stride +
+            (uint64_t)(t->head * a.G + (R - tok * a.G)) * a.g.D * 2u);
+#pragma unroll
+        for (uint32_t i = 0; i < kLd; ++i) {
+          const uint32_t row = i * kPer + my_sub;
+          const uint64_t src = __shfl_sync(0xFFFFFFFFu, p, row) + my_ch * 16u;
+          const bool there = wq * 32u + row < n && my_ch * 8u < a.g.D;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                           smem_addr(chunk_at(row, my_ch))),
+                       "l"(there ? src : p), "r"(there ? 16u : 0u)
+                       : "memory");
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    };
+    // this slot is done with an entry of the ring, or (twice) both are
+    auto release = [&](uint32_t e, bool twice) {
+      mbar_arrive(empty + e % kRing);
+      if (twice) mbar_arrive(empty + e % kRing);
+    };
     uint32_t sn = 0, tiles = 0, blocks = 0, e0 = 0;
     bool go = true;
-    Walk w = w0;
-    while (go && walk(a, w)) {
-      const uint64_t tile_u = w.u - w.count - w.blk;  // the tile's first block in the list
-      const bool two = w.t.two;
-      const uint32_t nrows = two ? w.t.rows : min(kRows, w.t.rows > slot * kRows ? w.t.rows - slot * kRows : 0u);
-      const uint32_t row0 = w.t.row0 + (two ? 0u : slot * kRows);
-      if (!two || slot == 0) {  // the slot's queries, 16 lanes a row
-        uint8_t* dst = s_q + slot * S::kTile;
-        constexpr uint32_t kCh = kDP / 8u;  // 16-byte chunks of a row
-#pragma unroll 4
-        for (uint32_t i = r; i < kRows * kCh; i += 128u) {
-          const uint32_t row = i / kCh, ch = i % kCh;
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (row < nrows && ch * 8u < a.g.D) {
-            const uint32_t R = row0 + row;
-            x = __ldg(reinterpret_cast<const uint4*>(
-                a.q + (uint64_t)(w.t.q0 + R / a.G) * a.q_stride +
-                ((uint64_t)w.t.head * a.G + R % a.G) * a.g.D * 2u + ch * 16u));
-          }
-          *reinterpret_cast<uint4*>(dst + (ch >> 3) * S::kHalf + row * 128u +
-                                    (((ch & 7u) ^ (row & 7u)) << 4)) = x;
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      }
-      mbar_arrive(q_full);
-      // this row's keys: [from, to)
+    while (go) {
+      const Info* t = info_of(tiles);
+      if (!t) break;
+      load_q(t);
+      const bool both = t->two != 0u;
+      const uint32_t count = t->count;
+      // this row, and its keys: [from, to)
+      const uint32_t nrows = both ? t->rows : min(kRows, t->rows > slot * kRows ? t->rows - slot * kRows : 0u);
       const bool live = r < nrows;
-      const int64_t pos = (int64_t)w.t.L - w.t.n + (row0 + (live ? r : 0u)) / a.G;
-      const uint32_t to_key = !live ? 0u : a.causal ? (uint32_t)(pos + 1 > 0 ? pos + 1 : 0) : w.t.L;
-      const uint32_t from_key =
-          a.window && pos + 1 > (int64_t)a.window ? (uint32_t)(pos + 1 - a.window) : 0u;
+      int32_t to_key, from_key;
+      uint64_t at;  // its place among [n_tokens, q_heads]
+      {
+        const uint32_t R = t->row0 + (both ? 0u : slot * kRows) + (live ? r : 0u);
+        const uint32_t tok = R / a.G;
+        at = ((uint64_t)(t->q0 + tok) * a.g.H + t->head) * a.G + (R - tok * a.G);
+        const int32_t pos = (int32_t)(t->L - t->n + tok);
+        to_key = !live ? 0 : a.causal ? max(pos + 1, 0) : (int32_t)t->L;
+        from_key = a.window && pos + 1 > (int32_t)a.window ? pos + 1 - (int32_t)a.window : 0;
+      }
+      int32_t key0 = (int32_t)t->key0;
+      const int32_t lo_key = (int32_t)t->lo, hi_key = (int32_t)t->hi;
+      // keys that every row of the warp sees need no mask
+      const int32_t all_to = __reduce_min_sync(0xFFFFFFFFu, live ? to_key : 0x7FFFFFFF);
+      const int32_t all_from = __reduce_max_sync(0xFFFFFFFFu, live ? from_key : 0);
       float m = -INFINITY, base = 0.f, l = 0.f;  // running maximum (scaled), reference, sum
       bool rowbad = false;
       bool any = false;  // a product has been accumulated
-      for (uint32_t i = two ? slot : 0u; i < w.count && go; i += two ? 2u : 1u) {
+      if (both) key0 += (int32_t)(slot * kKeys);
+      for (uint32_t i = both ? slot : 0u; i < count; i += both ? 2u : 1u) {
         go = wait_or_fail(s_full + slot, sn++ & 1u, s_fail);
         if (!go) break;
         tc_after();
@@ -589,16 +780,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32<32>(ts + 32u, sv);
         tmem_ld32<64>(ts + 64u, sv);
         tmem_ld32<96>(ts + 96u, sv);
-        const uint32_t key0 = (w.t.b0 + w.blk + i) * kKeys;
+        // these keys have been read, and with the product before them the values before
+        if (wq == 0 && lane == 0) {
+          release(e0 + 2u * i, both);
+          if (any) release(e0 + 2u * (i - (both ? 2u : 1u)) + 1u, both);
+        }
         const uint32_t badp = s_bad[(blocks + i) & 7u];
-        const bool edge = key0 + kKeys > w.t.hi || key0 < w.t.lo || badp;
-        if (edge && (two || slot == 0)) {
+        const bool edge = key0 + (int32_t)kKeys > hi_key || key0 < lo_key || badp;
+        if (edge) {
           // values that no row sees: zero, so that 0 * (what they hold) is 0
           const uint32_t ev = e0 + 2u * i + 1u;
           go = wait_or_fail(full + ev % kRing, (ev / kRing) & 1u, s_fail);
-          const uint32_t key = key0 + r;  // this thread's key
-          const uint32_t pg = r >> (a.g.page_lg < 7u ? a.g.page_lg : 7u);
-          if (go && (key >= w.t.hi || key < w.t.lo || (badp >> pg & 1u))) {
+          const int32_t key = key0 + (int32_t)r;  // this thread's key
+          if (go && (key >= hi_key || key < lo_key || (badp >> (r >> box_lg) & 1u))) {
             const uint32_t va = smem_addr(s_kv + (ev % kRing) * S::kTile) + r * 128u;
 #pragma unroll
             for (uint32_t x = 0; x < S::kHalves * 8u; ++x)
@@ -609,230 +803,249 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        tmem_wait_ld(sv);
-        float s[128];
-#pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = __uint_as_float(sv[j]);
-        uint32_t pw[64];
-        if (__any_sync(0xFFFFFFFFu, key0 + kKeys > to_key || key0 < from_key) || badp) {
-          const int32_t hi = (int32_t)to_key - (int32_t)key0, lo = (int32_t)from_key - (int32_t)key0;
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (j >= hi || j < lo) s[j] = -INFINITY;
-          if (badp) {
-            const uint32_t bl = a.g.page_lg < 7u ? a.g.page_lg : 7u;
-#pragma unroll
-            for (int j = 0; j < 128; ++j)
-              if (badp >> ((uint32_t)j >> bl) & 1u) {
-                rowbad = rowbad || (j < hi && j >= lo);
-                s[j] = -INFINITY;
+        const bool masked = key0 + (int32_t)kKeys > all_to || key0 < all_from || badp;
+        // 32 keys from k0 on: a bit for each that this row sees
+        auto seen = [&](int32_t k0) {
+          const int32_t hi = min(max(to_key - k0, 0), 32), lo = min(max(from_key - k0, 0), 32);
+          uint32_t v = (hi >= 32 ? ~0u : (1u << hi) - 1u) & (lo >= 32 ? 0u : ~0u << lo);
+          if (badp) {  // pages with an id out of range
+#pragma unroll 1
+            for (int j = 0; j < 32; ++j)
+              if ((v >> j & 1u) && (badp >> ((uint32_t)(k0 - key0 + j) >> box_lg) & 1u)) {
+                rowbad = true;
+                v &= ~(1u << j);
               }
             if (r == 0) set_status(a.g.status, IBP_ERANGE);
           }
-        }
-        float mx0 = s[0], mx1 = s[1], mx2 = s[2], mx3 = s[3];
+          return v;
+        };
+        tmem_wait_ld(sv);
+        if (masked)
 #pragma unroll
-        for (int j = 4; j < 128; j += 4) {
-          mx0 = fmaxf(mx0, s[j]);
-          mx1 = fmaxf(mx1, s[j + 1]);
-          mx2 = fmaxf(mx2, s[j + 2]);
-          mx3 = fmaxf(mx3, s[j + 3]);
+          for (int g = 0; g < 4; ++g) {
+            const uint32_t v = seen(key0 + 32 * g);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(v >> j & 1u)) sv[32 * g + j] = 0xFF800000u;
+          }
+        // The weights need a reference, not the maximum: they are computed with the one
+        // at hand while the maximum is found, and again in the rare block whose
+        // maximum has outgrown it.
+        const uint64_t c2 = pair2(c, c);
+        uint64_t l0, l1, b2;
+        auto weights = [&](const int j, uint32_t (&w2)[32]) {  // 4 keys
+          float p0, p1, p2, p3;
+          split(fma2(pair2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), c2, b2), p0, p1);
+          split(fma2(pair2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3])), c2, b2), p2, p3);
+          p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
+          l0 = add2(l0, pair2(p0, p1));
+          l1 = add2(l1, pair2(p2, p3));
+          w2[(j & 63) / 2] = pack2(p0, p1, kBf16);
+          w2[(j & 63) / 2 + 1] = pack2(p2, p3, kBf16);
+        };
+        uint32_t pa[32], pb[32];
+        b2 = pair2(-base, -base);
+        l0 = l1 = 0;
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 64; j += 4) {
+          weights(j, pa);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[k] = max3(x[k], __uint_as_float(sv[2 * j + 2 * k]),
+                        __uint_as_float(sv[2 * j + 2 * k + 1]));
         }
-        m = fmaxf(m, fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * c);
+        m = fmaxf(m, fmaxf(max3(x[0], x[1], x[2]), x[3]) * c);
         const bool none = l == 0.f;  // this row has seen no key: any reference will do
-        if (!any) {
-          base = m == -INFINITY ? 0.f : m;
-        } else if (__any_sync(0xFFFFFFFFu, m > base + 8.f || (none && m != -INFINITY))) {
-          // every product issued so far is done (the scores came after it)
+        if (__any_sync(0xFFFFFFFFu, m > base + 8.f || (none && m != -INFINITY))) {
           const float nb = none && m != -INFINITY ? m : fmaxf(m, base);
           const float f = none ? 1.f : ex2(base - nb);
           base = nb;
           l *= f;
+          // every product issued so far is done (the scores came after it)
+          if (any)
+#pragma unroll 1
+            for (uint32_t d = 0; 32u * d < a.g.D; ++d) {
+              uint32_t o[32];
+              tmem_ld32<0>(to + 32u * d, o);
+              tmem_wait_ld(o);
 #pragma unroll
-          for (uint32_t x = 0; x < kDP / 32u; ++x) {
-            if (32u * x >= a.g.D) break;
-            uint32_t o[32];
-            tmem_ld32<0>(to + 32u * x, o);
-            tmem_wait_ld(o);
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32<0>(to + 32u * d, o);
+            }
+          b2 = pair2(-base, -base);
+          l0 = l1 = 0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-            tmem_st32<0>(to + 32u * x, o);
-          }
+          for (int j = 0; j < 64; j += 4) weights(j, pa);
         }
         any = true;
-        float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+        tmem_st32<0>(ts, pa);
+        auto arrive = [&](uint64_t* bar) {
+          tmem_wait_st();
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
 #pragma unroll
-        for (int j = 0; j < 128; j += 4) {
-          const float p0 = ex2(fmaf(s[j], c, -base)), p1 = ex2(fmaf(s[j + 1], c, -base));
-          const float p2 = ex2(fmaf(s[j + 2], c, -base)), p3 = ex2(fmaf(s[j + 3], c, -base));
-          l0 += p0;
-          l1 += p1;
-          l2 += p2;
-          l3 += p3;
-          pw[j / 2] = pack2(p0, p1, kBf16);
-          pw[j / 2 + 1] = pack2(p2, p3, kBf16);
+        for (int j = 64; j < kEarly; j += 4) weights(j, pb);
+        arrive(p_full + slot);
+#pragma unroll
+        for (int j = kEarly; j < 128; j += 4) weights(j, pb);
+        tmem_st32<0>(ts + 32u, pb);
+        {
+          float u, v;
+          split(add2(l0, l1), u, v);
+          l += u + v;
         }
-        l += (l0 + l1) + (l2 + l3);
-        tmem_st32<0>(ts, pw);
-        tmem_st32<32>(ts + 32u, pw);
-        tmem_wait_st();
-        tc_before();
-        mbar_arrive(p_full + slot);
+        arrive(p2_full + slot);
+        key0 += (int32_t)(both ? 2u * kKeys : kKeys);
       }
-      blocks += w.count;
-      e0 += 2u * w.count;
-      go = go && wait_or_fail(o_full, tiles++ & 1u, s_fail);
+      const uint32_t last = both ? (count - 1u - slot) / 2u * 2u + slot : count - 1u;
+      const uint32_t e_last = e0 + 2u * last + 1u;  // this slot's last values
+      blocks += count;
+      e0 += 2u * count;
+      go = go && wait_or_fail(o_full, tiles & 1u, s_fail);
+      ++tiles;
       go = both_slots(go && *reinterpret_cast<volatile uint32_t*>(s_fail) == 0u);
       if (!go) break;
       tc_after();
-      const bool whole = w.blk == 0 && w.count == w.t.nb;
-      const bool ends = w.blk + w.count == w.t.nb;
-      Piece<kDP>* piece = pieces + 2u * blockIdx.x + (tile_u >= u0 ? 1u : 0u);
+      if (wq == 0 && lane == 0 && any) release(e_last, both);
+      const bool whole = t->whole != 0u;
       float f0 = 1.f, f1 = 0.f;
-      // alternate blocks: slot 1 hands its sums to slot 0 through the free half of the
-      // queries' space, 64 channels at a time, [channel][row]
+      // alternate blocks: slot 1 hands its sums to slot 0 through the space of its queries
       float* x_o = reinterpret_cast<float*>(s_q + S::kTile);
-      if (two) {
-        // (maximum, sum and the unread-page flag first)
+      if (both) {
         if (slot == 1) {
           x_o[r] = any ? base : -INFINITY;
           x_o[128u + r] = l;
           x_o[256u + r] = rowbad ? 1.f : 0.f;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
         if (slot == 0) {
           const float b1 = x_o[r], l1 = x_o[128u + r];
           rowbad = rowbad || x_o[256u + r] != 0.f;
-          const float nb = l1 != 0.f && b1 > base ? b1 : base;
-          f0 = ex2(base - nb);
-          f1 = b1 == -INFINITY ? 0.f : ex2(b1 - nb);
+          const float nb = l1 == 0.f ? base : l == 0.f ? b1 : fmaxf(b1, base);
+          f0 = l == 0.f ? 0.f : ex2(base - nb);
+          f1 = l1 == 0.f ? 0.f : ex2(b1 - nb);
           l = l * f0 + l1 * f1;
           base = nb;
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
       }
       const bool some = live && !rowbad && l != 0.f;
-      const uint32_t R = row0 + r;
-      const uint64_t at = live ? ((uint64_t)(w.t.q0 + R / a.G) * a.g.H + w.t.head) * a.G + R % a.G
-                               : 0u;
       const float inv = some ? 1.f / l : 0.f;
-      const uint32_t pr = slot * kRows + r;
-      const bool writes = live && !(two && slot == 1);
-#pragma unroll
-      for (uint32_t x = 0; x < kDP / 32u; ++x) {
-        if (32u * x >= a.g.D) break;
+      const bool mine = !(both && slot == 1);  // slot 0 writes for both
+      Piece<kDP>* piece = pieces + 2u * blockIdx.x + t->place;
+#pragma unroll 1
+      for (uint32_t x = 0; 32u * x < a.g.D; ++x) {
         uint32_t o[32];
         tmem_ld32<0>(to + 32u * x, o);
         tmem_wait_ld(o);
-        float of[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) of[j] = __uint_as_float(o[j]);
-        if (two) {
+        if (both) {
           if (slot == 1)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x_o[j * 128 + r] = any ? of[j] : 0.f;
-          asm volatile("bar.sync 1, 256;" ::: "memory");
+            for (int j = 0; j < 32; ++j) x_o[j * 128 + r] = any ? __uint_as_float(o[j]) : 0.f;
+          asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
           if (slot == 0)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              of[j] = f1 != 0.f ? of[j] * f0 + x_o[j * 128 + r] * f1 : of[j] * f0;
-          asm volatile("bar.sync 1, 256;" ::: "memory");
+              o[j] = __float_as_uint((f0 != 0.f ? __uint_as_float(o[j]) * f0 : 0.f) +
+                                     (f1 != 0.f ? x_o[j * 128 + r] * f1 : 0.f));
+          asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
         }
-        if (writes && whole) {
-          uint8_t* dst = a.out + (at * a.g.D + 32u * x) * 2u;
+        if (mine && whole) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (32u * x + 8u * v < a.g.D) {
-              uint32_t y[4];
+          for (uint32_t v = 0; v < 4; ++v) {
+            uint32_t y[4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                y[j] = pack2(some ? of[8 * v + 2 * j] * inv : 0.f,
-                             some ? of[8 * v + 2 * j + 1] * inv : 0.f, kBf16);
-              *reinterpret_cast<uint4*>(dst + 16 * v) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
-        } else if (writes) {
-          float4* dst = reinterpret_cast<float4*>(&piece->o[pr][32u * x]);
+            for (int j = 0; j < 4; ++j)
+              y[j] = some ? pack2(__uint_as_float(o[8 * v + 2 * j]) * inv,
+                                  __uint_as_float(o[8 * v + 2 * j + 1]) * inv, kBf16)
+                          : 0u;
+            *reinterpret_cast<uint4*>(chunk_at(lane, 4u * x + v)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        } else if (mine && live) {
+          float* dst = &piece->o[32u * x][slot * kRows + r];
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(of[4 * v], of[4 * v + 1], of[4 * v + 2], of[4 * v + 3]);
+          for (int j = 0; j < 32; ++j) dst[j * kTileRows] = __uint_as_float(o[j]);
         }
       }
-      if (writes && whole) {
-        if (a.lse) a.lse[at] = some ? (base + log2f(l)) * 0.69314718056f : -INFINITY;
-      } else if (writes) {
-        piece->m[pr] = base;
-        piece->l[pr] = rowbad ? INFINITY : l;
+      if (mine && whole) {  // rows of the output, 16 lanes (or 8) each
+        __syncwarp();
+#pragma unroll 4
+        for (uint32_t i = 0; i < kLd; ++i) {
+          const uint32_t row = i * kPer + my_sub;
+          const uint64_t to_row = __shfl_sync(0xFFFFFFFFu, live ? at : ~0ull, row);
+          if (to_row != ~0ull && my_ch * 8u < a.g.D)
+            *reinterpret_cast<uint4*>(a.out + (to_row * a.g.D + my_ch * 8u) * 2u) =
+                *reinterpret_cast<const uint4*>(chunk_at(row, my_ch));
+        }
+        if (a.lse && live) a.lse[at] = some ? (base + log2f(l)) * 0.69314718056f : -INFINITY;
+        __syncwarp();
+      } else if (mine && live) {
+        piece->m[slot * kRows + r] = base;
+        piece->l[slot * kRows + r] = rowbad ? INFINITY : l;
       }
       tc_before();
-      if (ends && !whole) {
-        uint64_t f = tile_u * ctas / total;
-        while (f + 1 < ctas && total * (f + 1) / ctas <= tile_u) ++f;
-        while (f > 0 && total * f / ctas > tile_u) --f;
-        join.first = (uint32_t)f;
-        join.count = blockIdx.x - (uint32_t)f + 1u;
-        join.q0 = w.t.q0;
-        join.head = w.t.head;
-        join.row0 = w.t.row0;
-        join.rows = w.t.rows;
-      }
     }
-    if (tid == 128u) joins[blockIdx.x] = join;
   }
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 1)
+  if (warp == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                  : "memory");
   if (tid == 0 && *s_fail) set_status(a.g.status, IBP_ETIMEOUT);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Joins the pieces of the tile that CTA blockIdx.x of the first kernel ended: a
-// warp per row, in the pieces' order.
+// Joins the pieces of the tile that CTA blockIdx.x of the first kernel ended, in the
+// pieces' order: 32 rows per CTA (lane = row), 16 channels per warp.
 template <int kDP, bool kBf16>
-__global__ void __launch_bounds__(256) k_paged_chunk_join(PagedAttnArgs a) {
+__global__ void __launch_bounds__(kDP * 2) k_paged_chunk_join(PagedAttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Join* joins = reinterpret_cast<const Join*>(a.ws + IBP_PAGED_WORKSPACE_BYTES -
                                                     kMaxCtas * sizeof(Join));
   const Piece<kDP>* pieces = reinterpret_cast<const Piece<kDP>*>(a.ws + kStepWsBytes);
   const uint4 j0 = __ldcg(reinterpret_cast<const uint4*>(joins + blockIdx.x));
   const uint4 j1 = __ldcg(reinterpret_cast<const uint4*>(joins + blockIdx.x) + 1);
-  const uint32_t first = j0.x, count = j0.y, rows = j1.y, lane = threadIdx.x & 31u;
-  if (count == 0) return;
+  const uint32_t first = j0.x, count = j0.y, rows = j1.y;
+  const uint32_t r = blockIdx.y * 32u + (threadIdx.x & 31u), d0 = (threadIdx.x >> 5) * 16u;
+  if (count == 0 || r >= rows || d0 >= a.g.D) return;
   auto at_piece = [&](uint32_t i) { return pieces + 2u * (first + i) + (i == 0u ? 1u : 0u); };
-  for (uint32_t r = blockIdx.y * 8u + (threadIdx.x >> 5); r < rows; r += gridDim.y * 8u) {
-    float mx = -INFINITY;
-    for (uint32_t i = lane; i < count; i += 32u)
-      if (__ldcg(&at_piece(i)->l[r]) != 0.f) mx = fmaxf(mx, __ldcg(&at_piece(i)->m[r]));
+  float mx = -INFINITY;
+  for (uint32_t i = 0; i < count; ++i)
+    if (__ldcg(&at_piece(i)->l[r]) != 0.f) mx = fmaxf(mx, __ldcg(&at_piece(i)->m[r]));
+  const float base = mx == -INFINITY ? 0.f : mx;
+  float ll = 0.f, ov[16];
+  bool bad = false;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-    const float base = mx == -INFINITY ? 0.f : mx;
-    float ll = 0.f, ov[kDP / 32];
-    bool bad = false;
+  for (int x = 0; x < 16; ++x) ov[x] = 0.f;
+  for (uint32_t i = 0; i < count; ++i) {
+    const Piece<kDP>* p = at_piece(i);
+    const float li = __ldcg(&p->l[r]);
+    const float f = ex2(__ldcg(&p->m[r]) - base);
+    float v[16];
 #pragma unroll
-    for (int x = 0; x < kDP / 32; ++x) ov[x] = 0.f;
-    for (uint32_t i = 0; i < count; ++i) {
-      const Piece<kDP>* p = at_piece(i);
-      const float li = __ldcg(&p->l[r]);
-      if (li == 0.f) continue;
-      const float f = ex2(__ldcg(&p->m[r]) - base);
-      bad = bad || li == INFINITY;
-      ll += f * li;
+    for (int x = 0; x < 16; ++x) v[x] = __ldcg(&p->o[d0 + x][r]);
+    if (li == 0.f) continue;
+    bad = bad || li == INFINITY;
+    ll += f * li;
 #pragma unroll
-      for (int x = 0; x < kDP / 32; ++x) ov[x] = fmaf(f, __ldcg(&p->o[r][lane + 32u * x]), ov[x]);
-    }
-    const uint32_t R = j1.x + r;
-    const uint64_t at = ((uint64_t)(j0.z + R / a.G) * a.g.H + j0.w) * a.G + R % a.G;
-    const bool some = !bad && ll != 0.f;
-    const float inv = some ? 1.f / ll : 0.f;
-    uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + at * a.g.D;
-#pragma unroll
-    for (int x = 0; x < kDP / 32; ++x)
-      if (lane + 32u * x < a.g.D)
-        dst[lane + 32u * x] = (uint16_t)pack2(some ? ov[x] * inv : 0.f, 0.f, kBf16);
-    if (a.lse && lane == 0) a.lse[at] = some ? (mx + log2f(ll)) * 0.69314718056f : -INFINITY;
+    for (int x = 0; x < 16; ++x) ov[x] = fmaf(f, v[x], ov[x]);
   }
+  const uint32_t R = j1.x + r;
+  const uint64_t at = ((uint64_t)(j0.z + R / a.G) * a.g.H + j0.w) * a.G + R % a.G;
+  const bool some = !bad && ll != 0.f;
+  const float inv = some ? 1.f / ll : 0.f;
+  uint32_t y[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) y[x] = some ? pack2(ov[2 * x] * inv, ov[2 * x + 1] * inv, kBf16) : 0u;
+  uint4* dst = reinterpret_cast<uint4*>(a.out + (at * a.g.D + d0) * 2u);
+  dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  if (a.lse && d0 == 0) a.lse[at] = some ? (mx + log2f(ll)) * 0.69314718056f : -INFINITY;
 }
 
 template <int kDP, bool kBf16>
@@ -847,7 +1060,7 @@ cudaError_t launch(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, cud
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 8, 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  cfg.blockDim = dim3(kDP * 2, 1, 1);  // a warp per 16 channels
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
