@@ -11,121 +11,149 @@ namespace {
 // kLanes lanes hold a head, 8 channels (16 bytes) each: the sum of squares is
 // a shuffle tree over them, and a channel's rotation partner lies rot/2 channels
 // away, a whole number of lanes (rot is a multiple of 16), or in the same lane
-// (adjacent pairs).  Every byte is read and written once, 16 at a time.
-template <int kLanes, bool kBf16>
-__global__ void __launch_bounds__(256) k_paged_append(PagedAppendArgs a) {
-  const uint32_t lane = threadIdx.x & (kLanes - 1u);
+// (adjacent pairs).  A lane keeps its channels over all heads of a token, so the
+// token's place, its row of the rotation table and the norms' weights are fetched
+// once, and kAhead heads are in flight at a time.  Bound by HBM: every byte is
+// read and written once, 16 at a time.
+template <int kLanes, int kAhead, bool kBf16>
+__global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_t per) {
+  constexpr uint32_t kSubs = 128u / kLanes;  // heads side by side
+  const uint32_t lane = threadIdx.x & (kLanes - 1u), sub = threadIdx.x / kLanes;
   const uint32_t heads = a.Hq + 2u * a.g.H;  // queries, keys, values of a token
-  const uint64_t item = ((uint64_t)blockIdx.x * 256u + threadIdx.x) / kLanes;
-  const bool live = item < (uint64_t)a.b.n_tokens * heads;
-  const uint32_t t = live ? (uint32_t)(item / heads) : 0u;
-  const uint32_t hh = live ? (uint32_t)(item % heads) : 0u;
-  const uint32_t kind = hh < a.Hq ? 0u : hh < a.Hq + a.g.H ? 1u : 2u;
-  const uint32_t h = kind == 0u ? hh : kind == 1u ? hh - a.Hq : hh - a.Hq - a.g.H;
-  const bool mine = live && lane * 8u < a.g.D;
-  uint4 x = make_uint4(0, 0, 0, 0);
-  if (mine) {
-    const uint8_t* src = kind == 0u   ? a.q + t * a.q_stride
-                         : kind == 1u ? a.kx + t * a.kv_stride
-                                      : a.vx + t * a.kv_stride;
-    x = __ldcs(reinterpret_cast<const uint4*>(src + (uint64_t)h * a.g.D * 2u + lane * 16u));
-  }
+  const uint32_t t = blockIdx.x, h0 = blockIdx.y * kSubs * per + sub;
+  const uint32_t h1 = min(heads, (blockIdx.y + 1u) * kSubs * per);
+  const uint32_t c0 = lane * 8u;
+  const bool mine = c0 < a.g.D;
+  const uint64_t row = a.g.D * 2ull;
+  auto load = [&](uint32_t hh) {
+    const uint8_t* src =
+        hh < a.Hq            ? a.q + t * a.q_stride + hh * row
+        : hh < a.Hq + a.g.H  ? a.kx + t * a.kv_stride + (hh - a.Hq) * row
+                             : a.vx + t * a.kv_stride + (hh - a.Hq - a.g.H) * row;
+    return mine && hh < h1 ? __ldcs(reinterpret_cast<const uint4*>(src + lane * 16u))
+                           : make_uint4(0, 0, 0, 0);
+  };
+  uint4 x[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = load(h0 + i * kSubs);
+  // the norms' weights
+  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
+  if (a.q_norm && mine) wq = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + lane);
+  if (a.k_norm && mine) wk = __ldg(reinterpret_cast<const uint4*>(a.k_norm) + lane);
   // the token's place
-  uint32_t s = a.b.n_seqs, pos = 0;
-  bool ok = false;
-  if (live) {
-    s = paged_find(a.b, t);
-    if (s < a.b.n_seqs) {
-      const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
-      pos = q.L - q.n + (t - q.q0);
-      ok = q.ok && q.L >= q.n && (!a.cos_sin || pos < a.n_pos);
-      if (!ok && lane == 0) set_status(a.g.status, IBP_ERANGE);
-    }
-  }
-  uint8_t* dst = nullptr;
-  if (kind == 0u) {
-    dst = a.q_out + t * a.qo_stride + (uint64_t)h * a.g.D * 2u;
-    if (s == a.b.n_seqs) dst = nullptr;  // a row of no sequence
-  } else if (ok) {
+  const uint32_t s = paged_find(a.b, t);
+  if (s == a.b.n_seqs) return;  // a row of no sequence
+  const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
+  const uint32_t pos = q.L - q.n + (t - q.q0);
+  bool ok = q.ok && q.L >= q.n && (!a.cos_sin || pos < a.n_pos);
+  uint8_t *kd = nullptr, *vd = nullptr;
+  if (ok) {
     const int32_t page = __ldg(a.b.table + s * a.b.table_stride + (pos >> a.g.page_lg));
-    if (page < 0 || (uint32_t)page >= a.g.n_pages) {
-      if (lane == 0) set_status(a.g.status, IBP_ERANGE);
-    } else {
-      dst = (kind == 1u ? a.g.k : a.g.v) + (uint64_t)(uint32_t)page * a.g.page_stride +
-            (pos & ((1u << a.g.page_lg) - 1u)) * a.g.token_stride + h * a.g.head_stride;
+    if (page >= 0 && (uint32_t)page < a.g.n_pages) {
+      const uint64_t at = (uint64_t)(uint32_t)page * a.g.page_stride +
+                          (pos & ((1u << a.g.page_lg) - 1u)) * a.g.token_stride;
+      kd = a.g.k + at;
+      vd = a.g.v + at;
     }
   }
-  // values pass the same shuffles as their neighbours in the warp, unchanged
-  const uint8_t* w = kind == 0u ? a.q_norm : kind == 1u ? a.k_norm : nullptr;
-  const bool turned = a.cos_sin && kind != 2u;
-  float f[8];
-  {
-    const float2 f0 = unpack2(x.x, kBf16), f1 = unpack2(x.y, kBf16), f2 = unpack2(x.z, kBf16),
-                 f3 = unpack2(x.w, kBf16);
-    f[0] = f0.x, f[1] = f0.y, f[2] = f1.x, f[3] = f1.y;
-    f[4] = f2.x, f[5] = f2.y, f[6] = f3.x, f[7] = f3.y;
+  if (!kd) {
+    ok = false;
+    if (threadIdx.x == 0) set_status(a.g.status, IBP_ERANGE);
   }
-  if (a.q_norm || a.k_norm) {
-    float ss = 0.f;
+  // this lane's cosines and sines, the sines negated where y = x c - (partner) s
+  const uint32_t half = a.rot / 2u;
+  const bool low = c0 < half;
+  float cc[8], ss[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(f[i], f[i], ss);
-#pragma unroll
-    for (int d = kLanes / 2; d; d >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, d);
-    if (w && mine) {
-      const float r = rsqrtf(ss / (float)a.g.D + a.eps);
-      const uint4 g = __ldg(reinterpret_cast<const uint4*>(w) + lane);
-      const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+  for (int i = 0; i < 8; ++i) cc[i] = 1.f, ss[i] = 0.f;
+  if (a.cos_sin && ok && c0 < a.rot) {
+    const float* cs = a.cos_sin + (uint64_t)pos * a.rot;
+    if (a.pairs) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(cs + c0 / 2u));
+      const float4 n = __ldg(reinterpret_cast<const float4*>(cs + half + c0 / 2u));
+      const float c4[4] = {c.x, c.y, c.z, c.w}, n4[4] = {n.x, n.y, n.z, n.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 gf = unpack2(gw[i], kBf16);
-        f[2 * i] *= r * gf.x;
-        f[2 * i + 1] *= r * gf.y;
-      }
-    }
-  }
-  if (a.cos_sin) {
-    const float* cs = a.cos_sin + (uint64_t)(ok ? pos : 0u) * a.rot;
-    const uint32_t half = a.rot / 2u, c0 = lane * 8u;
-    if (a.pairs) {
-      if (turned && c0 < a.rot) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(cs + c0 / 2u));
-        const float4 n = __ldg(reinterpret_cast<const float4*>(cs + half + c0 / 2u));
-        const float cc[4] = {c.x, c.y, c.z, c.w}, nn[4] = {n.x, n.y, n.z, n.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float u = f[2 * i], v = f[2 * i + 1];
-          f[2 * i] = u * cc[i] - v * nn[i];
-          f[2 * i + 1] = v * cc[i] + u * nn[i];
-        }
+        cc[2 * i] = cc[2 * i + 1] = c4[i];
+        ss[2 * i] = -n4[i];
+        ss[2 * i + 1] = n4[i];
       }
     } else {
-      const bool low = c0 < half;
-      const uint32_t hl = half / 8u;
-      const uint32_t base = (threadIdx.x & 31u) & ~(kLanes - 1u);
-      const uint32_t from = base + ((low ? lane + hl : lane - hl) & (kLanes - 1u));
-      float p[8];
+      const uint32_t at = low ? c0 : c0 - half;
+      const float4* cp = reinterpret_cast<const float4*>(cs + at);
+      const float4* np = reinterpret_cast<const float4*>(cs + half + at);
+      const float4 ca = __ldg(cp), cb = __ldg(cp + 1), na = __ldg(np), nb = __ldg(np + 1);
+      cc[0] = ca.x, cc[1] = ca.y, cc[2] = ca.z, cc[3] = ca.w;
+      cc[4] = cb.x, cc[5] = cb.y, cc[6] = cb.z, cc[7] = cb.w;
+      ss[0] = na.x, ss[1] = na.y, ss[2] = na.z, ss[3] = na.w;
+      ss[4] = nb.x, ss[5] = nb.y, ss[6] = nb.z, ss[7] = nb.w;
+      if (low)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = __shfl_sync(0xFFFFFFFFu, f[i], from);
-      if (turned && c0 < a.rot) {
-        const float4* c4 = reinterpret_cast<const float4*>(cs + (low ? c0 : c0 - half));
-        const float4* n4 = reinterpret_cast<const float4*>(cs + half + (low ? c0 : c0 - half));
-        const float4 ca = __ldg(c4), cb = __ldg(c4 + 1), na = __ldg(n4), nb = __ldg(n4 + 1);
-        const float cc[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-        const float nn[8] = {na.x, na.y, na.z, na.w, nb.x, nb.y, nb.z, nb.w};
+        for (int i = 0; i < 8; ++i) ss[i] = -ss[i];
+    }
+  }
+  const uint32_t from = ((threadIdx.x & 31u) & ~(kLanes - 1u)) +
+                        ((low ? lane + half / 8u : lane - half / 8u) & (kLanes - 1u));
+  // every lane of a warp walks the same heads' rounds, so that the shuffles have them all
+  for (uint32_t r = 0; r < per; r += kAhead) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          f[i] = low ? f[i] * cc[i] - p[i] * nn[i] : f[i] * cc[i] + p[i] * nn[i];
+    for (int i = 0; i < kAhead; ++i) {
+      if (r + i >= per) break;
+      const uint32_t hh = h0 + (r + i) * kSubs;
+      const uint32_t kind = hh < a.Hq ? 0u : hh < a.Hq + a.g.H ? 1u : 2u;
+      const uint8_t* w = kind == 0u ? a.q_norm : kind == 1u ? a.k_norm : nullptr;
+      const bool turned = a.cos_sin && kind != 2u;
+      uint4 y = x[i];
+      if (r + kAhead + i < per) x[i] = load(hh + kAhead * kSubs);
+      float f[8];
+      {
+        const float2 f0 = unpack2(y.x, kBf16), f1 = unpack2(y.y, kBf16), f2 = unpack2(y.z, kBf16),
+                     f3 = unpack2(y.w, kBf16);
+        f[0] = f0.x, f[1] = f0.y, f[2] = f1.x, f[3] = f1.y;
+        f[4] = f2.x, f[5] = f2.y, f[6] = f3.x, f[7] = f3.y;
+      }
+      if (a.q_norm || a.k_norm) {
+        float sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum = fmaf(f[k], f[k], sum);
+#pragma unroll
+        for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+        if (w) {
+          const float n = rsqrtf(sum / (float)a.g.D + a.eps);
+          const uint4 g = kind == 0u ? wq : wk;
+          const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 gf = unpack2(gw[k], kBf16);
+            f[2 * k] *= n * gf.x;
+            f[2 * k + 1] *= n * gf.y;
+          }
+        }
+      }
+      if (a.cos_sin) {
+        float p[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          p[k] = a.pairs ? f[k ^ 1] : __shfl_sync(0xFFFFFFFFu, f[k], from);
+        if (turned && c0 < a.rot)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) f[k] = f[k] * cc[k] + p[k] * ss[k];
+      }
+      if (w || turned)
+        y = make_uint4(pack2(f[0], f[1], kBf16), pack2(f[2], f[3], kBf16),
+                       pack2(f[4], f[5], kBf16), pack2(f[6], f[7], kBf16));
+      if (hh < h1 && mine) {
+        if (kind == 0u) {
+          if (!ok) y = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(a.q_out + t * a.qo_stride + hh * row + lane * 16u) = y;
+        } else if (kd) {
+          uint8_t* d = kind == 1u ? kd + (hh - a.Hq) * a.g.head_stride
+                                  : vd + (hh - a.Hq - a.g.H) * a.g.head_stride;
+          *reinterpret_cast<uint4*>(d + lane * 16u) = y;
+        }
       }
     }
   }
-  if (w || turned) {
-    x.x = pack2(f[0], f[1], kBf16);
-    x.y = pack2(f[2], f[3], kBf16);
-    x.z = pack2(f[4], f[5], kBf16);
-    x.w = pack2(f[6], f[7], kBf16);
-  }
-  if (kind == 0u && !ok) x = make_uint4(0, 0, 0, 0);
-  if (mine && dst) *reinterpret_cast<uint4*>(dst + lane * 16u) = x;
 }
 
 template <bool kBf16>
@@ -224,7 +252,7 @@ __global__ void __launch_bounds__(128)
 constexpr uint32_t kScoreGroup = 32;  // pages between two stores of scores
 
 template <bool kBf16, int kDP>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 3)
     k_paged_scores(PagedGeom g, PagedBatchView b, const uint8_t* q, uint64_t q_stride, uint32_t G,
                    const uint8_t* bounds, float* scores, uint32_t per_warp) {
   constexpr int kC = kDP / 32;  // 16-byte chunks per lane
@@ -247,7 +275,7 @@ __global__ void __launch_bounds__(128)
   const uint32_t g1 = min(groups, g0 + per_warp);
   const int64_t pos_last = (int64_t)sq.L - sq.n + t0 + nt - 1;
   const uint32_t seen_last = pos_last < 0 ? 0u : (uint32_t)(pos_last >> g.page_lg) + 1u;
-  uint32_t qp[kC * 4 * 2], qn[kC * 4 * 2];  // [chunk][4 words][row, row + 8]
+  uint32_t qv[kC * 4 * 2];  // [chunk][4 words][row, row + 8]
   for (uint32_t gr = g0; gr < g1; ++gr) {
     const uint32_t c0 = gr * kScoreGroup;
     float best = 0.f;  // over the queries of the earlier row blocks (G > 16)
@@ -261,7 +289,7 @@ __global__ void __launch_bounds__(128)
         }
       }
       for (uint32_t rb = 0; rb * 16u < (tpt == 1u ? G : 16u); ++rb) {
-        if (gr == g0 || G > 16u) {  // the rows' queries, split by sign
+        if (gr == g0 || G > 16u) {  // the rows' queries
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const uint32_t r = rb * 16u + r0 + 8u * e;
@@ -277,8 +305,7 @@ __global__ void __launch_bounds__(128)
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                qp[(c * 4 + i) * 2 + e] = max2<kBf16>(w[i], 0u);
-                qn[(c * 4 + i) * 2 + e] = min2<kBf16>(w[i], 0u);
+                qv[(c * 4 + i) * 2 + e] = w[i];
               }
             }
           }
@@ -301,8 +328,12 @@ __global__ void __launch_bounds__(128)
           }
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
-            const uint32_t* p = qp + c * 8;
-            const uint32_t* n = qn + c * 8;
+            uint32_t p[8], n[8];  // split by sign
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              p[k] = max2<kBf16>(qv[c * 8 + k], 0u);
+              n[k] = min2<kBf16>(qv[c * 8 + k], 0u);
+            }
             mma_16816<kBf16>(acc, p, hi[c].x, hi[c].y);
             mma_16816<kBf16>(acc, p + 4, hi[c].z, hi[c].w);
             mma_16816<kBf16>(acc, n, lo[c].x, lo[c].y);
@@ -341,23 +372,147 @@ __global__ void __launch_bounds__(128)
 }
 
 // ---------------------------------------------------------------- select
-// One CTA per (token, K/V head).  Scores become whole numbers of the same order
-// (the sign bit folded in, NaN above all, the token's own page above that); the
-// n_sel-th largest is found digit by digit, 8 bits from the top, with a
-// histogram of the candidates that share the digits found so far; then one
-// ordered pass writes the numbers above it and the first of those equal to it.
-constexpr uint32_t kSelThreads = 256, kSelKeys = 8192;
-
+// Scores become whole numbers of the same order (the sign bit folded in, NaN above
+// all, -0 as 0); the token's own page is taken whatever its score, and of the
+// others those above the threshold, the largest number that at least n_sel - 1 of
+// them reach, then the first of those equal to it.
 __device__ __forceinline__ uint32_t order_key(float f) {
   if (f != f) return 0xFFFFFFFEu;
-  const uint32_t u = __float_as_uint(f + 0.f);  // -0 counts as 0
+  const uint32_t u = __float_as_uint(f + 0.f);  // -0 + 0 is 0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+
+// The row's place: its own page; the number of pages to choose from (0: none).
+__device__ __forceinline__ uint32_t select_row(const PagedGeom& g, const PagedBatchView& b,
+                                               uint32_t t, uint32_t s, uint32_t& own) {
+  const PagedSeq q = paged_seq(b, g.page_lg, s);
+  const int64_t pos = (int64_t)q.L - q.n + (t - q.q0);
+  if (!q.ok) set_status(g.status, IBP_ERANGE);
+  own = pos < 0 ? 0u : (uint32_t)(pos >> g.page_lg);
+  return !q.ok || pos < 0 ? 0u : own + 1u;
+}
+
+// kWarps warps to a row, its keys in their registers (kPer each; a warp has a run of
+// numbers).  The threshold is bracketed, from the smallest and the largest key on, by
+// counts of the keys that reach a candidate between, placed by the counts at the
+// bracket's ends, until as many reach it as are wanted.  Bound by issue: 2 kPer
+// instructions a count.  4 rows to a CTA when kWarps is 1.
+template <int kWarps, int kPer>
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32)
+    k_paged_pick(PagedGeom g, PagedBatchView b, const float* scores, uint32_t n_sel,
+                 int32_t* selected) {
+  constexpr int kRowsPer = kWarps == 1 ? 4 : 1;
+  __shared__ uint32_t s_sum[2][kWarps][2];
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
+  const uint64_t row = (uint64_t)blockIdx.x * kRowsPer + (kWarps == 1 ? warp : 0u);
+  if (row >= (uint64_t)b.n_tokens * g.H) return;
+  const uint32_t part = kWarps == 1 ? 0u : warp;
+  const uint32_t t = (uint32_t)(row / g.H);
+  int32_t* out = selected + row * n_sel;
+  const uint32_t i0 = part * (32u * kPer);
+  const float* src = scores + row * b.max_pages;
+  float f[kPer];  // fetched before the row's length is known
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t i = i0 + 32u * j + lane;
+    f[j] = i < b.max_pages ? __ldg(src + i) : 0.f;
+  }
+  const uint32_t s = paged_find(b, t);
+  if (s == b.n_seqs) return;
+  uint32_t own;
+  const uint32_t n = select_row(g, b, t, s, own);
+  if (n <= n_sel) {
+    for (uint32_t i = part * 32u + lane; i < n_sel; i += kWarps * 32u)
+      out[i] = i < n ? (int32_t)i : -1;
+    return;
+  }
+  uint32_t phase = 0;
+  // the sums of two values over the row
+  auto sum2 = [&](uint32_t x, uint32_t y, uint32_t* below) {
+    x = __reduce_add_sync(0xFFFFFFFFu, x);
+    if (below) y = __reduce_add_sync(0xFFFFFFFFu, y);
+    if (below) below[0] = below[1] = 0;
+    if (kWarps > 1) {
+      if (lane == 0) s_sum[phase][part][0] = x, s_sum[phase][part][1] = y;
+      __syncthreads();
+      x = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        x += s_sum[phase][w][0];
+        if (below && w < (int)part) below[0] += s_sum[phase][w][0], below[1] += s_sum[phase][w][1];
+      }
+      phase ^= 1u;
+    }
+    return x;
+  };
+  uint32_t key[kPer], lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t i = i0 + 32u * j + lane;
+    key[j] = i < n && i != own ? order_key(f[j]) : 0u;  // a score's key is above 0
+    if (key[j]) lo = min(lo, key[j]), hi = max(hi, key[j]);
+  }
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  if (kWarps > 1) {
+    if (lane == 0) s_sum[1][part][0] = lo, s_sum[1][part][1] = hi;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      lo = min(lo, s_sum[1][w][0]), hi = max(hi, s_sum[1][w][1]);
+  }
+  const uint32_t want = n_sel - 1u;
+  // lo is reached by `clo` keys, at least the wanted; hi by `chi`, too few
+  uint32_t thr = lo, clo = n - 1u, chi = 0;
+  if (want) {
+    uint64_t top = (uint64_t)hi + 1u;
+    for (uint32_t k = 0; top - thr > 1u && clo != want; ++k) {
+      const uint32_t gap = (uint32_t)(top - thr);
+      // where the count would be met if the keys between lay evenly; every third time the middle
+      float part = (float)(clo - want) / (float)(clo - chi);
+      if (k % 3u == 2u) part = 0.5f;
+      uint32_t step = (uint32_t)((float)gap * part);
+      step = step < 1u ? 1u : step > gap - 1u ? gap - 1u : step;
+      const uint32_t cand = thr + step;
+      uint32_t c = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) c += key[j] >= cand;
+      c = sum2(c, 0, nullptr);
+      if (c >= want)
+        thr = cand, clo = c;
+      else
+        top = cand, chi = c;
+    }
+  }
+  uint32_t above = 0, equal = 0, below[2];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) above += key[j] > thr, equal += key[j] == thr;
+  const uint32_t all = sum2(above, equal, below);
+  // equal ones to take: none when only the own page is wanted
+  const uint32_t eq_want = want ? want - all : 0u;
+  uint32_t na = want ? below[0] : 0u, ne = below[1];
+  const uint32_t lt = (1u << lane) - 1u;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const uint32_t i = i0 + 32u * j + lane;
+    const bool up = want && key[j] > thr, eq = key[j] == thr && key[j];
+    const uint32_t bu = __ballot_sync(0xFFFFFFFFu, up), be = __ballot_sync(0xFFFFFFFFu, eq);
+    const uint32_t a = na + __popc(bu & lt), e = ne + __popc(be & lt);
+    const uint32_t at = a + min(e, eq_want) + (i > own ? 1u : 0u);
+    if (i == own || up || (eq && e < eq_want)) out[at] = (int32_t)i;
+    na += __popc(bu);
+    ne += __popc(be);
+  }
+}
+
+// Rows of more pages than that hold: one CTA to a row, the n_sel-th largest key
+// found digit by digit, 8 bits from the top, with a histogram of the keys that share
+// the digits found so far; then one ordered pass.
+constexpr uint32_t kSelThreads = 256;
 
 __global__ void __launch_bounds__(256)
     k_paged_select(PagedGeom g, PagedBatchView b, const float* scores, uint32_t n_sel,
                    int32_t* selected) {
-  __shared__ uint32_t s_key[kSelKeys];
   __shared__ uint32_t s_hist[256];
   __shared__ uint32_t s_warp[2][8];
   __shared__ uint32_t s_pick[2];
@@ -366,22 +521,14 @@ __global__ void __launch_bounds__(256)
   int32_t* out = selected + ((uint64_t)t * g.H + h) * n_sel;
   const uint32_t s = paged_find(b, t);
   if (s == b.n_seqs) return;
-  const PagedSeq q = paged_seq(b, g.page_lg, s);
-  const int64_t pos = (int64_t)q.L - q.n + (t - q.q0);
-  if (!q.ok && tid == 0) set_status(g.status, IBP_ERANGE);
-  const uint32_t own = pos < 0 ? 0u : (uint32_t)(pos >> g.page_lg);
-  const uint32_t n = !q.ok || pos < 0 ? 0u : own + 1u;  // pages to choose from
+  uint32_t own;
+  const uint32_t n = select_row(g, b, t, s, own);
   if (n <= n_sel) {
     for (uint32_t i = tid; i < n_sel; i += kSelThreads) out[i] = i < n ? (int32_t)i : -1;
     return;
   }
   const float* row = scores + ((uint64_t)t * g.H + h) * b.max_pages;
-  const bool held = n <= kSelKeys;
-  for (uint32_t i = tid; held && i < n; i += kSelThreads)
-    s_key[i] = i == own ? 0xFFFFFFFFu : order_key(__ldg(row + i));
-  auto key = [&](uint32_t i) {
-    return held ? s_key[i] : i == own ? 0xFFFFFFFFu : order_key(__ldg(row + i));
-  };
+  auto key = [&](uint32_t i) { return i == own ? 0xFFFFFFFFu : order_key(__ldg(row + i)); };
   uint32_t prefix = 0, mask = 0, want = n_sel;  // want-th largest among those with the prefix
   for (int sh = 24; sh >= 0; sh -= 8) {
     s_hist[tid] = 0;
@@ -443,28 +590,40 @@ uint32_t pow2_lanes(uint32_t D) { return D <= 32u ? 4u : D <= 64u ? 8u : 16u; }
 
 }  // namespace
 
-#define IBP_PAGED_LANES(KERN, GRID, BLOCK, ...)                                              \
-  do {                                                                                       \
-    const uint32_t ln = pow2_lanes(D_);                                                      \
-    if (bf_) {                                                                               \
-      if (ln == 4u) KERN<4, true><<<GRID, BLOCK, 0, st>>>(__VA_ARGS__);                      \
-      else if (ln == 8u) KERN<8, true><<<GRID, BLOCK, 0, st>>>(__VA_ARGS__);                 \
-      else KERN<16, true><<<GRID, BLOCK, 0, st>>>(__VA_ARGS__);                              \
-    } else {                                                                                 \
-      if (ln == 4u) KERN<4, false><<<GRID, BLOCK, 0, st>>>(__VA_ARGS__);                     \
-      else if (ln == 8u) KERN<8, false><<<GRID, BLOCK, 0, st>>>(__VA_ARGS__);                \
-      else KERN<16, false><<<GRID, BLOCK, 0, st>>>(__VA_ARGS__);                             \
-    }                                                                                        \
+#define IBP_PAGED_LANES(CALL)                                                     \
+  do {                                                                            \
+    const uint32_t ln = pow2_lanes(D_);                                           \
+    if (bf_) {                                                                    \
+      if (ln == 4u) CALL(4, true);                                                \
+      else if (ln == 8u) CALL(8, true);                                           \
+      else CALL(16, true);                                                        \
+    } else {                                                                      \
+      if (ln == 4u) CALL(4, false);                                               \
+      else if (ln == 8u) CALL(8, false);                                          \
+      else CALL(16, false);                                                       \
+    }                                                                             \
   } while (0)
 
-cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st) {
+cudaError_t launch_paged_append(const PagedAppendArgs& a, int sm_count, cudaStream_t st) {
   const uint32_t D_ = a.g.D;
   const bool bf_ = a.g.bf16 != 0u;
-  const uint64_t items = (uint64_t)a.b.n_tokens * (a.Hq + 2ull * a.g.H);
-  const uint64_t per = 256u / pow2_lanes(D_);
-  const uint64_t blocks = (items + per - 1) / per;
-  if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  IBP_PAGED_LANES(k_paged_append, (unsigned)blocks, 256, a);
+  // Heads that a lane goes over: 8 at most, all in flight while the token's place is
+  // looked up, and no more than leave eight CTAs to each SM.
+  const uint64_t subs = 128u / pow2_lanes(D_), heads = a.Hq + 2ull * a.g.H;
+  const uint64_t rounds = (heads + subs - 1) / subs;
+  uint64_t per = rounds * a.b.n_tokens / (8ull * sm_count);
+  per = per < 1u ? 1u : per > 8u ? 8u : per;
+  uint64_t y = (rounds + per - 1) / per;
+  per = (rounds + y - 1) / y;
+  if (y > 65535u) return cudaErrorInvalidValue;
+  const dim3 grid(a.b.n_tokens, (unsigned)y);
+#define IBP_CALL(L, B)                                                            \
+  do {                                                                            \
+    if (per >= 2u) k_paged_append<L, 8, B><<<grid, 128, 0, st>>>(a, (uint32_t)per); \
+    else k_paged_append<L, 1, B><<<grid, 128, 0, st>>>(a, (uint32_t)per);         \
+  } while (0)
+  IBP_PAGED_LANES(IBP_CALL);
+#undef IBP_CALL
   return cudaGetLastError();
 }
 
@@ -475,7 +634,9 @@ cudaError_t launch_paged_bounds(const PagedGeom& g, const PagedBatchView& b, uin
   const uint64_t tiles = ((uint64_t)b.n_tokens >> g.page_lg) + 2ull * b.n_seqs;
   const uint64_t blocks = (tiles * g.H + 3u) / 4u;
   if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  IBP_PAGED_LANES(k_paged_bounds, (unsigned)blocks, 128, g, b, bounds);
+#define IBP_CALL(L, B) k_paged_bounds<L, B><<<(unsigned)blocks, 128, 0, st>>>(g, b, bounds)
+  IBP_PAGED_LANES(IBP_CALL);
+#undef IBP_CALL
   return cudaGetLastError();
 }
 
@@ -486,9 +647,9 @@ cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, con
   const uint64_t tiles = (uint64_t)b.n_tokens / tpt + b.n_seqs;
   const uint64_t groups = (b.max_pages + kScoreGroup - 1u) / kScoreGroup;
   if (tiles > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  // enough warps to fill the GPU, as many groups of pages as that leaves to each
+  // groups of pages for each warp: one, until that makes 64 warps for every SM
   const uint64_t rows = tiles * g.H;
-  uint64_t per = (groups * rows + 24ull * sm_count - 1) / (24ull * sm_count);
+  uint64_t per = groups * rows / (64ull * sm_count);
   if (per > 16u) per = 16u;
   if (per < 1u) per = 1u;
   const uint64_t z = (groups + 4u * per - 1) / (4u * per);
@@ -513,8 +674,31 @@ cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, con
 }
 
 cudaError_t launch_paged_select(const PagedGeom& g, const PagedBatchView& b, const float* scores,
-                                uint32_t n_sel, int32_t* selected, cudaStream_t st) {
-  k_paged_select<<<dim3(b.n_tokens, g.H), kSelThreads, 0, st>>>(g, b, scores, n_sel, selected);
+                                uint32_t n_sel, int32_t* selected, int sm_count,
+                                cudaStream_t st) {
+  // One warp to a row when there are rows for every SM's issue slots (16 warps) and its
+  // registers hold them; else 8 warps.
+  const uint64_t rows = (uint64_t)b.n_tokens * g.H;
+  const uint32_t most = b.max_pages;
+#define IBP_PICK(W, P, BLOCKS)                                                             \
+  k_paged_pick<W, P><<<(unsigned)(BLOCKS), W == 1 ? 128 : W * 32, 0, st>>>(g, b, scores, n_sel, \
+                                                                          selected)
+  if (rows > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  if (rows >= 16ull * sm_count && most <= 2048u) {
+    const uint64_t blocks = (rows + 3u) / 4u;
+    if (most <= 256u) IBP_PICK(1, 8, blocks);
+    else if (most <= 512u) IBP_PICK(1, 16, blocks);
+    else if (most <= 1024u) IBP_PICK(1, 32, blocks);
+    else IBP_PICK(1, 64, blocks);
+  } else if (most <= 16384u) {
+    if (most <= 512u) IBP_PICK(8, 2, rows);
+    else if (most <= 2048u) IBP_PICK(8, 8, rows);
+    else if (most <= 8192u) IBP_PICK(8, 32, rows);
+    else IBP_PICK(8, 64, rows);
+  } else {
+    k_paged_select<<<dim3(b.n_tokens, g.H), kSelThreads, 0, st>>>(g, b, scores, n_sel, selected);
+  }
+#undef IBP_PICK
   return cudaGetLastError();
 }
 

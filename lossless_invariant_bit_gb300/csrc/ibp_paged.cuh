@@ -61,21 +61,22 @@ struct PagedAppendArgs {
 // workspace of an attention call: the one-token kernel's pieces, then the chunk kernel's
 constexpr uint64_t kStepWsBytes = 32ull << 20;
 
-cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t st);
+cudaError_t launch_paged_append(const PagedAppendArgs& a, int sm_count, cudaStream_t st);
 cudaError_t launch_paged_bounds(const PagedGeom& g, const PagedBatchView& b, uint8_t* bounds,
                                 cudaStream_t st);
 cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, const uint8_t* q,
                                 uint64_t q_stride, uint32_t G, const uint8_t* bounds,
                                 float* scores, int sm_count, cudaStream_t st);
 cudaError_t launch_paged_select(const PagedGeom& g, const PagedBatchView& b, const float* scores,
-                                uint32_t n_sel, int32_t* selected, cudaStream_t st);
+                                uint32_t n_sel, int32_t* selected, int sm_count,
+                                cudaStream_t st);
 // Sequences with at most a.max_rows rows (new tokens x query heads of a K/V
 // head), or tokens with a page list each.
 constexpr uint32_t kStepRows = 16;
 cudaError_t launch_paged_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
                               cudaStream_t st);
-// Tokens of a page in one box of the maps of the step and the chunk kernel.
-constexpr uint32_t kStepBox = 32, kChunkBox = 128;
+// Tokens of a page in one box of the maps, at most.
+constexpr uint32_t kBoxTokens = 128;
 // Sequences with more than a.max_rows rows.
 cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
                                cudaStream_t st);

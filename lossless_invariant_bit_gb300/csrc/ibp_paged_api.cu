@@ -55,7 +55,7 @@ struct ibp_paged {
   int status_at;
   ibp::PagedGeom g;
   int device, sm_count;
-  ibp::PagedMaps step, chunk;
+  ibp::PagedMaps maps;
 };
 
 namespace {
@@ -147,10 +147,8 @@ ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device) !=
           cudaSuccess ||
-      !page_map(&c->step.k, *d, d->k, ibp::kStepBox) ||
-      !page_map(&c->step.v, *d, d->v, ibp::kStepBox) ||
-      !page_map(&c->chunk.k, *d, d->k, ibp::kChunkBox) ||
-      !page_map(&c->chunk.v, *d, d->v, ibp::kChunkBox)) {
+      !page_map(&c->maps.k, *d, d->k, ibp::kBoxTokens) ||
+      !page_map(&c->maps.v, *d, d->v, ibp::kBoxTokens)) {
     delete c;
     return IBP_ECUDA;
   }
@@ -226,7 +224,7 @@ ibp_status ibp_paged_append(const ibp_paged* c, const ibp_paged_batch* b, const 
   a.n_pos = n_pos;
   a.rot = cos_sin ? rot_dim : 0u;
   a.pairs = pairs;
-  return cu(ibp::launch_paged_append(a, reinterpret_cast<cudaStream_t>(stream)));
+  return cu(ibp::launch_paged_append(a, c->sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, const void* q,
@@ -267,12 +265,12 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
   const bool few = selected || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
   if (few || b->n_seqs > 1u) {
     a.max_rows = ibp::kStepRows;
-    const cudaError_t ce = ibp::launch_paged_step(a, c->step, c->sm_count, st);
+    const cudaError_t ce = ibp::launch_paged_step(a, c->maps, c->sm_count, st);
     if (ce != cudaSuccess || few) return cu(ce);
   } else {
     a.max_rows = 0;
   }
-  return cu(ibp::launch_paged_chunk(a, c->chunk, c->sm_count, st));
+  return cu(ibp::launch_paged_chunk(a, c->maps, c->sm_count, st));
 }
 
 ibp_status ibp_paged_bounds(const ibp_paged* c, const ibp_paged_batch* b, void* bounds,
@@ -308,7 +306,7 @@ ibp_status ibp_paged_select(const ibp_paged* c, const ibp_paged_batch* b, const 
   if (!scores || !selected || n_selected == 0 || n_selected > IBP_PAGED_MAX_SELECTED)
     return IBP_EINVAL;
   if (misaligned(scores, 4) || misaligned(selected, 4)) return IBP_EALIGN;
-  return cu(ibp::launch_paged_select(c->g, view(b), scores, n_selected, selected,
+  return cu(ibp::launch_paged_select(c->g, view(b), scores, n_selected, selected, c->sm_count,
                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 

@@ -151,8 +151,16 @@ struct Info {
   uint32_t lo, hi, key0;  // keys that any row sees, first key of the run
   uint32_t whole;         // the run is the whole tile: write the result, not a piece
   uint32_t place;         // which of the CTA's two pieces
-  uint32_t pad[3];
+  uint32_t s;             // sequence
+  uint32_t all_lo, all_hi;  // keys that every row sees
 };
+// A block in which some rows see keys that others do not, and some of those keys'
+// values are infinite or NaN: bit per key.  A tile's rows span at most 256 positions,
+// so 3 blocks at either end of what they see, and a slot has that many at most.
+struct Odd {
+  uint32_t key0, keys[4];
+};
+constexpr uint32_t kOdd = 8;
 constexpr uint32_t kInfos = 8;
 // Keys whose weights are computed before the first half of them is handed over: what
 // waits for the first half's store is then hidden (64 to 112 measured alike).
@@ -170,17 +178,6 @@ __device__ __forceinline__ bool walk(const PagedAttnArgs& a, Walk& w) {
   if (w.count > left) w.count = (uint32_t)left;
   w.u += w.count;
   return true;
-}
-
-__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                              uint32_t x, uint32_t token, uint32_t head,
-                                              int32_t page) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(token), "r"(head),
-      "r"(page)
-      : "memory");
 }
 
 // The matrix instructions of a block, issued by the lane with `on` set while the
@@ -295,12 +292,6 @@ __device__ __forceinline__ void tc_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 // The registers of the launch, shared out again: 8 warps of 208 and 4 of 88 are
 // the 12 of 168 that the launch came with.
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;"); }
@@ -332,36 +323,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Whether both slots (256 threads) say so; every tile has one such vote, so that
-// neither waits for the other once one has given up.
-__device__ __forceinline__ bool both_slots(bool mine) {
-  uint32_t all;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " barrier.cta.red.and.pred q, 2, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(all)
-      : "r"((uint32_t)mine)
-      : "memory");
-  return all != 0u;
-}
-
-// A wait of a whole warp.  One that has run out (about two seconds) sets *fail;
-// the waits that run after it give up at once if what they wait for is not there.
-__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, uint32_t* fail) {
-  const uint32_t at = smem_addr(bar);
-  if (__all_sync(0xFFFFFFFFu, mbar_try(at, parity))) return true;
-  const uint64_t t0 = global_ns();
-  while (true) {
-    if (__all_sync(0xFFFFFFFFu, mbar_try(at, parity))) return true;
-    const bool late = global_ns() - t0 > 2000000000ull ||
-                      *reinterpret_cast<volatile uint32_t*>(fail) != 0u;
-    if (__any_sync(0xFFFFFFFFu, late)) {
-      atomicExch(fail, 1u);
-      return false;
-    }
-  }
-}
-
 template <int kDP, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap map_k,
@@ -381,11 +342,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = turn + 2;       // the tile's queries are there
   uint64_t* o_full = q_full + 1;     // every product of the tile is done
   uint64_t* done = o_full + 1;       // per slot, after a failure: its products are done
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 2);
+  uint64_t* looked = done + 2;       // per slot: its warps have searched a block's values
+  uint64_t* ended = looked + 2;      // both slots' warps have ended the tile
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(ended + 1);
   uint32_t* s_fail = s_tmem + 1;
   uint32_t* s_bad = s_fail + 1;      // 8 blocks: bit per page with an id out of range
   __shared__ Info s_info[kInfos];
   __shared__ uint64_t info_full[kInfos];
+  __shared__ uint32_t s_nan[8][4];   // 8 blocks: bit per key with such values
+  __shared__ Odd s_odd[2][kOdd];     // per slot, those of the tile
   __shared__ uint64_t s_scan[kThreads / 32];
   __shared__ uint64_t s_found[3];
 
@@ -406,10 +371,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p2_full + i, 4);
       mbar_init(turn + i, 1);
       mbar_init(done + i, 1);
+      mbar_init(looked + i, 4);
     }
     for (uint32_t i = 0; i < kInfos; ++i) mbar_init(info_full + i, 1);
     mbar_init(q_full, 8);
     mbar_init(o_full, 2);
+    mbar_init(ended, 8);
     *s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -523,6 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         x->key0 = (w.t.b0 + w.blk) * kKeys;
         x->whole = whole;
         x->place = tile_u >= u0 ? 1u : 0u;
+        x->s = w.t.s;
+        {
+          const int32_t first = (int32_t)(w.t.L - w.t.n + w.t.row0 / a.G);
+          const int32_t last = (int32_t)(w.t.L - w.t.n + (w.t.row0 + w.t.rows - 1u) / a.G);
+          x->all_hi = a.causal ? (uint32_t)max(first + 1, 0) : w.t.L;
+          x->all_lo = a.window ? (uint32_t)max(last + 1 - (int32_t)a.window, 0) : 0u;
+        }
         mbar_arrive(info_full + tiles % kInfos);
         if (more && w.blk + w.count == w.t.nb && !whole) {
           uint64_t f = tile_u * ctas / total;
@@ -560,7 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (round > 0) go = wait_or_fail(empty + st, (round - 1u) & 1u, s_fail);
           if (!go) break;
           if (lane == 0) {
-            if (kv == 0) s_bad[blocks & 7u] = bad;
+            if (kv == 0) {
+              s_bad[blocks & 7u] = bad;
+              for (int k = 0; k < 4; ++k) s_nan[blocks & 7u][k] = 0;
+            }
             mbar_expect_tx(full + st, bytes);
           }
           __syncwarp();
@@ -741,7 +718,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(empty + e % kRing);
       if (twice) mbar_arrive(empty + e % kRing);
     };
-    uint32_t sn = 0, tiles = 0, blocks = 0, e0 = 0;
+    // Infinities and NaN of the values of the block's odd keys that this row sees, into
+    // 32 channels of its sums: rare, and read again from the pages.
+    auto add_odd = [&](const Info* t, const Odd& b, uint32_t x, int32_t from, int32_t to,
+                       uint32_t (&o)[32]) {
+#pragma unroll 1
+      for (uint32_t j = 0; j < kKeys; ++j) {
+        const int32_t key = (int32_t)(b.key0 + j);
+        if (!(b.keys[j >> 5] >> (j & 31u) & 1u) || key < from || key >= to) continue;
+        const int32_t page =
+            __ldg(a.b.table + t->s * a.b.table_stride + ((uint32_t)key >> a.g.page_lg));
+        const uint16_t* v = reinterpret_cast<const uint16_t*>(
+            a.g.v + (uint64_t)(uint32_t)page * a.g.page_stride + t->head * a.g.head_stride +
+            ((uint32_t)key & ((1u << a.g.page_lg) - 1u)) * a.g.token_stride);
+#pragma unroll
+        for (int d = 0; d < 32; ++d)
+          if (32u * x + d < a.g.D) {
+            const float f = to_float(__ldg(v + 32u * x + d), kBf16);
+            if (!(fabsf(f) < INFINITY)) o[d] = __float_as_uint(__uint_as_float(o[d]) + f);
+          }
+      }
+    };
+    uint32_t sn = 0, tiles = 0, blocks = 0, e0 = 0, looks = 0;
     bool go = true;
     while (go) {
       const Info* t = info_of(tiles);
@@ -750,8 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool both = t->two != 0u;
       const uint32_t count = t->count;
       // this row, and its keys: [from, to)
-      const uint32_t nrows = both ? t->rows : min(kRows, t->rows > slot * kRows ? t->rows - slot * kRows : 0u);
-      const bool live = r < nrows;
+      const bool live = r + (both ? 0u : slot * kRows) < t->rows;
       int32_t to_key, from_key;
       uint64_t at;  // its place among [n_tokens, q_heads]
       {
@@ -764,6 +761,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int32_t key0 = (int32_t)t->key0;
       const int32_t lo_key = (int32_t)t->lo, hi_key = (int32_t)t->hi;
+      const int32_t every_lo = (int32_t)t->all_lo, every_hi = (int32_t)t->all_hi;
+      uint32_t odd = 0;  // entries of s_odd
       // keys that every row of the warp sees need no mask
       const int32_t all_to = __reduce_min_sync(0xFFFFFFFFu, live ? to_key : 0x7FFFFFFF);
       const int32_t all_from = __reduce_max_sync(0xFFFFFFFFu, live ? from_key : 0);
@@ -787,21 +786,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t badp = s_bad[(blocks + i) & 7u];
         const bool edge = key0 + (int32_t)kKeys > hi_key || key0 < lo_key || badp;
-        if (edge) {
-          // values that no row sees: zero, so that 0 * (what they hold) is 0
+        const bool mixed = key0 + (int32_t)kKeys > every_hi || key0 < every_lo;
+        if (edge || mixed) {
+          // Values that no row sees become zero, so that 0 * (what they hold) is 0.  Where
+          // only some rows see a key, infinities and NaN of its values become zero too and
+          // are added to the rows that see them at the tile's end.
           const uint32_t ev = e0 + 2u * i + 1u;
           go = wait_or_fail(full + ev % kRing, (ev / kRing) & 1u, s_fail);
           const int32_t key = key0 + (int32_t)r;  // this thread's key
-          if (go && (key >= hi_key || key < lo_key || (badp >> (r >> box_lg) & 1u))) {
-            const uint32_t va = smem_addr(s_kv + (ev % kRing) * S::kTile) + r * 128u;
+          const bool none = key >= hi_key || key < lo_key || (badp >> (r >> box_lg) & 1u);
+          const uint32_t va = smem_addr(s_kv + (ev % kRing) * S::kTile) + r * 128u;
+          if (go && none) {
 #pragma unroll
             for (uint32_t x = 0; x < S::kHalves * 8u; ++x)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
                                va + (x >> 3) * S::kHalf + (x & 7u) * 16u),
                            "r"(0u)
                            : "memory");
+          } else if (go && mixed) {
+            // an exponent of ones, plus one, reaches the sign's place
+            constexpr uint32_t kExp = kBf16 ? 0x7F807F80u : 0x7C007C00u;
+            constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
+            auto chunk = [&](uint32_t x) {
+              return va + (x >> 3) * S::kHalf + (((x & 7u) ^ (r & 7u)) << 4);
+            };
+            uint32_t hit = 0;
+#pragma unroll 8
+            for (uint32_t x = 0; x < S::kHalves * 8u; ++x) {
+              uint32_t y[4];
+              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                           : "r"(chunk(x))
+                           : "memory");
+#pragma unroll
+              for (int k = 0; k < 4; ++k) hit |= (y[k] & kExp) + kOne;
+            }
+            if (hit & 0x80008000u) {  // noted before they are cleared: the other slot may look next
+              atomicOr(&s_nan[(blocks + i) & 7u][r >> 5], 1u << (r & 31u));
+              __threadfence_block();
+#pragma unroll 1
+              for (uint32_t x = 0; x < S::kHalves * 32u; ++x) {
+                const uint32_t at = chunk(x >> 2) + 4u * (x & 3u);
+                uint32_t y;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(at) : "memory");
+                const uint32_t ones = ((y & kExp) + kOne) & 0x80008000u;  // a half's top bit
+                if (ones & 0x8000u) y &= 0xFFFF0000u;
+                if (ones & 0x80000000u) y &= 0x0000FFFFu;
+                if (ones)
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(y) : "memory");
+              }
+            }
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          if (mixed) {
+            // every thread of the slot has looked
+            __syncwarp();
+            if (lane == 0) mbar_arrive(looked + slot);
+            go = go && wait_or_fail(looked + slot, looks++ & 1u, s_fail);
+            const volatile uint32_t* f = s_nan[(blocks + i) & 7u];
+            if (f[0] | f[1] | f[2] | f[3]) {
+              if (odd < kOdd) {
+                if (r < 4u) s_odd[slot][odd].keys[r] = f[r];
+                if (r == 0) s_odd[slot][odd].key0 = (uint32_t)key0;
+                ++odd;
+              }
+            }
+          }
         }
         const bool masked = key0 + (int32_t)kKeys > all_to || key0 < all_from || badp;
         // 32 keys from k0 on: a bit for each that this row sees
@@ -906,7 +956,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       e0 += 2u * count;
       go = go && wait_or_fail(o_full, tiles & 1u, s_fail);
       ++tiles;
-      go = both_slots(go && *reinterpret_cast<volatile uint32_t*>(s_fail) == 0u);
+      // both slots say that they are here before either counts on the other below
+      if (go && lane == 0) mbar_arrive(ended);
+      __syncwarp();
+      go = go && wait_or_fail(ended, (tiles - 1u) & 1u, s_fail);
       if (!go) break;
       tc_after();
       if (wq == 0 && lane == 0 && any) release(e_last, both);
@@ -941,6 +994,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tmem_ld32<0>(to + 32u * x, o);
         tmem_wait_ld(o);
+        for (uint32_t k = 0; k < odd; ++k)
+          add_odd(t, s_odd[slot][k], x, from_key, to_key, o);
         if (both) {
           if (slot == 1)
 #pragma unroll

@@ -10,13 +10,15 @@
 // new tokens), 4 D rows operations against 4 D bytes.
 //
 //   - The work of all sequences and heads is one list of blocks of 128 keys;
-//     each CTA takes an equal run of it (one CTA per SM), whatever the
-//     lengths.  A (sequence, head) whose run is cut is joined by a second kernel
-//     from the pieces' maxima, sums and unscaled outputs, in the order of the
+//     each CTA takes an equal run of it (one CTA per SM, two for small heads),
+//     whatever the lengths.  A (sequence, head) whose run is cut is joined by a second
+//     kernel from the pieces' maxima, sums and unscaled outputs, in the order of the
 //     pieces, so that results do not depend on timing.
-//   - Each of the 4 warps takes 32 keys of a block, with a ring of stages in
-//     shared memory of its own that it fills by TMA (a box per page) and waits
-//     for by mbarrier: no barrier of the CTA within a run.
+//   - A producer warp walks the list, looks pages up (32 boxes at a time, the next
+//     ones while these load) and fills a ring of blocks in shared memory by TMA, a box
+//     per page; it tells the others of each tile through shared memory.  Each of
+//     the 4 other warps takes 32 keys of a block and waits for its mbarrier alone: no
+//     barrier of the CTA within a tile.
 //   - 16 rows are one left operand of mma.sync m16n8k16: at 16 rows the keys'
 //     bytes, not the products, are the bound, and a 128-row tcgen05 tile would be
 //     7/8 padding (the chunk kernel takes what has more rows).
@@ -27,10 +29,10 @@
 namespace ibp {
 namespace {
 
-constexpr uint32_t kWarps = 4, kBlock = 128, kWarpKeys = 32;
-// page references of a stage beside page numbers: nothing to read, an id out of range
-constexpr uint32_t kNoPage = 0xFFFFFFFFu, kBadPage = 0xFFFFFFFEu;
+constexpr uint32_t kWarps = 4, kBlock = 128, kWarpKeys = 32, kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kMaxCtas = 512;
+// in the place of a box's first position: nothing to read, a page id out of range
+constexpr uint32_t kNoPage = 0xFFFFFFFFu, kBadPage = 0xFFFFFFFEu;
 
 // One piece of a cut (sequence, head): 16 rows of running maximum, sum, output.
 template <int kDP>
@@ -38,12 +40,6 @@ struct Piece {
   float m[16], l[16];
   float o[16][kDP];
 };
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // What the joining kernel is told by a CTA that ended a cut tile.
 struct Join {
@@ -56,13 +52,26 @@ struct Join {
 template <int kDP>
 struct StepShape {
   static constexpr uint32_t kHalves = kDP / 64;
-  static constexpr uint32_t kHalfBytes = kWarpKeys * 128u;
-  static constexpr uint32_t kTile = kHalves * kHalfBytes;      // keys (or values) of a stage
+  static constexpr uint32_t kHalf = kBlock * 128u;             // 64 channels of a block
+  static constexpr uint32_t kTile = kHalves * kHalf;           // keys (or values) of a block
   static constexpr uint32_t kStages = kDP == 64 ? 2u : 3u;
-  static constexpr uint32_t kRing = kStages * 2u * kTile;      // per warp
+  static constexpr uint32_t kRing = kStages * 2u * kTile;
   static constexpr uint32_t kMerge = kWarps * 16u * (kDP + 4u) * 4u;
-  static constexpr uint32_t kSmem = 1024u + kWarps * kRing + kMerge + 256u;
+  static constexpr uint32_t kSmem = 1024u + kRing + kMerge + 256u;
 };
+
+// What the producer tells the others of a run of blocks of one tile; count 0: no
+// more.  A ring of 8: the producer is at most 3 blocks ahead.
+struct Info {
+  uint32_t count;         // blocks
+  uint32_t q0, head;      // first row of the sequence (or the token), K/V head
+  uint32_t row0, rows;    // the tile's rows among the sequence's n * G
+  uint32_t n, L, lo;      // tokens, keys, first key that a row sees
+  uint32_t key0;          // first key of the run (without a page list)
+  uint32_t whole, place;  // the run is the whole tile; else which of the CTA's pieces
+  uint32_t pad;
+};
+constexpr uint32_t kInfos = 8;
 
 // A tile: 16 rows of one (sequence, head), or of one (token, head) with a page
 // list, and its blocks of keys.  Row r is query r % G of token r / G.
@@ -149,50 +158,16 @@ __device__ __forceinline__ void next_tile(const PagedAttnArgs& a, Cursor& c) {
   } while (c.t.nb == 0);
 }
 
-// What this lane loads of a warp's 32 keys of a block: one box, a page or 32 tokens of one.
-struct PageRef {
-  int32_t id;      // the page to read; -1: none
-  uint32_t token;  // first token within it
-  uint32_t ref;    // number among the sequence's pages << 9 | token, or kNoPage, kBadPage
-};
-
-template <bool kSel>
-__device__ __forceinline__ PageRef page_of(const PagedAttnArgs& a, const Cursor& c, uint32_t warp,
-                                           uint32_t lane) {
-  const uint32_t lg = a.g.page_lg;
-  const uint32_t box = lg < 5u ? 1u << lg : 32u;
-  const uint32_t key = (c.t.b0 + c.blk) * kBlock + warp * kWarpKeys + lane * box;
-  PageRef r{-1, key & ((1u << lg) - 1u), kNoPage};
-  if (lane * box >= kWarpKeys) return r;
-  uint32_t col = key >> lg;
-  if (kSel) {
-    if (col >= a.n_sel) return r;
-    const int32_t v = __ldg(c.t.sel + col);
-    if (v < 0 || c.t.L == 0 || (uint32_t)v > (c.t.L - 1u) >> lg) return r;
-    col = (uint32_t)v;
-    if ((col << lg) + r.token >= c.t.L) return r;
-  } else if (key >= c.t.L || key + box <= c.t.lo) {
-    return r;
-  }
-  const int32_t id = __ldg(c.t.table + col);
-  if (id < 0 || (uint32_t)id >= a.g.n_pages) {
-    r.ref = kBadPage;
-    return r;
-  }
-  r.id = id;
-  r.ref = col << 9 | r.token;
-  return r;
-}
-
-__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar,
-                                              uint32_t x, uint32_t token, uint32_t head,
-                                              int32_t page) {
+// A barrier of the four warps that compute, and whether any of their threads says so.
+__device__ __forceinline__ bool any_of_four(bool mine) {
+  uint32_t any;
   asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(token), "r"(head),
-      "r"(page)
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"((uint32_t)mine)
       : "memory");
+  return any != 0u;
 }
 
 // One row of the result, by a warp: lane i holds channels i, i + 32, ...  A row
@@ -211,7 +186,7 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, uint64_t at, u
 }
 
 template <int kDP, bool kBf16, bool kSel>
-__global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
     k_paged_step(const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, PagedAttnArgs a) {
   using S = StepShape<kDP>;
@@ -219,19 +194,28 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023u) & ~static_cast<uintptr_t>(1023u));
-  __shared__ uint64_t s_scan[8];
+  __shared__ uint64_t s_scan[kWarps + 1];
   __shared__ uint64_t s_found[2];
-  __shared__ uint32_t s_ref[kWarps][S::kStages][4];  // the pages of each stage
+  __shared__ uint32_t s_pos[S::kStages][16];  // first position of each box of a block
+  __shared__ Info s_info[kInfos];
+  __shared__ uint32_t s_fail;
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, tid = threadIdx.x;
-  uint8_t* ring = smem + warp * S::kRing;
-  float* merge = reinterpret_cast<float*>(smem + kWarps * S::kRing);
-  uint64_t* full =
-      reinterpret_cast<uint64_t*>(smem + kWarps * S::kRing + S::kMerge) + warp * S::kStages;
+  float* merge = reinterpret_cast<float*>(smem + S::kRing);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing + S::kMerge);
+  uint64_t* empty = full + S::kStages;
+  uint64_t* info_full = empty + S::kStages;
   Piece<kDP>* pieces = reinterpret_cast<Piece<kDP>*>(a.ws);
   Join* joins = reinterpret_cast<Join*>(a.ws + kStepWsBytes - kMaxCtas * sizeof(Join));
 
-  if (lane == 0) {
-    for (uint32_t i = 0; i < S::kStages; ++i) mbar_init(full + i, 1);
+  if (tid == 0) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_k)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_v)) : "memory");
+    for (uint32_t i = 0; i < S::kStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kWarps);
+    }
+    for (uint32_t i = 0; i < kInfos; ++i) mbar_init(info_full + i, 1);
+    s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -260,7 +244,7 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
   } else {
     uint32_t b0, lo, nrb;
     uint64_t mine = 0;
-    for (uint32_t s = tid; s < a.b.n_seqs; s += 128u) {
+    for (uint32_t s = tid; s < a.b.n_seqs; s += kThreads) {
       const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
       if (!q.ok) set_status(a.g.status, IBP_ERANGE);
       mine += (uint64_t)seq_blocks(a, q, b0, lo, nrb) * nrb;
@@ -269,16 +253,16 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
     for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
     if (lane == 0) s_scan[warp] = mine;
     __syncthreads();
-    for (uint32_t w = 0; w < kWarps; ++w) total += s_scan[w];
+    for (uint32_t w = 0; w <= kWarps; ++w) total += s_scan[w];
     total *= a.g.H;
     if (total < ctas) ctas = (uint32_t)total;
     if (blockIdx.x < ctas) {
       u0 = total * blockIdx.x / ctas;
       u1 = total * (blockIdx.x + 1u) / ctas;
     }
-    // the sequence that holds block u0: sums over 128 sequences at a time
+    // the sequence that holds block u0: sums over as many sequences as threads at a time
     uint64_t base = 0;
-    for (uint32_t c = 0; c < a.b.n_seqs && u0 < u1; c += 128u) {
+    for (uint32_t c = 0; c < a.b.n_seqs && u0 < u1; c += kThreads) {
       uint64_t nb = 0;
       if (c + tid < a.b.n_seqs) {
         nb = seq_blocks(a, paged_seq(a.b, a.g.page_lg, c + tid), b0, lo, nrb);
@@ -291,12 +275,12 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
         if (lane >= d) inc += v;
       }
       __syncthreads();
-      if (lane == 31u) s_scan[4 + warp] = inc;
+      if (lane == 31u) s_scan[warp] = inc;
       __syncthreads();
       uint64_t before = 0, all = 0;
-      for (uint32_t w = 0; w < kWarps; ++w) {
-        if (w < warp) before += s_scan[4 + w];
-        all += s_scan[4 + w];
+      for (uint32_t w = 0; w <= kWarps; ++w) {
+        if (w < warp) before += s_scan[w];
+        all += s_scan[w];
       }
       const uint64_t lo_u = base + (before + inc - nb) * a.g.H;
       if (u0 >= lo_u && u0 < lo_u + nb * a.g.H) {
@@ -318,91 +302,174 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
       tile_u = u0 - ld.blk;
     }
   }
-  Join join{};
-  if (u0 < u1) {
-    Cursor c = ld;  // the block being worked on; `ld` runs ahead with the loads
-    uint64_t u_ld = u0;
-    // fill stage i with the block under `ld`
-    auto issue = [&](uint32_t st) {
-      const PageRef r = page_of<kSel>(a, ld, warp, lane);
-      const uint32_t box = a.g.page_lg < 5u ? 1u << a.g.page_lg : 32u;
-      const uint32_t bytes = r.id >= 0 ? 2u * S::kHalves * box * 128u : 0u;
-      const uint32_t all = __reduce_add_sync(0xFFFFFFFFu, bytes);
-      if (lane < 4u) s_ref[warp][st][lane] = r.ref;
-      if (lane == 0) mbar_expect_tx(full + st, all);
+  if (warp == kWarps) {
+    // ---------------- producer
+    const uint32_t lg = a.g.page_lg, box_lg = lg < 7u ? lg : 7u;
+    const uint32_t per_lg = 7u - box_lg;        // boxes of a block
+    const uint32_t grp = 32u >> per_lg;         // blocks whose boxes are looked up together
+    Join join{};
+    uint32_t blocks = 0, tiles = 0;
+    bool go = true;
+    uint64_t u = u0;
+    for (bool first = true;; first = false) {
+      const bool more = u < u1 && go;
+      if (more && !first) {
+        next_tile<kSel>(a, ld);
+        tile_u = u;
+      }
+      const uint32_t count = !more ? 0u
+                             : u1 - u < ld.t.nb - ld.blk ? (uint32_t)(u1 - u)
+                                                         : ld.t.nb - ld.blk;
+      const bool ends = ld.blk + count == ld.t.nb;
+      const bool whole = ld.blk == 0 && ends;
+      if (lane == 0) {
+        Info* x = s_info + tiles % kInfos;
+        x->count = count;
+        x->q0 = ld.t.q0;
+        x->head = ld.t.head;
+        x->row0 = ld.t.rb * 16u;
+        x->rows = ld.t.n ? min(16u, ld.t.n * a.G - ld.t.rb * 16u) : 0u;
+        x->n = ld.t.n;
+        x->L = ld.t.L;
+        x->lo = ld.t.lo;
+        x->key0 = (ld.t.b0 + ld.blk) * kBlock;
+        x->whole = whole;
+        x->place = tile_u >= u0 ? 1u : 0u;
+        mbar_arrive(info_full + tiles % kInfos);
+        if (more && ends && !whole) {  // this CTA has the tile's last piece
+          // the CTA that holds the tile's first block
+          uint64_t f = tile_u * ctas / total;
+          while (f + 1 < ctas && total * (f + 1) / ctas <= tile_u) ++f;
+          while (f > 0 && total * f / ctas > tile_u) --f;
+          join.first = (uint32_t)f;
+          join.count = blockIdx.x - (uint32_t)f + 1u;
+          join.q0 = ld.t.q0;
+          join.rows = x->rows;
+          join.row0 = x->row0;
+          join.head = ld.t.head;
+        }
+      }
+      ++tiles;
       __syncwarp();
-      if (r.id >= 0) {
-        uint8_t* k = ring + st * 2u * S::kTile + lane * box * 128u;
+      if (!more) break;
+      // box `lane` of the group of blocks from b on: its first position, then its page
+      auto pos_at = [&](uint32_t b) {
+        const uint32_t key = (ld.t.b0 + b) * kBlock + (lane << box_lg);
+        if (b + (lane >> per_lg) >= ld.blk + count) return kNoPage;
+        if (!kSel)
+          return key >= ld.t.L || key + (1u << box_lg) <= ld.t.lo ? kNoPage : key;
+        const uint32_t at = key >> lg;
+        if (at >= a.n_sel) return kNoPage;
+        const int32_t v = __ldg(ld.t.sel + at);
+        if (v < 0 || ld.t.L == 0 || (uint32_t)v > (ld.t.L - 1u) >> lg) return kNoPage;
+        const uint32_t p = ((uint32_t)v << lg) + (key & ((1u << lg) - 1u));
+        return p >= ld.t.L ? kNoPage : p;
+      };
+      auto page_at = [&](uint32_t pos) {
+        return pos == kNoPage ? -1 : __ldg(ld.t.table + (pos >> lg));
+      };
+      uint32_t pos = pos_at(ld.blk);
+      int32_t page = page_at(pos);
+      uint32_t pos2 = pos_at(ld.blk + grp);
+      for (uint32_t b = ld.blk; b < ld.blk + count && go; ++b, ++blocks) {
+        const uint32_t in = (b - ld.blk) & (grp - 1u);  // which block of the group
+        if (in == 0 && b != ld.blk) {
+          pos = pos2;
+          page = page_at(pos);
+          pos2 = pos_at(b + grp);
+        }
+        const uint32_t st = blocks % S::kStages, round = blocks / S::kStages;
+        if (round > 0) go = wait_or_fail(empty + st, (round - 1u) & 1u, &s_fail);
+        if (!go) break;
+        const bool mine = (lane >> per_lg) == in;
+        const bool there = mine && pos != kNoPage;
+        const bool bad = there && (page < 0 || (uint32_t)page >= a.g.n_pages);
+        const uint32_t boxes = __popc(__ballot_sync(0xFFFFFFFFu, there && !bad));
+        if (mine) s_pos[st][lane & ((1u << per_lg) - 1u)] = bad ? kBadPage : pos;
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(full + st, boxes * (2u * S::kHalves * 128u << box_lg));
+        __syncwarp();
+        if (there && !bad) {
+          const uint32_t slot = lane & ((1u << per_lg) - 1u);
+          uint8_t* k = smem + st * 2u * S::kTile + (slot << box_lg) * 128u;
 #pragma unroll
-        for (uint32_t hf = 0; hf < S::kHalves; ++hf) {
-          tma_load_page(k + hf * S::kHalfBytes, &map_k, full + st, 64u * hf, r.token, ld.t.head,
-                        r.id);
-          tma_load_page(k + S::kTile + hf * S::kHalfBytes, &map_v, full + st, 64u * hf, r.token,
-                        ld.t.head, r.id);
+          for (uint32_t hf = 0; hf < S::kHalves; ++hf) {
+            tma_load_page(k + hf * S::kHalf, &map_k, full + st, 64u * hf,
+                          pos & ((1u << lg) - 1u), ld.t.head, page);
+            tma_load_page(k + S::kTile + hf * S::kHalf, &map_v, full + st, 64u * hf,
+                          pos & ((1u << lg) - 1u), ld.t.head, page);
+          }
         }
       }
-      ++u_ld;
-      if (++ld.blk == ld.t.nb && u_ld < u1) next_tile<kSel>(a, ld);
-    };
-#pragma unroll
-    for (uint32_t i = 0; i < S::kStages; ++i)
-      if (u_ld < u1) issue(i);
-
-    uint32_t st = 0, ph = 0, lost_st = 0, lost_ph = 0;
-    uint32_t qf[kKs][4];
-    float o[2 * kKs][4];
-    float m[2], l[2];
-    bool fresh = true, lost = false, bad = false;
+      u += count;
+    }
+    if (lane == 0) joins[blockIdx.x] = join;
+    if (!go)  // the copies in flight land before the CTA leaves (or their waits give up too)
+      for (uint32_t i = blocks > S::kStages ? blocks - S::kStages : 0u; i < blocks; ++i)
+        mbar_wait(full + i % S::kStages, (i / S::kStages) & 1u);
+  } else {
+    // ---------------- 32 keys of each block
     const uint32_t r0 = lane >> 2, quad = lane & 3u;
-    for (uint64_t u = u0; u < u1; ++u) {
-      const uint32_t rows = c.t.n ? min(16u, c.t.n * a.G - c.t.rb * 16u) : 0u;
-      if (fresh) {  // a new tile: its queries, as the left operand
-        fresh = false;
+    const uint32_t box_lg = a.g.page_lg < 7u ? a.g.page_lg : 7u;
+    uint32_t blocks = 0;
+    bool go = true;
+    for (uint32_t tiles = 0;; ++tiles) {
+      const Info* t = s_info + tiles % kInfos;
+      // a wait that gives up ends the tile like any other: the warps meet at its end,
+      // and leave together
+      go = wait_or_fail(info_full + tiles % kInfos, (tiles / kInfos) & 1u, &s_fail);
+      const uint32_t count = go ? t->count : 0u;
+      const uint32_t rows = count ? t->rows : 0u, row0 = t->row0, n = t->n, L = t->L, lo = t->lo;
+      uint32_t qf[kKs][4];
+      float o[2 * kKs][4];
+      float m[2], l[2];
+      bool bad = false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t r = r0 + 8u * e;
-          const uint32_t tt = (c.t.rb * 16u + r) / a.G, gg = (c.t.rb * 16u + r) % a.G;
-          const uint8_t* src = a.q + (uint64_t)(c.t.q0 + tt) * a.q_stride +
-                               ((uint64_t)c.t.head * a.G + gg) * a.g.D * 2u;
+      for (int e = 0; e < 2; ++e) {  // the tile's queries, as the left operand
+        const uint32_t r = r0 + 8u * e;
+        const uint32_t tt = (row0 + r) / a.G, gg = (row0 + r) - tt * a.G;
+        const uint8_t* src = a.q + (uint64_t)(t->q0 + tt) * a.q_stride +
+                             ((uint64_t)t->head * a.G + gg) * a.g.D * 2u;
 #pragma unroll
-          for (int k = 0; k < kKs; ++k)
+        for (int k = 0; k < kKs; ++k)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const uint32_t d = 16u * k + 8u * x + 2u * quad;
-              qf[k][e + 2 * x] = r < rows && d < a.g.D
-                                     ? __ldg(reinterpret_cast<const uint32_t*>(src + d * 2u))
-                                     : 0u;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2 * kKs; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        m[0] = m[1] = -INFINITY;
-        l[0] = l[1] = 0.f;
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t d = 16u * k + 8u * x + 2u * quad;
+            qf[k][e + 2 * x] = r < rows && d < a.g.D
+                                   ? __ldg(reinterpret_cast<const uint32_t*>(src + d * 2u))
+                                   : 0u;
+          }
       }
-      // ---- this warp's 32 keys
-      const uint32_t key0 = (c.t.b0 + c.blk) * kBlock + warp * kWarpKeys;
-      if (!lost && !mbar_wait(full + st, ph)) lost = bad = true, lost_st = st, lost_ph = ph;
-      const uint32_t kb = smem_addr(ring + st * 2u * S::kTile), vb = kb + S::kTile;
-      // which of the 32 keys exist: a bit each
-      uint32_t there;
-      {
-        const uint32_t lg = a.g.page_lg, box_lg = lg < 5u ? lg : 5u;
-        const uint32_t ref = s_ref[warp][st][lane >> box_lg];
-        if (ref == kBadPage) {
-          set_status(a.g.status, IBP_ERANGE);
-          bad = true;
+#pragma unroll
+      for (int i = 0; i < 2 * kKs; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+      m[0] = m[1] = -INFINITY;
+      l[0] = l[1] = 0.f;
+      for (uint32_t b = 0; b < count && go; ++b, ++blocks) {
+        const uint32_t key0 = t->key0 + b * kBlock + warp * kWarpKeys;
+        const uint32_t st = blocks % S::kStages;
+        go = wait_or_fail(full + st, (blocks / S::kStages) & 1u, &s_fail);
+        if (!go) break;
+        const uint32_t kb = smem_addr(smem + st * 2u * S::kTile) + warp * kWarpKeys * 128u;
+        const uint32_t vb = kb + S::kTile;
+        // which of the 32 keys exist: a bit each
+        uint32_t there;
+        {
+          const uint32_t at = warp * kWarpKeys + lane;
+          const uint32_t first = s_pos[st][at >> box_lg];
+          if (first == kBadPage) {
+            set_status(a.g.status, IBP_ERANGE);
+            bad = true;
+          }
+          const uint32_t key = first + (at & ((1u << box_lg) - 1u));
+          there = __ballot_sync(0xFFFFFFFFu, first < kBadPage && key < L && key >= lo);
         }
-        const uint32_t key = kSel ? ((ref >> 9) << lg) + (ref & 511u) + (lane & ((1u << box_lg) - 1u))
-                                  : key0 + lane;
-        there = __ballot_sync(0xFFFFFFFFu, ref < kBadPage && key < c.t.L && key >= c.t.lo && !lost);
-      }
-      if (there) {
+        if (there) {
         if (there != 0xFFFFFFFFu) {
           // rows of values that do not exist: zero, so that 0 * (what they hold) is 0
           for (uint32_t i = lane; i < kWarpKeys * S::kHalves * 8u; i += 32u) {
             const uint32_t row = i / 8u % kWarpKeys;
             if (!(there >> row & 1u)) {
-              const uint32_t off = (i / (8u * kWarpKeys)) * S::kHalfBytes + row * 128u + i % 8u * 16u;
+              const uint32_t off = (i / (8u * kWarpKeys)) * S::kHalf + row * 128u + i % 8u * 16u;
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + off), "r"(0u)
                            : "memory");
             }
@@ -421,7 +488,7 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
             uint32_t b[4];
             const uint32_t row = 16u * i + (lane & 7u) + ((lane >> 4) << 3);
             const uint32_t ch = 2u * (k & 3) + ((lane >> 3) & 1u);
-            ldmatrix4(b, kb + (k >> 2) * S::kHalfBytes + row * 128u + ((ch ^ (row & 7u)) << 4));
+            ldmatrix4(b, kb + (k >> 2) * S::kHalf + row * 128u + ((ch ^ (row & 7u)) << 4));
             mma_16816<kBf16>(sc[2 * i], qf[k], b[0], b[1]);
             mma_16816<kBf16>(sc[2 * i + 1], qf[k], b[2], b[3]);
           }
@@ -429,13 +496,12 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
         // ---- masks: what does not exist, and what lies beyond a row's position
         const bool partial =
             there != 0xFFFFFFFFu ||
-            (!kSel && c.t.n > 1u &&
-             (key0 + kWarpKeys + c.t.n > c.t.L + 1u || a.window));
+            (!kSel && n > 1u && (key0 + kWarpKeys + n > L + 1u || a.window));
         if (partial) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const uint32_t tt = (c.t.rb * 16u + r0 + 8u * e) / a.G;
-            const int64_t pos = kSel ? 0x7FFFFFFF : (int64_t)c.t.L - c.t.n + tt;
+            const uint32_t tt = (row0 + r0 + 8u * e) / a.G;
+            const int64_t pos = kSel ? 0x7FFFFFFF : (int64_t)L - n + tt;
             const int64_t from = a.window ? pos - a.window : -1;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -477,6 +543,55 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
             o[i][2 * e + 1] *= f;
           }
         }
+        if (!kSel && partial && n > 1u) {
+          // Where only some rows see a key, infinities and NaN of its values go to those
+          // rows alone, and become zero for the product.
+          constexpr uint32_t kExp = kBf16 ? 0x7F80u : 0x7C00u;  // all ones: not finite
+          bool found = false;
+          for (uint32_t x = 0; x < S::kHalves * 8u; ++x) {
+            uint32_t y[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                         : "r"(vb + (x >> 3) * S::kHalf + lane * 128u +
+                               (((x & 7u) ^ (lane & 7u)) << 4))
+                         : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              found = found || (y[k] & kExp) == kExp || (y[k] >> 16 & kExp) == kExp;
+          }
+          uint32_t odd = __ballot_sync(0xFFFFFFFFu, found);
+          for (; odd; odd &= odd - 1u) {
+            const uint32_t j = __ffs(odd) - 1u;
+            bool see[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int64_t pos = (int64_t)L - n + (row0 + r0 + 8u * e) / a.G;
+              const int64_t key = (int64_t)key0 + j;
+              see[e] = (!a.causal || key <= pos) && (!a.window || key > pos - (int64_t)a.window);
+            }
+#pragma unroll
+            for (int i = 0; i < 2 * kKs; ++i) {
+              const uint32_t at = vb + (i >> 3) * S::kHalf + j * 128u +
+                                  (((i & 7) ^ (j & 7u)) << 4) + quad * 4u;
+              uint32_t y;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(at) : "memory");
+              const bool bad0 = (y & kExp) == kExp, bad1 = (y >> 16 & kExp) == kExp;
+              const float2 f = unpack2(y, kBf16);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (see[e] && bad0) o[i][2 * e] += f.x;
+                if (see[e] && bad1) o[i][2 * e + 1] += f.y;
+              }
+              __syncwarp();
+              if (r0 == 0 && (bad0 || bad1))
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(at),
+                             "r"((bad0 ? 0u : y & 0xFFFFu) | (bad1 ? 0u : y & 0xFFFF0000u))
+                             : "memory");
+            }
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i)  // 16 keys at a time
 #pragma unroll
@@ -484,92 +599,65 @@ __global__ void __launch_bounds__(128, kDP == 64 ? 2 : 1)
             uint32_t b[4];
             const uint32_t row = 16u * i + (lane & 15u);
             const uint32_t ch = 2u * (k & 3) + (lane >> 4);
-            ldmatrix4_t(b, vb + (k >> 2) * S::kHalfBytes + row * 128u + ((ch ^ (row & 7u)) << 4));
+            ldmatrix4_t(b, vb + (k >> 2) * S::kHalf + row * 128u + ((ch ^ (row & 7u)) << 4));
             mma_16816<kBf16>(o[2 * k], pf[i], b[0], b[1]);
             mma_16816<kBf16>(o[2 * k + 1], pf[i], b[2], b[3]);
           }
       }
-      __syncwarp();  // every lane has read the stage
-      if (u_ld < u1 && !lost) issue(st);
-      if (++st == S::kStages) st = 0, ph ^= 1u;
-
-      // ---- end of the tile, or of this CTA's run: join the four warps
-      const bool tile_end = c.blk + 1u == c.t.nb;
-      if (tile_end || u + 1 == u1) {
-        float* mw = merge + warp * 16u * (kDP + 4u);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
-          l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
-          float* row = mw + (r0 + 8u * e) * (kDP + 4u);
-          if (quad == 0) row[kDP] = m[e], row[kDP + 1] = l[e];
-#pragma unroll
-          for (int i = 0; i < 2 * kKs; ++i)
-            *reinterpret_cast<float2*>(row + 8 * i + 2u * quad) =
-                make_float2(o[i][2 * e], o[i][2 * e + 1]);
-        }
-        const bool isbad = __syncthreads_or(bad) != 0;
-        const bool whole = tile_end && tile_u >= u0;
-        Piece<kDP>* piece = pieces + 2u * blockIdx.x + (tile_u >= u0 ? 1u : 0u);
-        for (uint32_t r = warp; r < rows; r += kWarps) {
-          float mm[kWarps], mx = -INFINITY, ll = 0.f, ov[kDP / 32];
-#pragma unroll
-          for (uint32_t w = 0; w < kWarps; ++w) {
-            mm[w] = merge[(w * 16u + r) * (kDP + 4u) + kDP];
-            mx = fmaxf(mx, mm[w]);
-          }
-          const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
-          for (int i = 0; i < kDP / 32; ++i) ov[i] = 0.f;
-#pragma unroll
-          for (uint32_t w = 0; w < kWarps; ++w) {
-            const float* src = merge + (w * 16u + r) * (kDP + 4u);
-            const float f = ex2(mm[w] - base);
-            ll += f * src[kDP + 1];
-#pragma unroll
-            for (int i = 0; i < kDP / 32; ++i) ov[i] = fmaf(f, src[lane + 32u * i], ov[i]);
-          }
-          if (isbad) ll = INFINITY;  // a row that could not be read: zero, here or when joined
-          if (whole) {
-            const uint32_t R = c.t.rb * 16u + r;
-            const uint64_t at =
-                ((uint64_t)(c.t.q0 + R / a.G) * a.g.H + c.t.head) * a.G + R % a.G;
-            store_row<kDP, kBf16>(a, at, lane, ov, mx, ll, isbad);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kDP / 32; ++i) piece->o[r][lane + 32u * i] = ov[i];
-            if (lane == 0) piece->m[r] = mx, piece->l[r] = ll;
-          }
-        }
-        if (tile_end && !whole) {  // this CTA has the last piece
-          // the CTA that holds the tile's first block
-          uint64_t f = tile_u * ctas / total;
-          while (f + 1 < ctas && total * (f + 1) / ctas <= tile_u) ++f;
-          while (f > 0 && total * f / ctas > tile_u) --f;
-          join.first = (uint32_t)f;
-          join.count = blockIdx.x - (uint32_t)f + 1u;
-          join.q0 = c.t.q0;
-          join.rows = rows;
-          join.row0 = c.t.rb * 16u;
-          join.head = c.t.head;
-        }
-        __syncthreads();
-        bad = false;
-        fresh = true;
-        if (u + 1 < u1) {
-          tile_u += c.t.nb;
-          next_tile<kSel>(a, c);
-        }
-      } else {
-        ++c.blk;
+        __syncwarp();  // every lane has read the block
+        if (lane == 0) mbar_arrive(empty + st);
       }
-    }
-    if (lost) {  // the copies in flight land before the CTA leaves (or their waits give up too)
-      if (lane == 0) set_status(a.g.status, IBP_ETIMEOUT);
-      for (uint32_t i = 0; i < S::kStages; ++i) mbar_wait(full + i, lost_ph ^ (i < lost_st ? 1u : 0u));
+      if (!go) bad = true;
+      // ---- end of the tile, or of this CTA's run: join the four warps
+      float* mw = merge + warp * 16u * (kDP + 4u);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+        l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+        float* row = mw + (r0 + 8u * e) * (kDP + 4u);
+        if (quad == 0) row[kDP] = m[e], row[kDP + 1] = l[e];
+#pragma unroll
+        for (int i = 0; i < 2 * kKs; ++i)
+          *reinterpret_cast<float2*>(row + 8 * i + 2u * quad) =
+              make_float2(o[i][2 * e], o[i][2 * e + 1]);
+      }
+      const bool isbad = any_of_four(bad);
+      Piece<kDP>* piece = pieces + 2u * blockIdx.x + t->place;
+      for (uint32_t r = warp; r < rows; r += kWarps) {
+        float mm[kWarps], mx = -INFINITY, ll = 0.f, ov[kDP / 32];
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w) {
+          mm[w] = merge[(w * 16u + r) * (kDP + 4u) + kDP];
+          mx = fmaxf(mx, mm[w]);
+        }
+        const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+        for (int i = 0; i < kDP / 32; ++i) ov[i] = 0.f;
+#pragma unroll
+        for (uint32_t w = 0; w < kWarps; ++w) {
+          const float* src = merge + (w * 16u + r) * (kDP + 4u);
+          const float f = ex2(mm[w] - base);
+          ll += f * src[kDP + 1];
+#pragma unroll
+          for (int i = 0; i < kDP / 32; ++i) ov[i] = fmaf(f, src[lane + 32u * i], ov[i]);
+        }
+        if (isbad) ll = INFINITY;  // a row that could not be read: zero, here or when joined
+        if (t->whole) {
+          const uint32_t R = row0 + r;
+          const uint64_t at = ((uint64_t)(t->q0 + R / a.G) * a.g.H + t->head) * a.G + R % a.G;
+          store_row<kDP, kBf16>(a, at, lane, ov, mx, ll, isbad);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kDP / 32; ++i) piece->o[r][lane + 32u * i] = ov[i];
+          if (lane == 0) piece->m[r] = mx, piece->l[r] = ll;
+        }
+      }
+      // the sums have been read: the next tile may write its own
+      if (any_of_four(!go || count == 0)) break;
     }
   }
-  if (tid == 0) joins[blockIdx.x] = join;
+  __syncthreads();
+  if (tid == 0 && s_fail) set_status(a.g.status, IBP_ETIMEOUT);
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -620,7 +708,7 @@ cudaError_t launch(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, cud
   if (e != cudaSuccess) return e;
   uint32_t ctas = (uint32_t)sm_count * (kDP == 64 ? 2u : 1u);
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  kern<<<ctas, 128, S::kSmem, st>>>(m.k, m.v, a);
+  kern<<<ctas, kThreads, S::kSmem, st>>>(m.k, m.v, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};

@@ -60,6 +60,41 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// A wait of a whole warp.  One that has run out (about two seconds) sets *fail;
+// the waits that run after it give up at once if what they wait for is not there.
+__device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, uint32_t* fail) {
+  const uint32_t at = smem_addr(bar);
+  if (__all_sync(0xFFFFFFFFu, mbar_try(at, parity))) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (__all_sync(0xFFFFFFFFu, mbar_try(at, parity))) return true;
+    const bool late = global_ns() - t0 > 2000000000ull ||
+                      *reinterpret_cast<volatile uint32_t*>(fail) != 0u;
+    if (__any_sync(0xFFFFFFFFu, late)) {
+      atomicExch(fail, 1u);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// One box of a 4-D tensor map (channel x, token, head, page) into shared memory.
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                              uint32_t x, uint32_t token, uint32_t head,
+                                              int32_t page) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(bar)), "r"(x), "r"(token), "r"(head),
+      "r"(page)
+      : "memory");
+}
+
 // Shared-memory matrix descriptor of a K-major tile written by TMA with the
 // 128-byte swizzle: rows of 128 bytes, 8-row atoms 1024 bytes apart.
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
