@@ -583,7 +583,7 @@ IBP_API ibp_status ibp_paged_scores(const ibp_paged* cache, const ibp_paged_batc
 
 /* The n_selected pages of largest score of each new token and K/V head: the
  * page of the token's own position always, then by score, equal scores by the
- * smaller number, NaN before all; in ascending order, -1 behind the last where
+ * smaller number, NaN as inf; in ascending order, -1 behind the last where
  * fewer pages begin at or before the token's position.
  *   scores    device fp32 [n_tokens, kv_heads, max_pages]
  *   selected  device int32 [n_tokens, kv_heads, n_selected]

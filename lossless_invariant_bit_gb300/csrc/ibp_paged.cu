@@ -8,38 +8,61 @@ namespace ibp {
 namespace {
 
 // ---------------------------------------------------------------- append
-// kLanes lanes hold a head, 8 channels (16 bytes) each: the sum of squares is
-// a shuffle tree over them, and a channel's rotation partner lies rot/2 channels
-// away, a whole number of lanes (rot is a multiple of 16), or in the same lane
-// (adjacent pairs).  A lane keeps its channels over all heads of a token, so the
-// token's place, its row of the rotation table and the norms' weights are fetched
-// once, and kAhead heads are in flight at a time.  Bound by HBM: every byte is
-// read and written once, 16 at a time.
-template <int kLanes, int kAhead, bool kBf16>
+// kLanes lanes hold a head, 8 channels each: 4 and their 4 rotation partners
+// (channels 4 j and rot/2 + 4 j on, or 8 together when pairs are adjacent or past rot),
+// so that a rotation needs no other lane and the sum of squares one shuffle
+// tree.  A lane keeps its channels over all heads of a token, so the token's place,
+// its cosines and sines and the norms' weights are fetched once; kAhead heads are in
+// flight at a time.  Rounds of kSubs heads hold queries, keys or values alone.  Bound
+// by HBM (each byte is read and written once), with issue close behind: 90
+// instructions for the 16 bytes of a lane.
+template <int kLanes, int kAhead, bool kBf16, bool kPairs>
 __global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_t per) {
   constexpr uint32_t kSubs = 128u / kLanes;  // heads side by side
   const uint32_t lane = threadIdx.x & (kLanes - 1u), sub = threadIdx.x / kLanes;
-  const uint32_t heads = a.Hq + 2u * a.g.H;  // queries, keys, values of a token
-  const uint32_t t = blockIdx.x, h0 = blockIdx.y * kSubs * per + sub;
-  const uint32_t h1 = min(heads, (blockIdx.y + 1u) * kSubs * per);
-  const uint32_t c0 = lane * 8u;
-  const bool mine = c0 < a.g.D;
+  const uint32_t t = blockIdx.x;
+  const uint32_t nq = (a.Hq + kSubs - 1u) / kSubs, nk = (a.g.H + kSubs - 1u) / kSubs;
+  const uint32_t r0 = blockIdx.y * per, r1 = min(nq + 2u * nk, r0 + per);
+  // this lane's channels: 4 at c0, 4 at c1
+  const bool mine = lane * 8u < a.g.D;
+  const uint32_t half = a.rot / 2u;
+  const bool split = !kPairs && lane * 8u < a.rot;
+  const uint32_t c0 = split ? lane * 4u : lane * 8u, c1 = split ? half + lane * 4u : c0 + 4u;
+  const bool turned = lane * 8u < a.rot;
   const uint64_t row = a.g.D * 2ull;
-  auto load = [&](uint32_t hh) {
-    const uint8_t* src =
-        hh < a.Hq            ? a.q + t * a.q_stride + hh * row
-        : hh < a.Hq + a.g.H  ? a.kx + t * a.kv_stride + (hh - a.Hq) * row
-                             : a.vx + t * a.kv_stride + (hh - a.Hq - a.g.H) * row;
-    return mine && hh < h1 ? __ldcs(reinterpret_cast<const uint4*>(src + lane * 16u))
-                           : make_uint4(0, 0, 0, 0);
+  // a round's kind (0 queries, 1 keys, 2 values) and this thread's head in it
+  auto place = [&](uint32_t r, uint32_t& kind) {
+    kind = r < nq ? 0u : r < nq + nk ? 1u : 2u;
+    return (kind == 0u ? r : kind == 1u ? r - nq : r - nq - nk) * kSubs + sub;
+  };
+  auto load = [&](uint32_t r) {
+    uint32_t kind;
+    const uint32_t h = place(r, kind);
+    const uint8_t* src = kind == 0u   ? a.q + t * a.q_stride
+                         : kind == 1u ? a.kx + t * a.kv_stride
+                                      : a.vx + t * a.kv_stride;
+    uint4 x = make_uint4(0, 0, 0, 0);
+    if (r < r1 && mine && h < (kind == 0u ? a.Hq : a.g.H)) {
+      src += h * row;
+      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src + c0 * 2u));
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + c1 * 2u));
+      x = make_uint4(u.x, u.y, v.x, v.y);
+    }
+    return x;
   };
   uint4 x[kAhead];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) x[i] = load(h0 + i * kSubs);
+  for (int i = 0; i < kAhead; ++i) x[i] = load(r0 + i);
   // the norms' weights
-  uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-  if (a.q_norm && mine) wq = __ldg(reinterpret_cast<const uint4*>(a.q_norm) + lane);
-  if (a.k_norm && mine) wk = __ldg(reinterpret_cast<const uint4*>(a.k_norm) + lane);
+  uint2 wq[2] = {}, wk[2] = {};
+  if (a.q_norm && mine) {
+    wq[0] = __ldg(reinterpret_cast<const uint2*>(a.q_norm + c0 * 2u));
+    wq[1] = __ldg(reinterpret_cast<const uint2*>(a.q_norm + c1 * 2u));
+  }
+  if (a.k_norm && mine) {
+    wk[0] = __ldg(reinterpret_cast<const uint2*>(a.k_norm + c0 * 2u));
+    wk[1] = __ldg(reinterpret_cast<const uint2*>(a.k_norm + c1 * 2u));
+  }
   // the token's place
   const uint32_t s = paged_find(a.b, t);
   if (s == a.b.n_seqs) return;  // a row of no sequence
@@ -60,68 +83,39 @@ __global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_
     ok = false;
     if (threadIdx.x == 0) set_status(a.g.status, IBP_ERANGE);
   }
-  // this lane's cosines and sines, the sines negated where y = x c - (partner) s
-  const uint32_t half = a.rot / 2u;
-  const bool low = c0 < half;
-  float cc[8], ss[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cc[i] = 1.f, ss[i] = 0.f;
-  if (a.cos_sin && ok && c0 < a.rot) {
-    const float* cs = a.cos_sin + (uint64_t)pos * a.rot;
-    if (a.pairs) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(cs + c0 / 2u));
-      const float4 n = __ldg(reinterpret_cast<const float4*>(cs + half + c0 / 2u));
-      const float c4[4] = {c.x, c.y, c.z, c.w}, n4[4] = {n.x, n.y, n.z, n.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        cc[2 * i] = cc[2 * i + 1] = c4[i];
-        ss[2 * i] = -n4[i];
-        ss[2 * i + 1] = n4[i];
-      }
-    } else {
-      const uint32_t at = low ? c0 : c0 - half;
-      const float4* cp = reinterpret_cast<const float4*>(cs + at);
-      const float4* np = reinterpret_cast<const float4*>(cs + half + at);
-      const float4 ca = __ldg(cp), cb = __ldg(cp + 1), na = __ldg(np), nb = __ldg(np + 1);
-      cc[0] = ca.x, cc[1] = ca.y, cc[2] = ca.z, cc[3] = ca.w;
-      cc[4] = cb.x, cc[5] = cb.y, cc[6] = cb.z, cc[7] = cb.w;
-      ss[0] = na.x, ss[1] = na.y, ss[2] = na.z, ss[3] = na.w;
-      ss[4] = nb.x, ss[5] = nb.y, ss[6] = nb.z, ss[7] = nb.w;
-      if (low)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss[i] = -ss[i];
-    }
+  float4 cc = make_float4(1.f, 1.f, 1.f, 1.f), ss = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.cos_sin && ok && turned) {
+    const float* cs = a.cos_sin + (uint64_t)pos * a.rot + lane * 4u;
+    cc = __ldg(reinterpret_cast<const float4*>(cs));
+    ss = __ldg(reinterpret_cast<const float4*>(cs + half));
   }
-  const uint32_t from = ((threadIdx.x & 31u) & ~(kLanes - 1u)) +
-                        ((low ? lane + half / 8u : lane - half / 8u) & (kLanes - 1u));
-  // every lane of a warp walks the same heads' rounds, so that the shuffles have them all
-  for (uint32_t r = 0; r < per; r += kAhead) {
+  const float inv_d = 1.f / (float)a.g.D;
+  for (uint32_t r = r0; r < r1; r += kAhead) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      if (r + i >= per) break;
-      const uint32_t hh = h0 + (r + i) * kSubs;
-      const uint32_t kind = hh < a.Hq ? 0u : hh < a.Hq + a.g.H ? 1u : 2u;
-      const uint8_t* w = kind == 0u ? a.q_norm : kind == 1u ? a.k_norm : nullptr;
-      const bool turned = a.cos_sin && kind != 2u;
+      if (r + i >= r1) break;
+      uint32_t kind;
+      const uint32_t h = place(r + i, kind);
       uint4 y = x[i];
-      if (r + kAhead + i < per) x[i] = load(hh + kAhead * kSubs);
-      float f[8];
-      {
-        const float2 f0 = unpack2(y.x, kBf16), f1 = unpack2(y.y, kBf16), f2 = unpack2(y.z, kBf16),
-                     f3 = unpack2(y.w, kBf16);
-        f[0] = f0.x, f[1] = f0.y, f[2] = f1.x, f[3] = f1.y;
-        f[4] = f2.x, f[5] = f2.y, f[6] = f3.x, f[7] = f3.y;
-      }
-      if (a.q_norm || a.k_norm) {
-        float sum = 0.f;
+      x[i] = load(r + i + kAhead);
+      const bool normed = kind == 0u ? a.q_norm != nullptr : kind == 1u && a.k_norm;
+      if (kind != 2u && (normed || a.cos_sin)) {  // the same for the whole CTA
+        float f[8];
+        {
+          const float2 f0 = unpack2(y.x, kBf16), f1 = unpack2(y.y, kBf16),
+                       f2 = unpack2(y.z, kBf16), f3 = unpack2(y.w, kBf16);
+          f[0] = f0.x, f[1] = f0.y, f[2] = f1.x, f[3] = f1.y;
+          f[4] = f2.x, f[5] = f2.y, f[6] = f3.x, f[7] = f3.y;
+        }
+        if (normed) {
+          float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum = fmaf(f[k], f[k], sum);
+          for (int k = 0; k < 8; ++k) sum = fmaf(f[k], f[k], sum);
 #pragma unroll
-        for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        if (w) {
-          const float n = rsqrtf(sum / (float)a.g.D + a.eps);
-          const uint4 g = kind == 0u ? wq : wk;
-          const uint32_t gw[4] = {g.x, g.y, g.z, g.w};
+          for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+          const float n = rsqrtf(fmaf(sum, inv_d, a.eps));
+          const uint32_t gw[4] = {kind == 0u ? wq[0].x : wk[0].x, kind == 0u ? wq[0].y : wk[0].y,
+                                  kind == 0u ? wq[1].x : wk[1].x, kind == 0u ? wq[1].y : wk[1].y};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float2 gf = unpack2(gw[k], kBf16);
@@ -129,27 +123,28 @@ __global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_
             f[2 * k + 1] *= n * gf.y;
           }
         }
-      }
-      if (a.cos_sin) {
-        float p[8];
+        if (turned) {
+          const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          p[k] = a.pairs ? f[k ^ 1] : __shfl_sync(0xFFFFFFFFu, f[k], from);
-        if (turned && c0 < a.rot)
-#pragma unroll
-          for (int k = 0; k < 8; ++k) f[k] = f[k] * cc[k] + p[k] * ss[k];
-      }
-      if (w || turned)
+          for (int k = 0; k < 4; ++k) {
+            float& u = f[kPairs ? 2 * k : k];
+            float& v = f[kPairs ? 2 * k + 1 : k + 4];
+            const float u0 = u, v0 = v;
+            u = u0 * c4[k] - v0 * s4[k];
+            v = v0 * c4[k] + u0 * s4[k];
+          }
+        }
         y = make_uint4(pack2(f[0], f[1], kBf16), pack2(f[2], f[3], kBf16),
                        pack2(f[4], f[5], kBf16), pack2(f[6], f[7], kBf16));
-      if (hh < h1 && mine) {
-        if (kind == 0u) {
-          if (!ok) y = make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(a.q_out + t * a.qo_stride + hh * row + lane * 16u) = y;
-        } else if (kd) {
-          uint8_t* d = kind == 1u ? kd + (hh - a.Hq) * a.g.head_stride
-                                  : vd + (hh - a.Hq - a.g.H) * a.g.head_stride;
-          *reinterpret_cast<uint4*>(d + lane * 16u) = y;
+      }
+      if (mine && h < (kind == 0u ? a.Hq : a.g.H)) {
+        uint8_t* d = kind == 0u   ? a.q_out + t * a.qo_stride + h * row
+                     : kind == 1u ? kd + h * a.g.head_stride
+                                  : vd + h * a.g.head_stride;
+        if (kind == 0u && !ok) y = make_uint4(0, 0, 0, 0);
+        if (kind == 0u || ok) {
+          *reinterpret_cast<uint2*>(d + c0 * 2u) = make_uint2(y.x, y.y);
+          *reinterpret_cast<uint2*>(d + c1 * 2u) = make_uint2(y.z, y.w);
         }
       }
     }
@@ -372,12 +367,9 @@ __global__ void __launch_bounds__(128, 3)
 }
 
 // ---------------------------------------------------------------- select
-// Scores become whole numbers of the same order (the sign bit folded in, NaN above
-// all, -0 as 0); the token's own page is taken whatever its score, and of the
-// others those above the threshold, the largest number that at least n_sel - 1 of
-// them reach, then the first of those equal to it.
+// Scores as whole numbers of the same order: the sign bit folded in, -0 as 0, NaN as inf.
 __device__ __forceinline__ uint32_t order_key(float f) {
-  if (f != f) return 0xFFFFFFFEu;
+  if (f != f) f = INFINITY;
   const uint32_t u = __float_as_uint(f + 0.f);  // -0 + 0 is 0
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
@@ -392,11 +384,14 @@ __device__ __forceinline__ uint32_t select_row(const PagedGeom& g, const PagedBa
   return !q.ok || pos < 0 ? 0u : own + 1u;
 }
 
-// kWarps warps to a row, its keys in their registers (kPer each; a warp has a run of
-// numbers).  The threshold is bracketed, from the smallest and the largest key on, by
-// counts of the keys that reach a candidate between, placed by the counts at the
-// bracket's ends, until as many reach it as are wanted.  Bound by issue: 2 kPer
-// instructions a count.  4 rows to a CTA when kWarps is 1.
+// kWarps warps to a row, its scores in their registers (kPer each; a warp has a run of
+// numbers), the own page's as +inf.  A threshold that n_sel of them reach is bracketed
+// by counts, placed between the bracket's ends as if the count fell off
+// exponentially there (tails do), every third time in the middle: 6 to 8 counts for
+// 1000 normal scores.  Where no such threshold lies between two scores (equal ones,
+// infinities) the n_sel-th largest is found bit by bit, and of those equal to it the
+// first are taken.  Bound by issue: 2 kPer instructions a count, 9 kPer to write the
+// numbers.  4 rows to a CTA when kWarps is 1.
 template <int kWarps, int kPer>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32)
     k_paged_pick(PagedGeom g, PagedBatchView b, const float* scores, uint32_t n_sel,
@@ -409,14 +404,11 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32)
   const uint32_t part = kWarps == 1 ? 0u : warp;
   const uint32_t t = (uint32_t)(row / g.H);
   int32_t* out = selected + row * n_sel;
-  const uint32_t i0 = part * (32u * kPer);
-  const float* src = scores + row * b.max_pages;
-  float f[kPer];  // fetched before the row's length is known
+  const uint32_t i0 = part * (32u * kPer) + lane;  // number of this lane's first score
+  const float* src = scores + row * b.max_pages + i0;
+  float v[kPer];  // fetched before the row's length is known
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const uint32_t i = i0 + 32u * j + lane;
-    f[j] = i < b.max_pages ? __ldg(src + i) : 0.f;
-  }
+  for (int j = 0; j < kPer; ++j) v[j] = i0 + 32u * j < b.max_pages ? __ldcs(src + 32u * j) : 0.f;
   const uint32_t s = paged_find(b, t);
   if (s == b.n_seqs) return;
   uint32_t own;
@@ -427,11 +419,13 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32)
     return;
   }
   uint32_t phase = 0;
-  // the sums of two values over the row
-  auto sum2 = [&](uint32_t x, uint32_t y, uint32_t* below) {
+  // the sum over the row; below: those of the warps before this one, of two values
+  auto sum = [&](uint32_t x, uint32_t y, uint32_t* below) {
     x = __reduce_add_sync(0xFFFFFFFFu, x);
-    if (below) y = __reduce_add_sync(0xFFFFFFFFu, y);
-    if (below) below[0] = below[1] = 0;
+    if (below) {
+      y = __reduce_add_sync(0xFFFFFFFFu, y);
+      below[0] = below[1] = 0;
+    }
     if (kWarps > 1) {
       if (lane == 0) s_sum[phase][part][0] = x, s_sum[phase][part][1] = y;
       __syncthreads();
@@ -445,61 +439,86 @@ __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32)
     }
     return x;
   };
-  uint32_t key[kPer], lo = 0xFFFFFFFFu, hi = 0;
+  float lo = INFINITY, hi = -INFINITY;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const uint32_t i = i0 + 32u * j + lane;
-    key[j] = i < n && i != own ? order_key(f[j]) : 0u;  // a score's key is above 0
-    if (key[j]) lo = min(lo, key[j]), hi = max(hi, key[j]);
+    const uint32_t i = i0 + 32u * j;
+    if (i == own || v[j] != v[j]) v[j] = INFINITY;
+    lo = i < n ? fminf(lo, v[j]) : lo;
+    hi = i < n && i != own ? fmaxf(hi, v[j]) : hi;
+    if (i >= n) v[j] = -INFINITY;
   }
-  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+  uint32_t klo = __reduce_min_sync(0xFFFFFFFFu, order_key(lo));
+  uint32_t khi = __reduce_max_sync(0xFFFFFFFFu, order_key(hi));
   if (kWarps > 1) {
-    if (lane == 0) s_sum[1][part][0] = lo, s_sum[1][part][1] = hi;
+    if (lane == 0) s_sum[1][part][0] = klo, s_sum[1][part][1] = khi;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
-      lo = min(lo, s_sum[1][w][0]), hi = max(hi, s_sum[1][w][1]);
+      klo = min(klo, s_sum[1][w][0]), khi = max(khi, s_sum[1][w][1]);
   }
-  const uint32_t want = n_sel - 1u;
-  // lo is reached by `clo` keys, at least the wanted; hi by `chi`, too few
-  uint32_t thr = lo, clo = n - 1u, chi = 0;
-  if (want) {
-    uint64_t top = (uint64_t)hi + 1u;
-    for (uint32_t k = 0; top - thr > 1u && clo != want; ++k) {
-      const uint32_t gap = (uint32_t)(top - thr);
-      // where the count would be met if the keys between lay evenly; every third time the middle
-      float part = (float)(clo - want) / (float)(clo - chi);
-      if (k % 3u == 2u) part = 0.5f;
-      uint32_t step = (uint32_t)((float)gap * part);
-      step = step < 1u ? 1u : step > gap - 1u ? gap - 1u : step;
-      const uint32_t cand = thr + step;
-      uint32_t c = 0;
+  // a is reached by `clo` scores, at least n_sel; z, at least the largest but the own, by the
+  // own and no other, or by `chi`, too few
+  auto score = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); };
+  float a = score(klo), z = score(khi);
+  uint32_t clo = n, chi = 1;
+  if (n_sel == 1u) a = INFINITY, clo = z < INFINITY ? 1u : 2u;  // the own page, if no other is inf
+  for (int k = 0; clo != n_sel && a > -INFINITY && z < INFINITY; ++k) {
+    const float part_of = k % 3 == 2 ? 0.5f
+                                     : __fdividef(__log2f((float)clo) - __log2f((float)n_sel),
+                                                  __log2f((float)clo) - __log2f((float)chi));
+    float c = fmaf(z - a, part_of, a);
+    if (!(c > a && c < z)) c = a + 0.5f * (z - a);
+    if (!(c > a && c < z) || k == 32) break;  // neighbours, or no end: bit by bit
+    uint32_t m = 0;
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) c += key[j] >= cand;
-      c = sum2(c, 0, nullptr);
-      if (c >= want)
-        thr = cand, clo = c;
-      else
-        top = cand, chi = c;
-    }
+    for (int j = 0; j < kPer; ++j) m += v[j] >= c;
+    m = sum(m, 0, nullptr);
+    if (m >= n_sel)
+      a = c, clo = m;
+    else
+      z = c, chi = m;
   }
-  uint32_t above = 0, equal = 0, below[2];
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) above += key[j] > thr, equal += key[j] == thr;
-  const uint32_t all = sum2(above, equal, below);
-  // equal ones to take: none when only the own page is wanted
-  const uint32_t eq_want = want ? want - all : 0u;
-  uint32_t na = want ? below[0] : 0u, ne = below[1];
   const uint32_t lt = (1u << lane) - 1u;
+  uint32_t below[2];
+  if (clo == n_sel && a > -INFINITY) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) m += v[j] >= a;
+    if (kWarps > 1) sum(m, 0, below);
+    int32_t* to = out + (kWarps > 1 ? below[0] : 0u);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t w = __ballot_sync(0xFFFFFFFFu, v[j] >= a);
+      if (v[j] >= a) to[__popc(w & lt)] = (int32_t)(i0 + 32u * j);
+      to += __popc(w);
+    }
+    return;
+  }
+  // keys: 0 past the row's end, the own page's above all
+  auto key = [&](int j) {
+    const uint32_t i = i0 + 32u * j;
+    return i == own ? 0xFFFFFFFFu : i < n ? order_key(v[j]) : 0u;
+  };
+  uint32_t thr = 0;
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t cand = thr | 1u << bit;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) m += key(j) >= cand;
+    if (sum(m, 0, nullptr) >= n_sel) thr = cand;
+  }
+  uint32_t above = 0, equal = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) above += key(j) > thr, equal += key(j) == thr;
+  const uint32_t want = n_sel - sum(above, equal, below);  // of the equal ones
+  uint32_t na = below[0], ne = below[1];
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
-    const uint32_t i = i0 + 32u * j + lane;
-    const bool up = want && key[j] > thr, eq = key[j] == thr && key[j];
+    const bool up = key(j) > thr, eq = key(j) == thr;
     const uint32_t bu = __ballot_sync(0xFFFFFFFFu, up), be = __ballot_sync(0xFFFFFFFFu, eq);
-    const uint32_t a = na + __popc(bu & lt), e = ne + __popc(be & lt);
-    const uint32_t at = a + min(e, eq_want) + (i > own ? 1u : 0u);
-    if (i == own || up || (eq && e < eq_want)) out[at] = (int32_t)i;
+    const uint32_t e = ne + __popc(be & lt);
+    if (up || (eq && e < want)) out[na + __popc(bu & lt) + min(e, want)] = (int32_t)(i0 + 32u * j);
     na += __popc(bu);
     ne += __popc(be);
   }
@@ -607,20 +626,25 @@ uint32_t pow2_lanes(uint32_t D) { return D <= 32u ? 4u : D <= 64u ? 8u : 16u; }
 cudaError_t launch_paged_append(const PagedAppendArgs& a, int sm_count, cudaStream_t st) {
   const uint32_t D_ = a.g.D;
   const bool bf_ = a.g.bf16 != 0u;
-  // Heads that a lane goes over: 8 at most, all in flight while the token's place is
-  // looked up, and no more than leave eight CTAs to each SM.
-  const uint64_t subs = 128u / pow2_lanes(D_), heads = a.Hq + 2ull * a.g.H;
-  const uint64_t rounds = (heads + subs - 1) / subs;
-  uint64_t per = rounds * a.b.n_tokens / (8ull * sm_count);
-  per = per < 1u ? 1u : per > 8u ? 8u : per;
-  uint64_t y = (rounds + per - 1) / per;
+  // Rounds of a CTA: as many as leave 16 CTAs to each SM (a token's place is then looked up
+  // for more heads), 16 at most.
+  const uint64_t subs = 128u / pow2_lanes(D_);
+  const uint64_t rounds = (a.Hq + subs - 1) / subs + 2u * ((a.g.H + subs - 1) / subs);
+  uint64_t per = rounds * a.b.n_tokens / (16ull * sm_count);
+  per = per < 1u ? 1u : per > 16u ? 16u : per;
+  const uint64_t y = (rounds + per - 1) / per;
   per = (rounds + y - 1) / y;
   if (y > 65535u) return cudaErrorInvalidValue;
   const dim3 grid(a.b.n_tokens, (unsigned)y);
-#define IBP_CALL(L, B)                                                            \
-  do {                                                                            \
-    if (per >= 2u) k_paged_append<L, 8, B><<<grid, 128, 0, st>>>(a, (uint32_t)per); \
-    else k_paged_append<L, 1, B><<<grid, 128, 0, st>>>(a, (uint32_t)per);         \
+#define IBP_CALL(L, B)                                                                    \
+  do {                                                                                    \
+    if (per >= 2u) {                                                                      \
+      if (a.pairs) k_paged_append<L, 4, B, true><<<grid, 128, 0, st>>>(a, (uint32_t)per); \
+      else k_paged_append<L, 4, B, false><<<grid, 128, 0, st>>>(a, (uint32_t)per);        \
+    } else {                                                                              \
+      if (a.pairs) k_paged_append<L, 1, B, true><<<grid, 128, 0, st>>>(a, (uint32_t)per); \
+      else k_paged_append<L, 1, B, false><<<grid, 128, 0, st>>>(a, (uint32_t)per);        \
+    }                                                                                     \
   } while (0)
   IBP_PAGED_LANES(IBP_CALL);
 #undef IBP_CALL

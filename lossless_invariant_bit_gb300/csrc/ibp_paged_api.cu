@@ -123,8 +123,9 @@ ibp_status stride_ok(uint64_t stride, uint64_t heads, uint32_t D) {
 extern "C" {
 
 ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
-  if (!out || !d || !d->k || !d->v) return IBP_EINVAL;
+  if (!out) return IBP_EINVAL;
   *out = nullptr;
+  if (!d || !d->k || !d->v) return IBP_EINVAL;
   if (d->page_tokens < 8u || d->page_tokens > 256u || (d->page_tokens & (d->page_tokens - 1u)) ||
       d->head_dim == 0 || d->head_dim % 16u || d->head_dim > IBP_PAGED_MAX_HEAD_DIM ||
       d->kv_heads == 0 || d->kv_heads > 4096u || d->n_pages == 0 || d->n_pages > 0x7FFFFFFFu ||
