@@ -154,13 +154,13 @@ struct Info {
   uint32_t s;             // sequence
   uint32_t all_lo, all_hi;  // keys that every row sees
 };
-// A block in which some rows see keys that others do not, and some of those keys'
-// values are infinite or NaN: bit per key.  A tile's rows span at most 256 positions,
-// so 3 blocks at either end of what they see, and a slot has that many at most.
-struct Odd {
-  uint32_t key0, keys[4];
-};
+// The blocks of a tile in which some rows see keys that others do not, and some of those
+// keys' values are infinite or NaN: bit per key.  A tile's rows span at most 256
+// positions, so there are at most 3 such blocks at either end of what they see.
 constexpr uint32_t kOdd = 8;
+struct Odd {
+  uint32_t count, key0[kOdd], keys[kOdd][4];
+};
 constexpr uint32_t kInfos = 8;
 // Keys whose weights are computed before the first half of them is handed over: what
 // waits for the first half's store is then hidden (64 to 112 measured alike).
@@ -180,9 +180,10 @@ __device__ __forceinline__ bool walk(const PagedAttnArgs& a, Walk& w) {
   return true;
 }
 
-// The matrix instructions of a block, issued by the lane with `on` set while the
-// whole warp walks the same path (descriptors stay uniform values), as one run
-// of code: what lies between two of them counts, each works for 64 cycles only.
+// The matrix instructions of a block, as one run of code: the whole warp comes here
+// and elect.sync names the lane that issues.  (With a lane of one's own choosing the
+// compiler cannot tell that one lane issues, and each instruction took 60 to 130 cycles to
+// issue, as long as it works.)
 #define IBP_MMA_SS(inc)                                                         \
   " add.s64 a, a, " inc ";\n add.s64 b, b, " inc ";\n"                          \
   " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n"
@@ -192,48 +193,47 @@ __device__ __forceinline__ bool walk(const PagedAttnArgs& a, Walk& w) {
 
 // S = Q K^T over 64 channels: low descriptor words of both, their common high word;
 // accumulates from the start when `acc` is set.
-__device__ __forceinline__ void mma_qk(uint32_t on, uint32_t tmem, uint32_t qlo, uint32_t klo,
+__device__ __forceinline__ void mma_qk(uint32_t tmem, uint32_t qlo, uint32_t klo,
                                        uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, q, e;\n .reg .b64 a, b;\n setp.ne.b32 e, %5, 0;\n"
-      " setp.ne.b32 q, %6, 0;\n setp.eq.b32 p, 0, 0;\n"
+      "{\n .reg .pred p, q, e;\n .reg .b64 a, b;\n elect.sync _|e, 0xFFFFFFFF;\n"
+      " setp.ne.b32 q, %5, 0;\n setp.eq.b32 p, 0, 0;\n"
       " mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, q;\n" IBP_MMA_SS("2")
           IBP_MMA_SS("2") IBP_MMA_SS("2") "}\n" ::"r"(tmem),
-      "r"(qlo), "r"(klo), "r"(hi), "r"(idesc), "r"(on), "r"(acc)
+      "r"(qlo), "r"(klo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
 // One step of it, for the head sizes between.
-__device__ __forceinline__ void mma_qk_step(uint32_t on, uint32_t tmem, uint32_t qlo,
+__device__ __forceinline__ void mma_qk_step(uint32_t tmem, uint32_t qlo,
                                             uint32_t klo, uint32_t hi, uint32_t idesc,
                                             uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 e, %5, 0;\n"
-      " setp.ne.b32 p, %6, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n elect.sync _|e, 0xFFFFFFFF;\n"
+      " setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(tmem),
-      "r"(qlo), "r"(klo), "r"(hi), "r"(idesc), "r"(on), "r"(acc)
+      "r"(qlo), "r"(klo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
 // O (+)= P V over 64 keys, P in tensor memory; accumulates from the start when `acc` is set.
-__device__ __forceinline__ void mma_pv(uint32_t on, uint32_t tmem, uint32_t p, uint32_t vlo,
+__device__ __forceinline__ void mma_pv(uint32_t tmem, uint32_t p, uint32_t vlo,
                                        uint32_t hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p, q, e;\n .reg .b64 b;\n .reg .b32 c;\n setp.ne.b32 e, %5, 0;\n"
-      " setp.ne.b32 q, %6, 0;\n setp.eq.b32 p, 0, 0;\n mov.b64 b, {%2, %3};\n"
+      "{\n .reg .pred p, q, e;\n .reg .b64 b;\n .reg .b32 c;\n elect.sync _|e, 0xFFFFFFFF;\n"
+      " setp.ne.b32 q, %5, 0;\n setp.eq.b32 p, 0, 0;\n mov.b64 b, {%2, %3};\n"
       " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, q;\n" IBP_MMA_TS("8")
           IBP_MMA_TS("16") IBP_MMA_TS("24") "}\n" ::"r"(tmem),
-      "r"(p), "r"(vlo), "r"(hi), "r"(idesc), "r"(on), "r"(acc)
+      "r"(p), "r"(vlo), "r"(hi), "r"(idesc), "r"(acc)
       : "memory");
 }
 
-__device__ __forceinline__ void commit(uint32_t on, uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar) {
   asm volatile(
-      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      "{\n .reg .pred e;\n elect.sync _|e, 0xFFFFFFFF;\n"
       " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
-          smem_addr(bar)),
-      "r"(on)
+          smem_addr(bar))
       : "memory");
 }
 
@@ -342,15 +342,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = turn + 2;       // the tile's queries are there
   uint64_t* o_full = q_full + 1;     // every product of the tile is done
   uint64_t* done = o_full + 1;       // per slot, after a failure: its products are done
-  uint64_t* looked = done + 2;       // per slot: its warps have searched a block's values
-  uint64_t* ended = looked + 2;      // both slots' warps have ended the tile
+  uint64_t* ended = done + 2;        // both slots' warps have ended the tile
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(ended + 1);
   uint32_t* s_fail = s_tmem + 1;
   uint32_t* s_bad = s_fail + 1;      // 8 blocks: bit per page with an id out of range
   __shared__ Info s_info[kInfos];
   __shared__ uint64_t info_full[kInfos];
-  __shared__ uint32_t s_nan[8][4];   // 8 blocks: bit per key with such values
-  __shared__ Odd s_odd[2][kOdd];     // per slot, those of the tile
+  __shared__ Odd s_odd[2];  // of this tile and the next
   __shared__ uint64_t s_scan[kThreads / 32];
   __shared__ uint64_t s_found[3];
 
@@ -371,7 +369,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(p2_full + i, 4);
       mbar_init(turn + i, 1);
       mbar_init(done + i, 1);
-      mbar_init(looked + i, 4);
     }
     for (uint32_t i = 0; i < kInfos; ++i) mbar_init(info_full + i, 1);
     mbar_init(q_full, 8);
@@ -534,10 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (round > 0) go = wait_or_fail(empty + st, (round - 1u) & 1u, s_fail);
           if (!go) break;
           if (lane == 0) {
-            if (kv == 0) {
-              s_bad[blocks & 7u] = bad;
-              for (int k = 0; k < 4; ++k) s_nan[blocks & 7u][k] = 0;
-            }
+            if (kv == 0) s_bad[blocks & 7u] = bad;
             mbar_expect_tx(full + st, bytes);
           }
           __syncwarp();
@@ -559,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 9 || warp == 10) {
     reg_dec();
     // ---------------- a slot's matrix products
-    const uint32_t on = lane == 0 ? 1u : 0u, slot = warp - 9u;
+    const uint32_t slot = warp - 9u;
     {
       const uint32_t base_desc = (1u << 4) | ((uint32_t)kBf16 << 7) | ((uint32_t)kBf16 << 10) |
                                  ((kRows >> 4) << 24);
@@ -578,24 +572,29 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool go = true;
       // S = Q K^T; the other slot's turn begins with the last of it, since a turn takes
       // as long to pass on as two products to run
-      auto qk = [&](uint32_t qslot, uint32_t e, bool pass) {
+      auto release = [&](uint32_t e, bool twice) {  // once its products are done; twice: for both slots
+        commit(empty + e % kRing);
+        if (twice) commit(empty + e % kRing);
+      };
+      auto qk = [&](uint32_t qslot, uint32_t e, bool two, bool pass) {
         const uint32_t qa = q_lo + qslot * (S::kTile >> 4);
         const uint32_t ka = kv_lo + (e % kRing) * (S::kTile >> 4);
         if (k_steps == kDP / 16u) {
-          if (kDP == 128) mma_qk(on, ts, qa, ka, desc_hi, qk_desc, 0u);
+          if (kDP == 128) mma_qk(ts, qa, ka, desc_hi, qk_desc, 0u);
           if (pass && lane == 0) mbar_arrive(turn + (slot ^ 1u));
           __syncwarp();
           constexpr uint32_t kOff = kDP == 128 ? S::kHalf >> 4 : 0u;
-          mma_qk(on, ts, qa + kOff, ka + kOff, desc_hi, qk_desc, kDP == 128 ? 1u : 0u);
+          mma_qk(ts, qa + kOff, ka + kOff, desc_hi, qk_desc, kDP == 128 ? 1u : 0u);
         } else {
           for (uint32_t k = 0; k < k_steps; ++k) {
             const uint32_t off = (k >> 2) * (S::kHalf >> 4) + 2u * (k & 3u);
-            mma_qk_step(on, ts, qa + off, ka + off, desc_hi, qk_desc, k ? 1u : 0u);
+            mma_qk_step(ts, qa + off, ka + off, desc_hi, qk_desc, k ? 1u : 0u);
           }
           if (pass && lane == 0) mbar_arrive(turn + (slot ^ 1u));
           __syncwarp();
         }
-        commit(on, s_full + slot);
+        commit(s_full + slot);
+        release(e, two);
       };
       while (go) {
         const Info* x = info_of(tiles);
@@ -610,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ek = e0 + 2u * i;
           go = wait_or_fail(full + ek % kRing, (ek / kRing) & 1u, s_fail);
           tc_after();
-          if (go) qk(qslot, ek, false);
+          if (go) qk(qslot, ek, two, false);
         }
         // The slots take turns, so that one's products run while the other's weights are
         // computed (left alone they fall into step, and both wait for both).
@@ -624,43 +623,114 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_after();
           if (!go) break;
           if (i < nb) {
-            mma_pv(on, to, ts, va, desc_hi, pv_desc, b ? 1u : 0u);
+            mma_pv(to, ts, va, desc_hi, pv_desc, b ? 1u : 0u);
             go = wait_or_fail(p2_full + slot, parity, s_fail);
             tc_after();
             if (!go) break;
-            mma_pv(on, to, ts + 32u, va + 512u, desc_hi, pv_desc, 1u);
+            mma_pv(to, ts + 32u, va + 512u, desc_hi, pv_desc, 1u);
+            release(ev, two);
             ++pn;
           }
           if (i + step < nb) {
-            qk(qslot, ek, true);
+            qk(qslot, ek, two, true);
           } else {
             if (lane == 0) mbar_arrive(turn + (slot ^ 1u));
             __syncwarp();
           }
         }
-        commit(on, o_full);
+        commit(o_full);
         e0 += 2u * nb;
         ++tiles;
       }
       if (!go) {  // products in flight finish before the tensor memory goes
-        commit(on, done + slot);
+        commit(done + slot);
         mbar_wait(done + slot, 0);
       }
     }
   } else if (warp == 11) {
     reg_dec();
     // ---------------- keys and values are there: one arrival with each block's weights
-    uint32_t e0 = 0, tiles = 0, pn[2] = {0, 0};
+    uint32_t e0 = 0, tiles = 0, blocks = 0, pn[2] = {0, 0};
     bool go = true;
+    const uint32_t box_lg = a.g.page_lg < 7u ? a.g.page_lg : 7u;
     auto entry = [&](uint32_t e) {
       go = go && wait_or_fail(full + e % kRing, (e / kRing) & 1u, s_fail);
     };
     while (go) {
+      Odd* odd = s_odd + (tiles & 1u);
       const Info* t = info_of(tiles++);
       if (!t) break;
       const uint32_t nb = t->count, two = t->two, step = two ? 2u : 1u;
-      for (uint32_t i = 0; i < nb && go; ++i) {
-        entry(e0 + 2u * i + 1u);                         // these values
+      const int32_t lo = (int32_t)t->lo, hi = (int32_t)t->hi;
+      const int32_t every_lo = (int32_t)t->all_lo, every_hi = (int32_t)t->all_hi;
+      uint32_t n_odd = 0;
+      if (lane == 0) odd->count = 0;
+      for (uint32_t i = 0; i < nb && go; ++i, ++blocks) {
+        const uint32_t ev = e0 + 2u * i + 1u;
+        entry(ev);  // these values
+        if (!go) break;
+        // Values that no row sees become zero, so that 0 * (what they hold) is 0.  Where only
+        // some rows see a key, infinities and NaN of its values become zero too, and are
+        // added to the rows that see them at the tile's end.
+        const int32_t key0 = (int32_t)(t->key0 + i * kKeys);
+        const uint32_t badp = s_bad[blocks & 7u];
+        const bool mixed = key0 + (int32_t)kKeys > every_hi || key0 < every_lo;
+        if (mixed || badp || key0 + (int32_t)kKeys > hi || key0 < lo) {
+          uint32_t found[4];
+#pragma unroll
+          for (uint32_t g = 0; g < 4; ++g) {
+            const uint32_t row = 32u * g + lane;  // this thread's key
+            const int32_t key = key0 + (int32_t)row;
+            const uint32_t va = smem_addr(s_kv + (ev % kRing) * S::kTile) + row * 128u;
+            // an exponent of ones, plus one, reaches the sign's place
+            constexpr uint32_t kExp = kBf16 ? 0x7F807F80u : 0x7C007C00u;
+            constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
+            auto chunk = [&](uint32_t x) {
+              return va + (x >> 3) * S::kHalf + (((x & 7u) ^ (lane & 7u)) << 4);
+            };
+            uint32_t hit = 0;
+            if (key >= hi || key < lo || (badp >> (row >> box_lg) & 1u)) {
+#pragma unroll 4
+              for (uint32_t x = 0; x < S::kHalves * 8u; ++x)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(chunk(x)), "r"(0u)
+                             : "memory");
+            } else if (mixed) {
+#pragma unroll 4
+              for (uint32_t x = 0; x < S::kHalves * 8u; ++x) {
+                uint32_t y[4];
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
+                             : "r"(chunk(x))
+                             : "memory");
+#pragma unroll
+                for (int k = 0; k < 4; ++k) hit |= (y[k] & kExp) + kOne;
+              }
+              hit &= 0x80008000u;
+              if (hit)
+#pragma unroll 1
+                for (uint32_t x = 0; x < S::kHalves * 32u; ++x) {
+                  const uint32_t at = chunk(x >> 2) + 4u * (x & 3u);
+                  uint32_t y;
+                  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(at) : "memory");
+                  const uint32_t ones = (y & kExp) + kOne;  // a half's top bit
+                  if (ones & 0x8000u) y &= 0xFFFF0000u;
+                  if (ones & 0x80000000u) y &= 0x0000FFFFu;
+                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(y) : "memory");
+                }
+            }
+            found[g] = __ballot_sync(0xFFFFFFFFu, hit != 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if ((found[0] | found[1] | found[2] | found[3]) && n_odd < kOdd) {
+            if (lane == 0) {
+              odd->key0[n_odd] = (uint32_t)key0;
+              for (int g = 0; g < 4; ++g) odd->keys[n_odd][g] = found[g];
+              odd->count = n_odd + 1u;
+            }
+            ++n_odd;
+          }
+        }
         if (i + step < nb) entry(e0 + 2u * (i + step));  // the slot's next keys
         if (!go) break;
         const uint32_t s0 = two ? i & 1u : 0u, s1 = two ? s0 : 1u;
@@ -713,19 +783,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
     };
-    // this slot is done with an entry of the ring, or (twice) both are
-    auto release = [&](uint32_t e, bool twice) {
-      mbar_arrive(empty + e % kRing);
-      if (twice) mbar_arrive(empty + e % kRing);
-    };
     // Infinities and NaN of the values of the block's odd keys that this row sees, into
     // 32 channels of its sums: rare, and read again from the pages.
-    auto add_odd = [&](const Info* t, const Odd& b, uint32_t x, int32_t from, int32_t to,
-                       uint32_t (&o)[32]) {
+    auto add_odd = [&](const Info* t, uint32_t key0, const uint32_t (&keys)[4], uint32_t x,
+                       int32_t from, int32_t to, uint32_t (&o)[32]) {
 #pragma unroll 1
       for (uint32_t j = 0; j < kKeys; ++j) {
-        const int32_t key = (int32_t)(b.key0 + j);
-        if (!(b.keys[j >> 5] >> (j & 31u) & 1u) || key < from || key >= to) continue;
+        const int32_t key = (int32_t)(key0 + j);
+        if (!(keys[j >> 5] >> (j & 31u) & 1u) || key < from || key >= to) continue;
         const int32_t page =
             __ldg(a.b.table + t->s * a.b.table_stride + ((uint32_t)key >> a.g.page_lg));
         const uint16_t* v = reinterpret_cast<const uint16_t*>(
@@ -739,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       }
     };
-    uint32_t sn = 0, tiles = 0, blocks = 0, e0 = 0, looks = 0;
+    uint32_t sn = 0, tiles = 0, blocks = 0, e0 = 0;
     bool go = true;
     while (go) {
       const Info* t = info_of(tiles);
@@ -760,9 +825,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         from_key = a.window && pos + 1 > (int32_t)a.window ? pos + 1 - (int32_t)a.window : 0;
       }
       int32_t key0 = (int32_t)t->key0;
-      const int32_t lo_key = (int32_t)t->lo, hi_key = (int32_t)t->hi;
-      const int32_t every_lo = (int32_t)t->all_lo, every_hi = (int32_t)t->all_hi;
-      uint32_t odd = 0;  // entries of s_odd
       // keys that every row of the warp sees need no mask
       const int32_t all_to = __reduce_min_sync(0xFFFFFFFFu, live ? to_key : 0x7FFFFFFF);
       const int32_t all_from = __reduce_max_sync(0xFFFFFFFFu, live ? from_key : 0);
@@ -779,80 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32<32>(ts + 32u, sv);
         tmem_ld32<64>(ts + 64u, sv);
         tmem_ld32<96>(ts + 96u, sv);
-        // these keys have been read, and with the product before them the values before
-        if (wq == 0 && lane == 0) {
-          release(e0 + 2u * i, both);
-          if (any) release(e0 + 2u * (i - (both ? 2u : 1u)) + 1u, both);
-        }
         const uint32_t badp = s_bad[(blocks + i) & 7u];
-        const bool edge = key0 + (int32_t)kKeys > hi_key || key0 < lo_key || badp;
-        const bool mixed = key0 + (int32_t)kKeys > every_hi || key0 < every_lo;
-        if (edge || mixed) {
-          // Values that no row sees become zero, so that 0 * (what they hold) is 0.  Where
-          // only some rows see a key, infinities and NaN of its values become zero too and
-          // are added to the rows that see them at the tile's end.
-          const uint32_t ev = e0 + 2u * i + 1u;
-          go = wait_or_fail(full + ev % kRing, (ev / kRing) & 1u, s_fail);
-          const int32_t key = key0 + (int32_t)r;  // this thread's key
-          const bool none = key >= hi_key || key < lo_key || (badp >> (r >> box_lg) & 1u);
-          const uint32_t va = smem_addr(s_kv + (ev % kRing) * S::kTile) + r * 128u;
-          if (go && none) {
-#pragma unroll
-            for (uint32_t x = 0; x < S::kHalves * 8u; ++x)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                               va + (x >> 3) * S::kHalf + (x & 7u) * 16u),
-                           "r"(0u)
-                           : "memory");
-          } else if (go && mixed) {
-            // an exponent of ones, plus one, reaches the sign's place
-            constexpr uint32_t kExp = kBf16 ? 0x7F807F80u : 0x7C007C00u;
-            constexpr uint32_t kOne = kBf16 ? 0x00800080u : 0x04000400u;
-            auto chunk = [&](uint32_t x) {
-              return va + (x >> 3) * S::kHalf + (((x & 7u) ^ (r & 7u)) << 4);
-            };
-            uint32_t hit = 0;
-#pragma unroll 8
-            for (uint32_t x = 0; x < S::kHalves * 8u; ++x) {
-              uint32_t y[4];
-              asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3])
-                           : "r"(chunk(x))
-                           : "memory");
-#pragma unroll
-              for (int k = 0; k < 4; ++k) hit |= (y[k] & kExp) + kOne;
-            }
-            if (hit & 0x80008000u) {  // noted before they are cleared: the other slot may look next
-              atomicOr(&s_nan[(blocks + i) & 7u][r >> 5], 1u << (r & 31u));
-              __threadfence_block();
-#pragma unroll 1
-              for (uint32_t x = 0; x < S::kHalves * 32u; ++x) {
-                const uint32_t at = chunk(x >> 2) + 4u * (x & 3u);
-                uint32_t y;
-                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(at) : "memory");
-                const uint32_t ones = ((y & kExp) + kOne) & 0x80008000u;  // a half's top bit
-                if (ones & 0x8000u) y &= 0xFFFF0000u;
-                if (ones & 0x80000000u) y &= 0x0000FFFFu;
-                if (ones)
-                  asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(y) : "memory");
-              }
-            }
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          if (mixed) {
-            // every thread of the slot has looked
-            __syncwarp();
-            if (lane == 0) mbar_arrive(looked + slot);
-            go = go && wait_or_fail(looked + slot, looks++ & 1u, s_fail);
-            const volatile uint32_t* f = s_nan[(blocks + i) & 7u];
-            if (f[0] | f[1] | f[2] | f[3]) {
-              if (odd < kOdd) {
-                if (r < 4u) s_odd[slot][odd].keys[r] = f[r];
-                if (r == 0) s_odd[slot][odd].key0 = (uint32_t)key0;
-                ++odd;
-              }
-            }
-          }
-        }
         const bool masked = key0 + (int32_t)kKeys > all_to || key0 < all_from || badp;
         // 32 keys from k0 on: a bit for each that this row sees
         auto seen = [&](int32_t k0) {
@@ -950,8 +939,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         arrive(p2_full + slot);
         key0 += (int32_t)(both ? 2u * kKeys : kKeys);
       }
-      const uint32_t last = both ? (count - 1u - slot) / 2u * 2u + slot : count - 1u;
-      const uint32_t e_last = e0 + 2u * last + 1u;  // this slot's last values
       blocks += count;
       e0 += 2u * count;
       go = go && wait_or_fail(o_full, tiles & 1u, s_fail);
@@ -962,8 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       go = go && wait_or_fail(ended, (tiles - 1u) & 1u, s_fail);
       if (!go) break;
       tc_after();
-      if (wq == 0 && lane == 0 && any) release(e_last, both);
       const bool whole = t->whole != 0u;
+      const Odd& odd = s_odd[(tiles - 1u) & 1u];
       float f0 = 1.f, f1 = 0.f;
       // alternate blocks: slot 1 hands its sums to slot 0 through the space of its queries
       float* x_o = reinterpret_cast<float*>(s_q + S::kTile);
@@ -994,8 +981,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t o[32];
         tmem_ld32<0>(to + 32u * x, o);
         tmem_wait_ld(o);
-        for (uint32_t k = 0; k < odd; ++k)
-          add_odd(t, s_odd[slot][k], x, from_key, to_key, o);
         if (both) {
           if (slot == 1)
 #pragma unroll
@@ -1008,6 +993,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      (f1 != 0.f ? x_o[j * 128 + r] * f1 : 0.f));
           asm volatile("barrier.cta.sync 1, 256;" ::: "memory");
         }
+        if (mine)
+          for (uint32_t k = 0; k < odd.count; ++k)
+            add_odd(t, odd.key0[k], odd.keys[k], x, from_key, to_key, o);
         if (mine && whole) {
 #pragma unroll
           for (uint32_t v = 0; v < 4; ++v) {

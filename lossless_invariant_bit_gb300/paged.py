@@ -20,6 +20,7 @@ through ``IbpStore``: ``key_rows()`` and ``value_rows()`` are the rows.
 """
 from __future__ import annotations
 
+import ctypes
 import math
 from typing import Optional, Tuple, Union
 
@@ -30,10 +31,14 @@ from . import ibp
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
 
+def _as_stream(stream) -> torch.cuda.Stream:
+    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+
+
 class PagedBatch:
     """The sequences of one step; keeps its tensors alive."""
 
-    __slots__ = ("desc", "page_table", "kv_lens", "q_starts", "n_tokens", "max_pages")
+    __slots__ = ("desc", "address", "page_table", "kv_lens", "q_starts", "n_tokens", "max_pages")
 
     def __init__(self, page_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor,
                  n_tokens: int, max_q_tokens: int):
@@ -51,15 +56,20 @@ class PagedBatch:
         self.desc = ibp.ibp_paged_batch(page_table.data_ptr(), kv_lens.data_ptr(),
                                         q_starts.data_ptr(), stride, n, self.max_pages,
                                         self.n_tokens, int(max_q_tokens))
+        self.address = ctypes.addressof(self.desc)
 
 
 class PagedCache:
     """Key and value pages of one layer, [n_pages, page_tokens, kv_heads, head_dim]
-    (any strides of whole heads; allocated when not given)."""
+    (any strides of whole heads; allocated when not given).
+
+    Calls run on the current stream, or on `stream` (a torch stream or a
+    cudaStream_t), on which their outputs and workspaces are then allocated too."""
 
     def __init__(self, kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
                  dtype: torch.dtype = torch.bfloat16, k: Optional[torch.Tensor] = None,
                  v: Optional[torch.Tensor] = None, device=None):
+        self.handle = None
         if dtype not in _DTYPES:
             raise ValueError("a paged cache holds float16 or bfloat16")
         shape = (n_pages, page_tokens, kv_heads, head_dim)
@@ -77,10 +87,11 @@ class PagedCache:
             raise ValueError("k and v must have the same strides")
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.n_pages, self.dtype, self.k, self.v = n_pages, dtype, k, v
-        self.handle = None
+        self.device = k.device
         # a dimension of one element has no stride to speak of
         row = head_dim * 2
         st = [s * 2 if n > 1 else max(s * 2, row) for s, n in zip(k.stride(), shape)]
+        self._lib = ibp._lib_handle()
         self.handle = ibp.ibp_paged_create(ibp.ibp_paged_desc(
             k.data_ptr(), v.data_ptr(), st[0], st[2], st[1], n_pages, page_tokens, kv_heads,
             head_dim, _DTYPES[dtype]))
@@ -128,15 +139,18 @@ class PagedCache:
         most max_q_tokens."""
         return PagedBatch(page_table, kv_lens, q_starts, n_tokens, max_q_tokens)
 
+    def _raw(self) -> int:
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
     def _heads(self, name: str, t: torch.Tensor, batch: PagedBatch, heads: Optional[int]) -> int:
         """Checks a [n_tokens, heads, head_dim] tensor; its token stride in bytes."""
-        s = t.shape
+        s, st = t.shape, t.stride()
         if (len(s) != 3 or s[0] != batch.n_tokens or s[2] != self.head_dim
                 or (heads is not None and s[1] != heads) or t.dtype != self.dtype or not t.is_cuda
-                or t.stride(2) != 1 or (s[1] > 1 and t.stride(1) != self.head_dim)):
+                or st[2] != 1 or (s[1] > 1 and st[1] != s[2])):
             raise ValueError("%s must be a device tensor [n_tokens, heads, head_dim] of the "
                              "cache's type whose heads lie side by side" % name)
-        return t.stride(0) * 2 if s[0] > 1 else s[1] * s[2] * 2
+        return st[0] * 2 if s[0] > 1 else s[1] * s[2] * 2
 
     def append(self, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor,
                q: Optional[torch.Tensor] = None, q_norm: Optional[torch.Tensor] = None,
@@ -146,17 +160,22 @@ class PagedCache:
         """Writes k and v [n_tokens, kv_heads, head_dim] into their pages; k and q
         normalised for each head (weights q_norm, k_norm) and rotated (cos_sin fp32
         [positions, rot_dim]: cosines, then sines) on the way.  Returns the queries."""
+        if stream is not None:
+            with torch.cuda.stream(_as_stream(stream)):
+                return self.append(batch, k, v, q, q_norm, k_norm, eps, cos_sin, pairs, q_out)
         ks = self._heads("k", k, batch, self.kv_heads)
         if self._heads("v", v, batch, self.kv_heads) != ks:
             raise ValueError("k and v must have the same token stride")
         qs = os = heads = 0
         if q is not None:
-            heads = q.shape[1] if q.dim() == 3 else 0
             qs = self._heads("q", q, batch, None)
+            heads = q.shape[1]
             if q_out is None:
-                q_out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=q.dtype,
-                                    device=q.device)
-            os = self._heads("q_out", q_out, batch, heads)
+                q_out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=self.dtype,
+                                    device=self.device)
+                os = heads * self.head_dim * 2
+            else:
+                os = self._heads("q_out", q_out, batch, heads)
         for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
             if w is not None and (w.shape != (self.head_dim,) or w.dtype != self.dtype
                                   or not w.is_cuda or not w.is_contiguous()):
@@ -167,8 +186,13 @@ class PagedCache:
                     or not cos_sin.is_contiguous()):
                 raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim]")
             n_pos, rot = cos_sin.shape
-        ibp.ibp_paged_append(self.handle, batch.desc, k, v, ks, q, qs, q_out, os, heads, q_norm,
-                             k_norm, eps, cos_sin, n_pos, rot, pairs, stream)
+        ibp._check(self._lib.ibp_paged_append(
+            self.handle, batch.address, k.data_ptr(), v.data_ptr(), ks,
+            None if q is None else q.data_ptr(), qs, None if q is None else q_out.data_ptr(), os,
+            heads, None if q_norm is None else q_norm.data_ptr(),
+            None if k_norm is None else k_norm.data_ptr(), eps,
+            None if cos_sin is None else cos_sin.data_ptr(), n_pos, rot, 1 if pairs else 0,
+            self._raw()), "ibp_paged_append")
         return q_out
 
     def attention(self, batch: PagedBatch, q: torch.Tensor, scale: Optional[float] = None,
@@ -178,25 +202,32 @@ class PagedCache:
         """Attention of q [n_tokens, q_heads, head_dim] over the cached tokens, or
         over the selected pages (int32 [n_tokens, kv_heads, n]); with lse=True also
         the log of each row's sum [n_tokens, q_heads].  scale: 1/sqrt(head_dim)."""
+        if stream is not None:
+            with torch.cuda.stream(_as_stream(stream)):
+                return self.attention(batch, q, scale, causal, window, pages, lse, out)
         qs = self._heads("q", q, batch, None)
-        heads = q.shape[1]
+        heads, device = q.shape[1], self.device
         if out is None:
-            out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=q.dtype,
-                              device=q.device)
+            out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=self.dtype,
+                              device=device)
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and type")
-        total = (torch.empty((batch.n_tokens, heads), dtype=torch.float32, device=q.device)
+        total = (torch.empty((batch.n_tokens, heads), dtype=torch.float32, device=device)
                  if lse else None)
         n = 0
         if pages is not None:
             if (pages.dim() != 3 or pages.shape[:2] != (batch.n_tokens, self.kv_heads)
-                    or pages.dtype != torch.int32 or not pages.is_contiguous()):
+                    or pages.dtype != torch.int32 or not pages.is_cuda
+                    or not pages.is_contiguous()):
                 raise ValueError("pages must be a contiguous int32 [n_tokens, kv_heads, n]")
             n = pages.shape[2]
-        ws = torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=q.device)
-        ibp.ibp_paged_attention(self.handle, batch.desc, q, qs, heads, out, total,
-                                1.0 / math.sqrt(self.head_dim) if scale is None else scale,
-                                causal, window, pages, n, ws, ibp.PAGED_WORKSPACE_BYTES, stream)
+        ws = torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        ibp._check(self._lib.ibp_paged_attention(
+            self.handle, batch.address, q.data_ptr(), qs, heads, out.data_ptr(),
+            total.data_ptr() if lse else None,
+            1.0 / math.sqrt(self.head_dim) if scale is None else scale, 1 if causal else 0, window,
+            None if pages is None else pages.data_ptr(), n, ws.data_ptr(),
+            ibp.PAGED_WORKSPACE_BYTES, self._raw()), "ibp_paged_attention")
         return (out, total) if lse else out
 
     def _bounds(self, bounds: torch.Tensor) -> None:
@@ -209,33 +240,47 @@ class PagedCache:
     def update_bounds(self, batch: PagedBatch, bounds: torch.Tensor, stream=None) -> None:
         """Smallest and largest keys of the pages that the new tokens went into,
         into bounds [n_pages, kv_heads, 2, head_dim]."""
+        if stream is not None:
+            with torch.cuda.stream(_as_stream(stream)):
+                return self.update_bounds(batch, bounds)
         self._bounds(bounds)
-        ibp.ibp_paged_bounds(self.handle, batch.desc, bounds, stream)
+        ibp._check(self._lib.ibp_paged_bounds(self.handle, batch.address, bounds.data_ptr(),
+                                              self._raw()), "ibp_paged_bounds")
 
     def page_scores(self, batch: PagedBatch, q: torch.Tensor, bounds: torch.Tensor,
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Upper bounds of q . k over each page, [n_tokens, kv_heads, max_pages]."""
+        if stream is not None:
+            with torch.cuda.stream(_as_stream(stream)):
+                return self.page_scores(batch, q, bounds, out)
         self._bounds(bounds)
         qs = self._heads("q", q, batch, None)
         shape = (batch.n_tokens, self.kv_heads, batch.max_pages)
         if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=q.device)
+            out = torch.empty(shape, dtype=torch.float32, device=self.device)
         elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous():
             raise ValueError("out must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
-        ibp.ibp_paged_scores(self.handle, batch.desc, q, qs, q.shape[1], bounds, out, stream)
+        ibp._check(self._lib.ibp_paged_scores(
+            self.handle, batch.address, q.data_ptr(), qs, q.shape[1], bounds.data_ptr(),
+            out.data_ptr(), self._raw()), "ibp_paged_scores")
         return out
 
     def select_pages(self, batch: PagedBatch, scores: torch.Tensor, n: int,
                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """The n pages of largest score of each token and head, int32
         [n_tokens, kv_heads, n], ascending, -1 behind the last."""
+        if stream is not None:
+            with torch.cuda.stream(_as_stream(stream)):
+                return self.select_pages(batch, scores, n, out)
         if (scores.shape != (batch.n_tokens, self.kv_heads, batch.max_pages)
-                or scores.dtype != torch.float32 or not scores.is_contiguous()):
+                or scores.dtype != torch.float32 or not scores.is_cuda
+                or not scores.is_contiguous()):
             raise ValueError("scores must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
         shape = (batch.n_tokens, self.kv_heads, n)
         if out is None:
-            out = torch.empty(shape, dtype=torch.int32, device=scores.device)
+            out = torch.empty(shape, dtype=torch.int32, device=self.device)
         elif out.shape != shape or out.dtype != torch.int32 or not out.is_contiguous():
             raise ValueError("out must be a contiguous int32 [n_tokens, kv_heads, n]")
-        ibp.ibp_paged_select(self.handle, batch.desc, scores, n, out, stream)
+        ibp._check(self._lib.ibp_paged_select(self.handle, batch.address, scores.data_ptr(), n,
+                                              out.data_ptr(), self._raw()), "ibp_paged_select")
         return out
