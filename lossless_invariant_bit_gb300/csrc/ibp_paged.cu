@@ -3,6 +3,7 @@
 // of the pages, and the choice of the pages with the largest scores.
 #include "ibp_paged.cuh"
 #include "ibp_sm103.cuh"
+#include "ibp_tma.cuh"
 
 namespace ibp {
 namespace {
@@ -239,29 +240,37 @@ __global__ void __launch_bounds__(128)
 // sum_d max(q lo, q hi) = sum_d max(q, 0) hi + min(q, 0) lo: a product of
 // [max(q, 0), min(q, 0)] with [hi, lo], whose 16-bit products are exact in fp32.
 // A warp holds 16 rows (as many tokens of one sequence as their G queries
-// allow; 16 of the G queries at a time when G > 16) as the left operand and
-// goes over pages, 8 to a matrix instruction.  The sum runs over the
-// channels in any order, so a lane takes 8 channels together (one 16-byte
-// load) where the instruction's layout wants pairs: four lanes cover 64 bytes
-// of a page's bounds, straight from global memory into the operand's registers.
-constexpr uint32_t kScoreGroup = 32;  // pages between two stores of scores
+// allow; 16 of the G queries at a time when G > 16) as the left operand, and 32 pages'
+// bounds in shared memory, all in flight together: bound by HBM where tokens are few.
+// (16-byte asynchronous copies: a bulk copy for each page's 512 bytes took 35 us for
+// 134 MB, as many as the copy engine starts.)
+// The sum runs over the channels in any order, so a lane takes 8 channels
+// together (one 16-byte load) where the instruction's layout wants pairs; rows are 16
+// bytes longer than their bounds, so that eight pages' loads meet no bank twice.
+constexpr uint32_t kScoreGroup = 32;  // pages of a warp at a time
+
+template <int kDP>
+constexpr uint32_t score_smem() {
+  return 4u * kScoreGroup * (kDP * 4u + 16u);
+}
 
 template <bool kBf16, int kDP>
 __global__ void __launch_bounds__(128, 3)
     k_paged_scores(PagedGeom g, PagedBatchView b, const uint8_t* q, uint64_t q_stride, uint32_t G,
                    const uint8_t* bounds, float* scores, uint32_t per_warp) {
   constexpr int kC = kDP / 32;  // 16-byte chunks per lane
+  extern __shared__ __align__(128) uint8_t s_bounds[];
   __shared__ float s_c[4][16][kScoreGroup + 1];
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
   const uint32_t quad = lane & 3u, r0 = lane >> 2;
   const uint32_t tpt = G >= 16u ? 1u : 16u / G;  // tokens of a tile
   const uint32_t h = blockIdx.y;
+  const uint32_t stride = g.D * 4u + 16u;
+  uint8_t* mine = s_bounds + warp * kScoreGroup * stride;
   uint32_t first;
   const uint32_t s = paged_find_tile(b, tpt, 1u, blockIdx.x, first);
   const PagedSeq sq = paged_seq(b, g.page_lg, s);
-  if (!sq.ok) {
-    if (threadIdx.x == 0) set_status(g.status, IBP_ERANGE);
-  }
+  if (!sq.ok && threadIdx.x == 0) set_status(g.status, IBP_ERANGE);
   const uint32_t t0 = (blockIdx.x - first) * tpt;
   if (blockIdx.x < first || t0 >= sq.n) return;
   const uint32_t nt = min(tpt, sq.n - t0);
@@ -270,98 +279,137 @@ __global__ void __launch_bounds__(128, 3)
   const uint32_t g1 = min(groups, g0 + per_warp);
   const int64_t pos_last = (int64_t)sq.L - sq.n + t0 + nt - 1;
   const uint32_t seen_last = pos_last < 0 ? 0u : (uint32_t)(pos_last >> g.page_lg) + 1u;
+  const float hidden = __int_as_float((int)0xFF800000u);
   uint32_t qv[kC * 4 * 2];  // [chunk][4 words][row, row + 8]
+  auto page_at = [&](uint32_t c) {
+    return c + lane < seen_last ? __ldg(b.table + s * b.table_stride + c + lane) : -1;
+  };
+  // Half of a group's bounds, on their way: a page's 16-byte pieces to as many lanes
+  // (the next power of two), 32 / kPiece pages at a time.
+  constexpr uint32_t kPiece = kDP / 4u;
+  const uint32_t piece = lane % kPiece, page0 = lane / kPiece;
+  const uint8_t* from = bounds + ((uint64_t)h * g.D / 4u + piece) * 16u;
+  const uint32_t to = smem_addr(mine) + page0 * stride + piece * 16u;
+  const uint32_t page_bytes = g.H * g.D * 4u;
+  auto copy_half = [&](uint32_t half, int32_t id) {
+#pragma unroll 4
+    for (uint32_t k = 0; k < kScoreGroup / 2u; k += 32u / kPiece) {
+      const uint32_t at = half * (kScoreGroup / 2u) + k;
+      const int32_t pid = __shfl_sync(0xFFFFFFFFu, id, at + page0);
+      if ((uint32_t)pid < g.n_pages && piece < g.D / 4u)  // (negative: none)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + at * stride),
+                     "l"(from + (uint64_t)(uint32_t)pid * page_bytes)
+                     : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  const uint32_t blocks = tpt == 1u ? (G + 15u) / 16u : 1u;  // of 16 rows
+  int32_t next = page_at(g0 * kScoreGroup), next2 = page_at((g0 + 1u) * kScoreGroup);
+  copy_half(0, next);
+  copy_half(1, next);
   for (uint32_t gr = g0; gr < g1; ++gr) {
     const uint32_t c0 = gr * kScoreGroup;
+    if (c0 >= seen_last) {
+      for (uint32_t tt = 0; tt < nt; ++tt)
+        if (c0 + lane < b.max_pages)
+          scores[((uint64_t)(sq.q0 + t0 + tt) * g.H + h) * b.max_pages + c0 + lane] = hidden;
+      continue;
+    }
+    int32_t id = next;  // this lane's page
+    next = next2;
+    next2 = page_at(c0 + 2u * kScoreGroup);
+    if (c0 + lane < seen_last && (id < 0 || (uint32_t)id >= g.n_pages)) {
+      set_status(g.status, IBP_ERANGE);
+      id = -1;
+    }
     float best = 0.f;  // over the queries of the earlier row blocks (G > 16)
-    if (c0 < seen_last) {
-      int32_t id = -1;
-      if (c0 + lane < seen_last) {
-        id = __ldg(b.table + s * b.table_stride + c0 + lane);
-        if (id < 0 || (uint32_t)id >= g.n_pages) {
-          set_status(g.status, IBP_ERANGE);
-          id = -1;
-        }
-      }
-      for (uint32_t rb = 0; rb * 16u < (tpt == 1u ? G : 16u); ++rb) {
-        if (gr == g0 || G > 16u) {  // the rows' queries
+    for (uint32_t rb = 0; rb < blocks; ++rb) {
+      if (gr == g0 || blocks > 1u) {  // the rows' queries
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint32_t r = rb * 16u + r0 + 8u * e;
-            const uint32_t tt = r / G, gg = r % G;
-            const bool live = tt < nt;
-            const uint8_t* src = q + (uint64_t)(sq.q0 + t0 + tt) * q_stride +
-                                 ((uint64_t)h * G + gg) * g.D * 2u;
-#pragma unroll
-            for (int c = 0; c < kC; ++c) {
-              const uint32_t ch = 32u * c + 8u * quad;
-              uint4 x = make_uint4(0, 0, 0, 0);
-              if (live && ch < g.D) x = __ldg(reinterpret_cast<const uint4*>(src + ch * 2u));
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                qv[(c * 4 + i) * 2 + e] = w[i];
-              }
-            }
-          }
-        }
-#pragma unroll
-        for (uint32_t nt8 = 0; nt8 < kScoreGroup / 8u; ++nt8) {
-          const int32_t pid = __shfl_sync(0xFFFFFFFFu, id, nt8 * 8u + r0);
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
-          uint4 lo[kC], hi[kC];
-          const uint8_t* src =
-              bounds + ((uint64_t)(uint32_t)(pid < 0 ? 0 : pid) * g.H + h) * g.D * 4u;
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t r = rb * 16u + r0 + 8u * e;
+          const uint32_t tt = r / G, gg = r % G;
+          const bool live = tt < nt;
+          const uint8_t* src = q + (uint64_t)(sq.q0 + t0 + tt) * q_stride +
+                               ((uint64_t)h * G + gg) * g.D * 2u;
 #pragma unroll
           for (int c = 0; c < kC; ++c) {
             const uint32_t ch = 32u * c + 8u * quad;
-            lo[c] = hi[c] = make_uint4(0, 0, 0, 0);
-            if (pid >= 0 && ch < g.D) {
-              lo[c] = __ldg(reinterpret_cast<const uint4*>(src + ch * 2u));
-              hi[c] = __ldg(reinterpret_cast<const uint4*>(src + (g.D + ch) * 2u));
-            }
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live && ch < g.D) x = __ldg(reinterpret_cast<const uint4*>(src + ch * 2u));
+            qv[(c * 4 + 0) * 2 + e] = x.x;
+            qv[(c * 4 + 1) * 2 + e] = x.y;
+            qv[(c * 4 + 2) * 2 + e] = x.z;
+            qv[(c * 4 + 3) * 2 + e] = x.w;
           }
-#pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            uint32_t p[8], n[8];  // split by sign
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              p[k] = max2<kBf16>(qv[c * 8 + k], 0u);
-              n[k] = min2<kBf16>(qv[c * 8 + k], 0u);
-            }
-            mma_16816<kBf16>(acc, p, hi[c].x, hi[c].y);
-            mma_16816<kBf16>(acc, p + 4, hi[c].z, hi[c].w);
-            mma_16816<kBf16>(acc, n, lo[c].x, lo[c].y);
-            mma_16816<kBf16>(acc, n + 4, lo[c].z, lo[c].w);
-          }
-          float* d0 = &s_c[warp][r0][nt8 * 8u + 2u * quad];
-          float* d1 = &s_c[warp][r0 + 8u][nt8 * 8u + 2u * quad];
-          d0[0] = acc[0], d0[1] = acc[1], d1[0] = acc[2], d1[1] = acc[3];
         }
-        __syncwarp();
-        // the largest over each token's queries, kept by the lane of the page
-        const uint32_t rows = tpt == 1u ? min(16u, G - rb * 16u) : G;
-        for (uint32_t tt = 0; tt < nt; ++tt) {
-          float m = s_c[warp][tt * G][lane];
-          for (uint32_t i = 1; i < rows; ++i) {
-            const float v = s_c[warp][tt * G + i][lane];
-            m = (v > m || v != v) ? v : m;
-          }
-          if (tpt == 1u && rb) m = (best > m || best != best) ? best : m;
-          best = m;
-          const int64_t pos = (int64_t)sq.L - sq.n + t0 + tt;
-          const bool seen = pos >= 0 && c0 + lane <= (uint32_t)(pos >> g.page_lg) && id >= 0;
-          if (c0 + lane < b.max_pages && (rb + 1u) * 16u >= (tpt == 1u ? G : 16u))
-            scores[((uint64_t)(sq.q0 + t0 + tt) * g.H + h) * b.max_pages + c0 + lane] =
-                seen ? m : __int_as_float((int)0xFF800000u);
-        }
-        __syncwarp();
       }
-    } else {
-      for (uint32_t tt = 0; tt < nt; ++tt)
-        if (c0 + lane < b.max_pages)
+#pragma unroll 1
+      for (uint32_t half = 0; half < 2u; ++half) {
+        if (rb == 0) {  // all but the half that was asked for last
+          if (blocks == 1u)
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+          else
+            asm volatile("cp.async.wait_all;" ::: "memory");
+          __syncwarp();
+        }
+        // 16 pages, 8 to an instruction; the signs' products apart: four chains of sums
+        const uint8_t* src = mine + (half * 16u + r0) * stride + quad * 16u;
+        float acc[2][2][4] = {};
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          uint32_t p[8], n[8];  // the queries split by sign
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            p[k] = max2<kBf16>(qv[c * 8 + k], 0u);
+            n[k] = min2<kBf16>(qv[c * 8 + k], 0u);
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const uint8_t* at = src + x * 8u * stride + c * 64u;
+            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
+            if (32u * c + 8u * quad < g.D) {
+              lo = *reinterpret_cast<const uint4*>(at);
+              hi = *reinterpret_cast<const uint4*>(at + g.D * 2u);
+            }
+            mma_16816<kBf16>(acc[x][0], p, hi.x, hi.y);
+            mma_16816<kBf16>(acc[x][1], n, lo.x, lo.y);
+            mma_16816<kBf16>(acc[x][0], p + 4, hi.z, hi.w);
+            mma_16816<kBf16>(acc[x][1], n + 4, lo.z, lo.w);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          float* d0 = &s_c[warp][r0][half * 16u + x * 8u + 2u * quad];
+          float* d1 = &s_c[warp][r0 + 8u][half * 16u + x * 8u + 2u * quad];
+          d0[0] = acc[x][0][0] + acc[x][1][0], d0[1] = acc[x][0][1] + acc[x][1][1];
+          d1[0] = acc[x][0][2] + acc[x][1][2], d1[1] = acc[x][0][3] + acc[x][1][3];
+        }
+        // a half that has been read makes room for the next group's
+        if (rb + 1u == blocks) {
+          __syncwarp();
+          copy_half(half, gr + 1u < g1 ? next : -1);
+        }
+      }
+      __syncwarp();
+      // the largest over each token's queries, kept by the lane of the page (memory of a
+      // page that was not copied is never looked at)
+      const uint32_t rows = tpt == 1u ? min(16u, G - rb * 16u) : G;
+      for (uint32_t tt = 0; tt < nt; ++tt) {
+        float m = s_c[warp][tt * G][lane];
+        for (uint32_t i = 1; i < rows; ++i) {
+          const float v = s_c[warp][tt * G + i][lane];
+          m = (v > m || v != v) ? v : m;
+        }
+        if (rb) m = (best > m || best != best) ? best : m;
+        best = m;
+        const int64_t pos = (int64_t)sq.L - sq.n + t0 + tt;
+        const bool seen = pos >= 0 && c0 + lane <= (uint32_t)(pos >> g.page_lg) && id >= 0;
+        if (c0 + lane < b.max_pages && rb + 1u == blocks)
           scores[((uint64_t)(sq.q0 + t0 + tt) * g.H + h) * b.max_pages + c0 + lane] =
-              __int_as_float((int)0xFF800000u);
+              seen ? m : hidden;
+      }
+      __syncwarp();
     }
   }
 }
@@ -393,7 +441,7 @@ __device__ __forceinline__ uint32_t select_row(const PagedGeom& g, const PagedBa
 // first are taken.  Bound by issue: 2 kPer instructions a count, 9 kPer to write the
 // numbers.  4 rows to a CTA when kWarps is 1.
 template <int kWarps, int kPer>
-__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32)
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32, kPer <= 16 ? 4 : kPer <= 32 && kWarps == 1 ? 6 : 1)
     k_paged_pick(PagedGeom g, PagedBatchView b, const float* scores, uint32_t n_sel,
                  int32_t* selected) {
   constexpr int kRowsPer = kWarps == 1 ? 4 : 1;
@@ -671,29 +719,34 @@ cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, con
   const uint64_t tiles = (uint64_t)b.n_tokens / tpt + b.n_seqs;
   const uint64_t groups = (b.max_pages + kScoreGroup - 1u) / kScoreGroup;
   if (tiles > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  // groups of pages for each warp: one, until that makes 64 warps for every SM
-  const uint64_t rows = tiles * g.H;
-  uint64_t per = groups * rows / (64ull * sm_count);
-  if (per > 16u) per = 16u;
-  if (per < 1u) per = 1u;
-  const uint64_t z = (groups + 4u * per - 1) / (4u * per);
+  // A row's groups of pages go to as many CTAs as the GPU holds at a time (three to an SM),
+  // so that what a CTA looks up first is paid once: 16 tokens x 8 heads x 2048 pages in
+  // 34.9 us with a group to a warp.  (Tiles that hold rows: the numbers leave gaps.)
+  const uint64_t full = b.n_tokens < (uint64_t)tpt * b.n_seqs
+                            ? (b.n_tokens < b.n_seqs ? b.n_tokens : b.n_seqs)
+                            : (b.n_tokens + tpt - 1u) / tpt;
+  uint64_t z = 3ull * sm_count / (full * g.H);
+  if (z < 1u) z = 1u;
+  const uint64_t per = (groups + 4u * z - 1) / (4u * z);
+  z = (groups + 4u * per - 1) / (4u * per);
   if (z > 65535u) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)tiles, g.H, (unsigned)z);
+#define IBP_SCORES(B, DP)                                                                    \
+  do {                                                                                       \
+    const cudaError_t e =                                                                    \
+        smem_limit(reinterpret_cast<const void*>(k_paged_scores<B, DP>), score_smem<DP>());  \
+    if (e != cudaSuccess) return e;                                                          \
+    k_paged_scores<B, DP><<<grid, 128, 4u * kScoreGroup * (g.D * 4u + 16u), st>>>(           \
+        g, b, q, q_stride, G, bounds, scores, (uint32_t)per);                                \
+  } while (0)
   if (g.D <= 64u) {
-    if (g.bf16)
-      k_paged_scores<true, 64><<<grid, 128, 0, st>>>(g, b, q, q_stride, G, bounds, scores,
-                                                     (uint32_t)per);
-    else
-      k_paged_scores<false, 64><<<grid, 128, 0, st>>>(g, b, q, q_stride, G, bounds, scores,
-                                                      (uint32_t)per);
+    if (g.bf16) IBP_SCORES(true, 64);
+    else IBP_SCORES(false, 64);
   } else {
-    if (g.bf16)
-      k_paged_scores<true, 128><<<grid, 128, 0, st>>>(g, b, q, q_stride, G, bounds, scores,
-                                                      (uint32_t)per);
-    else
-      k_paged_scores<false, 128><<<grid, 128, 0, st>>>(g, b, q, q_stride, G, bounds, scores,
-                                                       (uint32_t)per);
+    if (g.bf16) IBP_SCORES(true, 128);
+    else IBP_SCORES(false, 128);
   }
+#undef IBP_SCORES
   return cudaGetLastError();
 }
 

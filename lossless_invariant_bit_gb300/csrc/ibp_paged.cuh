@@ -110,42 +110,50 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedBatchView& b, uint32_t 
   return r;
 }
 
-// The sequence of row t: the last one that begins at or before t.  n_seqs when none holds it.
+// The last i in [0, n) with key(i) <= x, for keys that do not decrease (0 if none; some
+// number below n if they do): 32 at a time, by a whole warp with one x.
+template <typename Key>
+__device__ __forceinline__ uint32_t warp_search(uint32_t n, uint64_t x, Key key) {
+  const uint32_t lane = threadIdx.x & 31u;
+  uint32_t lo = 0, len = n;
+  while (len > 1u) {
+    const uint32_t step = (len + 31u) / 32u;
+    const uint32_t at = lane * step;
+    const uint32_t reach =
+        __popc(__ballot_sync(0xFFFFFFFFu, at < len && key(lo + at) <= x));
+    const uint32_t k = reach ? reach - 1u : 0u;
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  return lo;
+}
+
+// The sequence of row t; n_seqs when none holds it.  For a whole warp.
 __device__ __forceinline__ uint32_t paged_find(const PagedBatchView& b, uint32_t t) {
-  uint32_t lo = 0, hi = b.n_seqs;  // the answer lies in [lo, hi)
   if (b.n_seqs == b.n_tokens && t < b.n_seqs && __ldg(b.q_starts + t) == (int32_t)t &&
       __ldg(b.q_starts + t + 1) == (int32_t)t + 1)
     return t;  // one row per sequence
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (__ldg(b.q_starts + mid) <= (int32_t)t)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  return __ldg(b.q_starts + lo) <= (int32_t)t && (int32_t)t < __ldg(b.q_starts + lo + 1)
-             ? lo
-             : b.n_seqs;
+  const uint32_t s = warp_search(b.n_seqs, t, [&](uint32_t i) {
+    const int32_t q = __ldg(b.q_starts + i);
+    return (uint64_t)(q < 0 ? 0 : q);
+  });
+  return __ldg(b.q_starts + s) <= (int32_t)t && (int32_t)t < __ldg(b.q_starts + s + 1) ? s
+                                                                                        : b.n_seqs;
 }
 
-// Tiles of `lg`-sized groups of a sequence's rows (or pages), numbered so that a
-// tile's sequence is found without sums over the sequences: sequence s owns the
-// numbers from q_starts[s] / size + c * s on, which leaves room for its at most
-// n / size + c tiles.  Returns the sequence of tile x, and the first number it owns.
+// Tiles of `size` rows (or tokens of pages) of a sequence, numbered so that a tile's
+// sequence is found without sums over the sequences: sequence s owns the numbers from
+// q_starts[s] / size + c * s on, which leaves room for its at most n / size + c tiles.
+// Returns the sequence of tile x, and the first number it owns.  For a whole warp.
 __device__ __forceinline__ uint32_t paged_find_tile(const PagedBatchView& b, uint32_t size,
                                                     uint32_t c, uint32_t x, uint32_t& first) {
-  uint32_t lo = 0, hi = b.n_seqs;
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) >> 1;
-    const int32_t q = __ldg(b.q_starts + mid);
-    if ((uint64_t)(q < 0 ? 0 : q) / size + (uint64_t)c * mid <= x)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  const int32_t q = __ldg(b.q_starts + lo);
-  first = (uint32_t)(q < 0 ? 0 : q) / size + c * lo;
-  return lo;
+  auto key = [&](uint32_t i) {
+    const int32_t q = __ldg(b.q_starts + i);
+    return (uint64_t)((uint32_t)(q < 0 ? 0 : q) / size) + (uint64_t)c * i;
+  };
+  const uint32_t s = warp_search(b.n_seqs, x, key);
+  first = (uint32_t)key(s);
+  return s;
 }
 
 #endif

@@ -31,6 +31,20 @@ from . import ibp
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
 
+# Attention's workspace of each (device, stream): calls on one stream follow one another.
+_workspaces = {}
+
+
+def _workspace(device: torch.device, raw: int) -> torch.Tensor:
+    if torch.cuda.is_current_stream_capturing():  # a graph's replays may run on any stream
+        return torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+    ws = _workspaces.get((device.index, raw))
+    if ws is None:
+        ws = torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        _workspaces[device.index, raw] = ws
+    return ws
+
+
 def _as_stream(stream) -> torch.cuda.Stream:
     return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
 
@@ -221,13 +235,14 @@ class PagedCache:
                     or not pages.is_contiguous()):
                 raise ValueError("pages must be a contiguous int32 [n_tokens, kv_heads, n]")
             n = pages.shape[2]
-        ws = torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
+        raw = self._raw()
+        ws = _workspace(device, raw)
         ibp._check(self._lib.ibp_paged_attention(
             self.handle, batch.address, q.data_ptr(), qs, heads, out.data_ptr(),
             total.data_ptr() if lse else None,
             1.0 / math.sqrt(self.head_dim) if scale is None else scale, 1 if causal else 0, window,
             None if pages is None else pages.data_ptr(), n, ws.data_ptr(),
-            ibp.PAGED_WORKSPACE_BYTES, self._raw()), "ibp_paged_attention")
+            ibp.PAGED_WORKSPACE_BYTES, raw), "ibp_paged_attention")
         return (out, total) if lse else out
 
     def _bounds(self, bounds: torch.Tensor) -> None:
