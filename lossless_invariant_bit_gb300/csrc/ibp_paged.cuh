@@ -73,13 +73,16 @@ cudaError_t launch_paged_select(const PagedGeom& g, const PagedBatchView& b, con
 // Sequences with at most a.max_rows rows (new tokens x query heads of a K/V
 // head), or tokens with a page list each.
 constexpr uint32_t kStepRows = 16;
-cudaError_t launch_paged_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
+// behind: it may start while the chunk kernel of the same call ends.
+cudaError_t launch_paged_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, bool behind,
                               cudaStream_t st);
 // Tokens of a page in one box of the maps, at most.
 constexpr uint32_t kBoxTokens = 128;
 // Sequences with more than a.max_rows rows.
 cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
                                cudaStream_t st);
+// Joins its pieces: after it, and after the step kernel where the call has one.
+cudaError_t launch_paged_chunk_join(const PagedAttnArgs& a, int sm_count, cudaStream_t st);
 
 #ifdef __CUDACC__
 

@@ -262,16 +262,16 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
   a.ws = static_cast<uint8_t*>(workspace);
   const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   // Lists of pages, and sequences with one tile of 16 rows at most, go to the step
-  // kernel, the others to the chunk kernel; a batch may need both.
+  // kernel, the others to the chunk kernel; a batch may need both, and the step kernel's
+  // CTAs then fill the SMs that the chunk kernel's have left.
   const bool few = selected || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
-  if (few || b->n_seqs > 1u) {
-    a.max_rows = ibp::kStepRows;
-    const cudaError_t ce = ibp::launch_paged_step(a, c->maps, c->sm_count, st);
-    if (ce != cudaSuccess || few) return cu(ce);
-  } else {
-    a.max_rows = 0;
-  }
-  return cu(ibp::launch_paged_chunk(a, c->maps, c->sm_count, st));
+  const bool both = !few && b->n_seqs > 1u;
+  a.max_rows = few || both ? ibp::kStepRows : 0u;
+  cudaError_t ce = few ? cudaSuccess : ibp::launch_paged_chunk(a, c->maps, c->sm_count, st);
+  if (ce == cudaSuccess && (few || both))
+    ce = ibp::launch_paged_step(a, c->maps, c->sm_count, both, st);
+  if (ce == cudaSuccess && !few) ce = ibp::launch_paged_chunk_join(a, c->sm_count, st);
+  return cu(ce);
 }
 
 ibp_status ibp_paged_bounds(const ibp_paged* c, const ibp_paged_batch* b, void* bounds,

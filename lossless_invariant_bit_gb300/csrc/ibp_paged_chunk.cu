@@ -386,6 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // what comes behind may take the SMs that have ended (it waits for this grid itself)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // ---- the list of blocks and this CTA's run of it
   uint64_t mine = 0, total = 0;
   for (uint32_t s = tid; s < a.b.n_seqs; s += kThreads) {
@@ -1040,7 +1042,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                  : "memory");
   if (tid == 0 && *s_fail) set_status(a.g.status, IBP_ETIMEOUT);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 // Joins the pieces of the tile that CTA blockIdx.x of the first kernel ended, in the
@@ -1101,8 +1102,13 @@ cudaError_t launch(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, cud
   kern<<<ctas, kThreads, S::kSmem, st>>>(m.k, m.v, a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  return cudaSuccess;
+}
+
+template <int kDP, bool kBf16>
+cudaError_t launch_join(const PagedAttnArgs& a, int sm_count, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 8, 1);
+  cfg.gridDim = dim3((uint32_t)sm_count < kMaxCtas ? (uint32_t)sm_count : kMaxCtas, 8, 1);
   cfg.blockDim = dim3(kDP * 2, 1, 1);  // a warp per 16 channels
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1121,6 +1127,13 @@ cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const PagedMaps& m, int s
   if (a.g.D <= 64u)
     return b ? launch<64, true>(a, m, sm_count, st) : launch<64, false>(a, m, sm_count, st);
   return b ? launch<128, true>(a, m, sm_count, st) : launch<128, false>(a, m, sm_count, st);
+}
+
+cudaError_t launch_paged_chunk_join(const PagedAttnArgs& a, int sm_count, cudaStream_t st) {
+  const bool b = a.g.bf16 != 0u;
+  if (a.g.D <= 64u)
+    return b ? launch_join<64, true>(a, sm_count, st) : launch_join<64, false>(a, sm_count, st);
+  return b ? launch_join<128, true>(a, sm_count, st) : launch_join<128, false>(a, sm_count, st);
 }
 
 }  // namespace ibp

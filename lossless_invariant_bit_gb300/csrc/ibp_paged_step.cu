@@ -658,6 +658,9 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
   }
   __syncthreads();
   if (tid == 0 && s_fail) set_status(a.g.status, IBP_ETIMEOUT);
+  // launched behind the chunk kernel of the same call, it ends after it: what follows
+  // this kernel may count on both
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
@@ -701,24 +704,29 @@ __global__ void __launch_bounds__(128) k_paged_step_join(PagedAttnArgs a) {
 }
 
 template <int kDP, bool kBf16, bool kSel>
-cudaError_t launch(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, cudaStream_t st) {
+cudaError_t launch(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, bool behind,
+                   cudaStream_t st) {
   using S = StepShape<kDP>;
   auto kern = k_paged_step<kDP, kBf16, kSel>;
   cudaError_t e = smem_limit(reinterpret_cast<const void*>(kern), S::kSmem);
   if (e != cudaSuccess) return e;
   uint32_t ctas = (uint32_t)sm_count * (kDP == 64 ? 2u : 1u);
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  kern<<<ctas, kThreads, S::kSmem, st>>>(m.k, m.v, a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 4, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
+  cfg.numAttrs = behind ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, m.k, m.v, a);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(ctas, 4, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, k_paged_step_join<kDP, kBf16>, a);
 }
@@ -728,21 +736,21 @@ static_assert(2u * kMaxCtas * sizeof(Piece<128>) + kMaxCtas * sizeof(Join) <= kS
 
 }  // namespace
 
-cudaError_t launch_paged_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
+cudaError_t launch_paged_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, bool behind,
                               cudaStream_t st) {
   const bool b = a.g.bf16 != 0u;
   if (a.selected) {
     if (a.g.D <= 64u)
-      return b ? launch<64, true, true>(a, m, sm_count, st)
-               : launch<64, false, true>(a, m, sm_count, st);
-    return b ? launch<128, true, true>(a, m, sm_count, st)
-             : launch<128, false, true>(a, m, sm_count, st);
+      return b ? launch<64, true, true>(a, m, sm_count, behind, st)
+               : launch<64, false, true>(a, m, sm_count, behind, st);
+    return b ? launch<128, true, true>(a, m, sm_count, behind, st)
+             : launch<128, false, true>(a, m, sm_count, behind, st);
   }
   if (a.g.D <= 64u)
-    return b ? launch<64, true, false>(a, m, sm_count, st)
-             : launch<64, false, false>(a, m, sm_count, st);
-  return b ? launch<128, true, false>(a, m, sm_count, st)
-           : launch<128, false, false>(a, m, sm_count, st);
+    return b ? launch<64, true, false>(a, m, sm_count, behind, st)
+             : launch<64, false, false>(a, m, sm_count, behind, st);
+  return b ? launch<128, true, false>(a, m, sm_count, behind, st)
+           : launch<128, false, false>(a, m, sm_count, behind, st);
 }
 
 }  // namespace ibp
