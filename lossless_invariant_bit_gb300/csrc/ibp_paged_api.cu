@@ -17,28 +17,42 @@ constexpr int kDevices = 64, kWords = 4096;
 struct StatusPool {
   uint32_t* words = nullptr;  // 32 bytes apart
   bool used[kWords] = {};
+  bool fresh[kWords] = {};  // cleared with the block, never given out since
   int next = 0;
 };
 
 std::mutex g_pool_mu;
 StatusPool g_pool[kDevices];
 
-// A word that no handle uses, not yet cleared; -1: none left (or no memory).
+// A word that no handle uses, cleared; -1: none left, or no memory.
 int take_status(int device, uint32_t** word) {
   if (device < 0 || device >= kDevices) return -1;
   std::lock_guard<std::mutex> lock(g_pool_mu);
   StatusPool& p = g_pool[device];
-  if (!p.words && cudaMalloc(reinterpret_cast<void**>(&p.words), 32u * kWords) != cudaSuccess) {
-    cudaGetLastError();
-    p.words = nullptr;
-    return -1;
+  if (!p.words) {
+    if (cudaMalloc(reinterpret_cast<void**>(&p.words), 32u * kWords) != cudaSuccess ||
+        cudaMemset(p.words, 0, 32u * kWords) != cudaSuccess ||
+        cudaStreamSynchronize(nullptr) != cudaSuccess) {
+      cudaGetLastError();
+      cudaFree(p.words);
+      p.words = nullptr;
+      return -1;
+    }
+    for (bool& f : p.fresh) f = true;
   }
   for (int i = 0; i < kWords; ++i) {
     const int at = (p.next + i) % kWords;
     if (p.used[at]) continue;
-    p.used[at] = true;
-    p.next = at + 1;
     *word = p.words + 8 * at;
+    // a word used before may hold that handle's last error
+    if (!p.fresh[at] && (cudaMemset(*word, 0, 4) != cudaSuccess ||
+                         cudaStreamSynchronize(nullptr) != cudaSuccess)) {
+      cudaGetLastError();
+      return -1;
+    }
+    p.used[at] = true;
+    p.fresh[at] = false;
+    p.next = at + 1;
     return at;
   }
   return -1;
@@ -90,8 +104,9 @@ ibp_status check(const ibp_paged* c, const ibp_paged_batch* b, bool* empty) {
   if (!b->page_table || !b->kv_lens || !b->q_starts || b->max_pages == 0 ||
       b->max_q_tokens == 0 || b->table_stride < b->max_pages)
     return IBP_EINVAL;
-  // positions, and rows with their heads, are 31-bit numbers
-  if (((uint64_t)b->max_pages << c->g.page_lg) > 0x7FFFFFFFull || b->n_tokens > 0x1FFFFFFFu ||
+  // positions are 30-bit numbers (blocks of them may reach past the last), rows with their
+  // heads 31-bit ones
+  if (((uint64_t)b->max_pages << c->g.page_lg) > (1ull << 30) || b->n_tokens > 0x1FFFFFFFu ||
       b->n_seqs > 0xFFFFFFu)
     return IBP_EINVAL;
   if (misaligned(b->page_table, 4) || misaligned(b->kv_lens, 4) || misaligned(b->q_starts, 4))
@@ -157,12 +172,6 @@ ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
   if (c->status_at < 0) {
     delete c;
     return IBP_ENOMEM;
-  }
-  if (cudaMemset(c->g.status, 0, 4) != cudaSuccess ||
-      cudaStreamSynchronize(nullptr) != cudaSuccess) {
-    give_status(c->device, c->status_at);
-    delete c;
-    return IBP_ECUDA;
   }
   *out = c;
   return IBP_OK;
