@@ -31,20 +31,23 @@ __global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_
   const uint32_t c0 = split ? lane * 4u : lane * 8u, c1 = split ? half + lane * 4u : c0 + 4u;
   const bool turned = lane * 8u < a.rot;
   const uint64_t row = a.g.D * 2ull;
-  // a round's kind (0 queries, 1 keys, 2 values) and this thread's head in it
-  auto place = [&](uint32_t r, uint32_t& kind) {
-    kind = r < nq ? 0u : r < nq + nk ? 1u : 2u;
-    return (kind == 0u ? r : kind == 1u ? r - nq : r - nq - nk) * kSubs + sub;
+  // The rounds of one kind that fall to this CTA: a pointer walks over this thread's heads.
+  struct Part {
+    const uint8_t* src;  // this thread's head of the first round
+    uint32_t h, n;       // that head, rounds
   };
-  auto load = [&](uint32_t r) {
-    uint32_t kind;
-    const uint32_t h = place(r, kind);
-    const uint8_t* src = kind == 0u   ? a.q + t * a.q_stride
-                         : kind == 1u ? a.kx + t * a.kv_stride
-                                      : a.vx + t * a.kv_stride;
+  auto part = [&](const uint8_t* base, uint32_t first, uint32_t rounds) {
+    const uint32_t lo = max(r0, first), hi = min(r1, first + rounds);
+    const uint32_t h = (lo - first) * kSubs + sub;
+    return Part{base + h * row, h, hi > lo ? hi - lo : 0u};
+  };
+  const Part pq = part(a.q + t * a.q_stride, 0, nq);
+  const Part pk = part(a.kx + t * a.kv_stride, nq, nk);
+  const Part pv = part(a.vx + t * a.kv_stride, nq + nk, nk);
+  auto load = [&](const Part& p, uint32_t r, uint32_t heads) {
     uint4 x = make_uint4(0, 0, 0, 0);
-    if (r < r1 && mine && h < (kind == 0u ? a.Hq : a.g.H)) {
-      src += h * row;
+    if (r < p.n && mine && p.h + r * kSubs < heads) {
+      const uint8_t* src = p.src + (uint64_t)(r * kSubs) * row;
       const uint2 u = __ldcs(reinterpret_cast<const uint2*>(src + c0 * 2u));
       const uint2 v = __ldcs(reinterpret_cast<const uint2*>(src + c1 * 2u));
       x = make_uint4(u.x, u.y, v.x, v.y);
@@ -52,8 +55,9 @@ __global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_
     return x;
   };
   uint4 x[kAhead];
+  const Part& p0 = pq.n ? pq : pk.n ? pk : pv;
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) x[i] = load(r0 + i);
+  for (int i = 0; i < kAhead; ++i) x[i] = load(p0, i, pq.n ? a.Hq : a.g.H);
   // the norms' weights
   uint2 wq[2] = {}, wk[2] = {};
   if (a.q_norm && mine) {
@@ -84,72 +88,98 @@ __global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_
     ok = false;
     if (threadIdx.x == 0) set_status(a.g.status, IBP_ERANGE);
   }
-  float4 cc = make_float4(1.f, 1.f, 1.f, 1.f), ss = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 cc = make_float4(0.f, 0.f, 0.f, 0.f), ss = cc;
   if (a.cos_sin && ok && turned) {
     const float* cs = a.cos_sin + (uint64_t)pos * a.rot + lane * 4u;
     cc = __ldg(reinterpret_cast<const float4*>(cs));
     ss = __ldg(reinterpret_cast<const float4*>(cs + half));
   }
   const float inv_d = 1.f / (float)a.g.D;
-  for (uint32_t r = r0; r < r1; r += kAhead) {
+  // one kind's rounds: `first` says that their first heads are on their way already
+  auto go = [&](const Part& p, uint32_t heads, const bool turns, const bool normed,
+                const uint2 (&w)[2], uint8_t* dst, uint64_t head_stride, const bool zero,
+                const bool first) {
+    if (p.n == 0) return;
+    if (!first)
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (r + i >= r1) break;
-      uint32_t kind;
-      const uint32_t h = place(r + i, kind);
-      uint4 y = x[i];
-      x[i] = load(r + i + kAhead);
-      const bool normed = kind == 0u ? a.q_norm != nullptr : kind == 1u && a.k_norm;
-      if (kind != 2u && (normed || a.cos_sin)) {  // the same for the whole CTA
-        float f[8];
-        {
-          const float2 f0 = unpack2(y.x, kBf16), f1 = unpack2(y.y, kBf16),
-                       f2 = unpack2(y.z, kBf16), f3 = unpack2(y.w, kBf16);
-          f[0] = f0.x, f[1] = f0.y, f[2] = f1.x, f[3] = f1.y;
-          f[4] = f2.x, f[5] = f2.y, f[6] = f3.x, f[7] = f3.y;
-        }
-        if (normed) {
-          float sum = 0.f;
+      for (int i = 0; i < kAhead; ++i) x[i] = load(p, i, heads);
+    dst += p.h * head_stride;
+    for (uint32_t r = 0; r < p.n; r += kAhead) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sum = fmaf(f[k], f[k], sum);
-#pragma unroll
-          for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-          const float n = rsqrtf(fmaf(sum, inv_d, a.eps));
-          const uint32_t gw[4] = {kind == 0u ? wq[0].x : wk[0].x, kind == 0u ? wq[0].y : wk[0].y,
-                                  kind == 0u ? wq[1].x : wk[1].x, kind == 0u ? wq[1].y : wk[1].y};
+      for (int i = 0; i < kAhead; ++i) {
+        if (r + i >= p.n) break;
+        uint4 y = x[i];
+        x[i] = load(p, r + i + kAhead, heads);
+        if (normed || turns) {  // the same for the whole CTA
+          const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
+          uint64_t f[4];  // two channels each
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float2 gf = unpack2(gw[k], kBf16);
-            f[2 * k] *= n * gf.x;
-            f[2 * k + 1] *= n * gf.y;
+            const float2 v = unpack2(yw[k], kBf16);
+            f[k] = pair2(v.x, v.y);
           }
-        }
-        if (turned) {
-          const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+          if (normed) {
+            uint64_t s2 = mul2(f[0], f[0]);
+#pragma unroll
+            for (int k = 1; k < 4; ++k) s2 = fma2(f[k], f[k], s2);
+            float sum, odd;
+            halves2(s2, sum, odd);
+            sum += odd;
+#pragma unroll
+            for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            const float n = rsqrtf(fmaf(sum, inv_d, a.eps));
+            const uint64_t n2 = pair2(n, n);
+            const uint32_t gw[4] = {w[0].x, w[0].y, w[1].x, w[1].y};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 gf = unpack2(gw[k], kBf16);
+              f[k] = mul2(f[k], mul2(n2, pair2(gf.x, gf.y)));
+            }
+          }
+          if (turns && turned) {
+            if (kPairs) {  // a pair of channels is a pair of the rotation
+              const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                float u, v;
+                halves2(f[k], u, v);
+                f[k] = fma2(f[k], pair2(c4[k], c4[k]), mul2(pair2(-v, u), pair2(s4[k], s4[k])));
+              }
+            } else {
+              const uint64_t c2[2] = {pair2(cc.x, cc.y), pair2(cc.z, cc.w)};
+              const uint64_t s2[2] = {pair2(ss.x, ss.y), pair2(ss.z, ss.w)};
+              const uint64_t m2[2] = {pair2(-ss.x, -ss.y), pair2(-ss.z, -ss.w)};
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint64_t u = f[k], v = f[k + 2];
+                f[k] = fma2(u, c2[k], mul2(v, m2[k]));
+                f[k + 2] = fma2(v, c2[k], mul2(u, s2[k]));
+              }
+            }
+          }
+          uint32_t z[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float& u = f[kPairs ? 2 * k : k];
-            float& v = f[kPairs ? 2 * k + 1 : k + 4];
-            const float u0 = u, v0 = v;
-            u = u0 * c4[k] - v0 * s4[k];
-            v = v0 * c4[k] + u0 * s4[k];
+            float u, v;
+            halves2(f[k], u, v);
+            z[k] = pack2(u, v, kBf16);
           }
+          y = make_uint4(z[0], z[1], z[2], z[3]);
         }
-        y = make_uint4(pack2(f[0], f[1], kBf16), pack2(f[2], f[3], kBf16),
-                       pack2(f[4], f[5], kBf16), pack2(f[6], f[7], kBf16));
-      }
-      if (mine && h < (kind == 0u ? a.Hq : a.g.H)) {
-        uint8_t* d = kind == 0u   ? a.q_out + t * a.qo_stride + h * row
-                     : kind == 1u ? kd + h * a.g.head_stride
-                                  : vd + h * a.g.head_stride;
-        if (kind == 0u && !ok) y = make_uint4(0, 0, 0, 0);
-        if (kind == 0u || ok) {
+        if (mine && p.h + (r + i) * kSubs < heads) {
+          uint8_t* d = dst + (uint64_t)((r + i) * kSubs) * head_stride;
+          if (zero) y = make_uint4(0, 0, 0, 0);
           *reinterpret_cast<uint2*>(d + c0 * 2u) = make_uint2(y.x, y.y);
           *reinterpret_cast<uint2*>(d + c1 * 2u) = make_uint2(y.z, y.w);
         }
       }
     }
-  }
+  };
+  const bool turns = a.cos_sin != nullptr;
+  go(pq, a.Hq, turns, a.q_norm != nullptr, wq, a.q_out + t * a.qo_stride, row, !ok, true);
+  if (!ok) return;
+  go(pk, a.g.H, turns, a.k_norm != nullptr, wk, kd, a.g.head_stride, false, pq.n == 0);
+  go(pv, a.g.H, false, false, wk, vd, a.g.head_stride, false, pq.n == 0 && pk.n == 0);
 }
 
 template <bool kBf16>

@@ -298,25 +298,6 @@ __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.al
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
 static_assert(8 * 208 + 4 * 88 <= 12 * 168, "no more registers than the launch has");
 
-// Two fp32 values at a time.
-__device__ __forceinline__ uint64_t pair2(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -876,8 +857,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t l0, l1, b2;
         auto weights = [&](const int j, uint32_t (&w2)[32]) {  // 4 keys
           float p0, p1, p2, p3;
-          split(fma2(pair2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), c2, b2), p0, p1);
-          split(fma2(pair2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3])), c2, b2), p2, p3);
+          halves2(fma2(pair2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), c2, b2), p0, p1);
+          halves2(fma2(pair2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3])), c2, b2), p2, p3);
           p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
           l0 = add2(l0, pair2(p0, p1));
           l1 = add2(l1, pair2(p2, p3));
@@ -935,7 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st32<0>(ts + 32u, pb);
         {
           float u, v;
-          split(add2(l0, l1), u, v);
+          halves2(add2(l0, l1), u, v);
           l += u + v;
         }
         arrive(p2_full + slot);

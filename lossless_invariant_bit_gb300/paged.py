@@ -29,6 +29,7 @@ import torch
 from . import ibp
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device
 
 
 # Attention's workspace of each (device, stream): calls on one stream follow one another.
@@ -36,7 +37,7 @@ _workspaces = {}
 
 
 def _workspace(device: torch.device, raw: int) -> torch.Tensor:
-    if torch.cuda.is_current_stream_capturing():  # a graph's replays may run on any stream
+    if torch._C._cuda_isCurrentStreamCapturing():  # a graph's replays may run on any stream
         return torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
     ws = _workspaces.get((device.index, raw))
     if ws is None:
@@ -101,7 +102,7 @@ class PagedCache:
             raise ValueError("k and v must have the same strides")
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.n_pages, self.dtype, self.k, self.v = n_pages, dtype, k, v
-        self.device = k.device
+        self.device, self._index = k.device, k.device.index
         # a dimension of one element has no stride to speak of
         row = head_dim * 2
         st = [s * 2 if n > 1 else max(s * 2, row) for s, n in zip(k.stride(), shape)]
@@ -153,15 +154,12 @@ class PagedCache:
         most max_q_tokens."""
         return PagedBatch(page_table, kv_lens, q_starts, n_tokens, max_q_tokens)
 
-    def _raw(self) -> int:
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
-
     def _heads(self, name: str, t: torch.Tensor, batch: PagedBatch, heads: Optional[int]) -> int:
         """Checks a [n_tokens, heads, head_dim] tensor; its token stride in bytes."""
         s, st = t.shape, t.stride()
         if (len(s) != 3 or s[0] != batch.n_tokens or s[2] != self.head_dim
-                or (heads is not None and s[1] != heads) or t.dtype != self.dtype or not t.is_cuda
-                or st[2] != 1 or (s[1] > 1 and st[1] != s[2])):
+                or t.dtype is not self.dtype or not t.is_cuda or st[2] != 1
+                or (heads is not None and s[1] != heads) or (s[1] > 1 and st[1] != s[2])):
             raise ValueError("%s must be a device tensor [n_tokens, heads, head_dim] of the "
                              "cache's type whose heads lie side by side" % name)
         return st[0] * 2 if s[0] > 1 else s[1] * s[2] * 2
@@ -185,12 +183,12 @@ class PagedCache:
             qs = self._heads("q", q, batch, None)
             heads = q.shape[1]
             if q_out is None:
-                q_out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=self.dtype,
-                                    device=self.device)
+                q_out = q.new_empty((batch.n_tokens, heads, self.head_dim))
                 os = heads * self.head_dim * 2
             else:
                 os = self._heads("q_out", q_out, batch, heads)
-        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+        for name, w in ((("q_norm", q_norm), ("k_norm", k_norm))
+                        if q_norm is not None or k_norm is not None else ()):
             if w is not None and (w.shape != (self.head_dim,) or w.dtype != self.dtype
                                   or not w.is_cuda or not w.is_contiguous()):
                 raise ValueError("%s must be [head_dim] of the cache's type" % name)
@@ -206,7 +204,7 @@ class PagedCache:
             heads, None if q_norm is None else q_norm.data_ptr(),
             None if k_norm is None else k_norm.data_ptr(), eps,
             None if cos_sin is None else cos_sin.data_ptr(), n_pos, rot, 1 if pairs else 0,
-            self._raw()), "ibp_paged_append")
+            _raw_stream(self._index)), "ibp_paged_append")
         return q_out
 
     def attention(self, batch: PagedBatch, q: torch.Tensor, scale: Optional[float] = None,
@@ -220,14 +218,12 @@ class PagedCache:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.attention(batch, q, scale, causal, window, pages, lse, out)
         qs = self._heads("q", q, batch, None)
-        heads, device = q.shape[1], self.device
+        heads = q.shape[1]
         if out is None:
-            out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=self.dtype,
-                              device=device)
+            out = q.new_empty((batch.n_tokens, heads, self.head_dim))
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and type")
-        total = (torch.empty((batch.n_tokens, heads), dtype=torch.float32, device=device)
-                 if lse else None)
+        total = q.new_empty((batch.n_tokens, heads), dtype=torch.float32) if lse else None
         n = 0
         if pages is not None:
             if (pages.dim() != 3 or pages.shape[:2] != (batch.n_tokens, self.kv_heads)
@@ -235,8 +231,8 @@ class PagedCache:
                     or not pages.is_contiguous()):
                 raise ValueError("pages must be a contiguous int32 [n_tokens, kv_heads, n]")
             n = pages.shape[2]
-        raw = self._raw()
-        ws = _workspace(device, raw)
+        raw = _raw_stream(self._index)
+        ws = _workspace(self.device, raw)
         ibp._check(self._lib.ibp_paged_attention(
             self.handle, batch.address, q.data_ptr(), qs, heads, out.data_ptr(),
             total.data_ptr() if lse else None,
@@ -260,7 +256,7 @@ class PagedCache:
                 return self.update_bounds(batch, bounds)
         self._bounds(bounds)
         ibp._check(self._lib.ibp_paged_bounds(self.handle, batch.address, bounds.data_ptr(),
-                                              self._raw()), "ibp_paged_bounds")
+                                              _raw_stream(self._index)), "ibp_paged_bounds")
 
     def page_scores(self, batch: PagedBatch, q: torch.Tensor, bounds: torch.Tensor,
                     out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -272,12 +268,12 @@ class PagedCache:
         qs = self._heads("q", q, batch, None)
         shape = (batch.n_tokens, self.kv_heads, batch.max_pages)
         if out is None:
-            out = torch.empty(shape, dtype=torch.float32, device=self.device)
+            out = q.new_empty(shape, dtype=torch.float32)
         elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous():
             raise ValueError("out must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
         ibp._check(self._lib.ibp_paged_scores(
             self.handle, batch.address, q.data_ptr(), qs, q.shape[1], bounds.data_ptr(),
-            out.data_ptr(), self._raw()), "ibp_paged_scores")
+            out.data_ptr(), _raw_stream(self._index)), "ibp_paged_scores")
         return out
 
     def select_pages(self, batch: PagedBatch, scores: torch.Tensor, n: int,
@@ -293,9 +289,9 @@ class PagedCache:
             raise ValueError("scores must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
         shape = (batch.n_tokens, self.kv_heads, n)
         if out is None:
-            out = torch.empty(shape, dtype=torch.int32, device=self.device)
+            out = scores.new_empty(shape, dtype=torch.int32)
         elif out.shape != shape or out.dtype != torch.int32 or not out.is_contiguous():
             raise ValueError("out must be a contiguous int32 [n_tokens, kv_heads, n]")
         ibp._check(self._lib.ibp_paged_select(self.handle, batch.address, scores.data_ptr(), n,
-                                              out.data_ptr(), self._raw()), "ibp_paged_select")
+                                              out.data_ptr(), _raw_stream(self._index)), "ibp_paged_select")
         return out
