@@ -457,7 +457,8 @@ IBP_API ibp_status ibp_project_compress(ibp_store* store, const void* x, uint64_
  * q_starts[s] are new; new token i (row q_starts[s] + i of the call's [n_tokens,
  * heads, head_dim] arrays) sits at position kv_lens[s] - (number of new
  * tokens) + i; rows of no sequence are left alone.  The arrays are read on the device, so a
- * captured call follows their contents.  Positions stay below 2^30.  A handle knows the geometry and owns a status word; it may be
+ * captured call follows their contents.  Positions stay below 2^30.  A handle
+ * knows the geometry and owns a status word; it may be
  * used on several streams at once.
  *
  * Errors that a kernel finds set the handle's status word: IBP_ERANGE for

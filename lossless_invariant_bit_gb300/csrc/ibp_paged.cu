@@ -14,11 +14,14 @@ namespace {
 // so that a rotation needs no other lane and the sum of squares one shuffle
 // tree.  A lane keeps its channels over all heads of a token, so the token's place,
 // its cosines and sines and the norms' weights are fetched once; kAhead heads are in
-// flight at a time.  Rounds of kSubs heads hold queries, keys or values alone.  Bound
-// by HBM (each byte is read and written once), with issue close behind: 90
-// instructions for the 16 bytes of a lane.
+// flight at a time.  Rounds of kSubs heads hold queries, keys or values alone.  HBM sets
+// the floor (each byte is read and written once) and the schedulers' issue the time, so
+// sums and products run on pairs of floats.  10 CTAs of 128 threads share an SM and three
+// heads are in flight per lane: 51 us for 5,900 tokens of 64 + 8 + 8 heads of 128
+// with both norms (243 MB, 4.8 TB/s); unbounded registers and four heads 62 us, 8 CTAs and
+// four 53, 12 CTAs and two 51, 16 CTAs (32 registers, spilled) 52 to 55.
 template <int kLanes, int kAhead, bool kBf16, bool kPairs>
-__global__ void __launch_bounds__(128) k_paged_append(PagedAppendArgs a, uint32_t per) {
+__global__ void __launch_bounds__(128, 10) k_paged_append(PagedAppendArgs a, uint32_t per) {
   constexpr uint32_t kSubs = 128u / kLanes;  // heads side by side
   const uint32_t lane = threadIdx.x & (kLanes - 1u), sub = threadIdx.x / kLanes;
   const uint32_t t = blockIdx.x;
@@ -471,7 +474,8 @@ __device__ __forceinline__ uint32_t select_row(const PagedGeom& g, const PagedBa
 // first are taken.  Bound by issue: 2 kPer instructions a count, 9 kPer to write the
 // numbers.  4 rows to a CTA when kWarps is 1.
 template <int kWarps, int kPer>
-__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32, kPer <= 16 ? 4 : kPer <= 32 && kWarps == 1 ? 6 : 1)
+__global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32,
+                                  kPer <= 16 ? 4 : kPer <= 32 && kWarps == 1 ? 6 : 1)
     k_paged_pick(PagedGeom g, PagedBatchView b, const float* scores, uint32_t n_sel,
                  int32_t* selected) {
   constexpr int kRowsPer = kWarps == 1 ? 4 : 1;
@@ -705,7 +709,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, int sm_count, cudaStre
   const uint32_t D_ = a.g.D;
   const bool bf_ = a.g.bf16 != 0u;
   // Rounds of a CTA: as many as leave 16 CTAs to each SM (a token's place is then looked up
-  // for more heads), 16 at most.
+  // for more heads), 16 at most.  At 5,900 tokens of 10 rounds: all of a token's in one CTA
+  // 51 us, 5 rounds 53, 3 rounds 64, 2 rounds 72.
   const uint64_t subs = 128u / pow2_lanes(D_);
   const uint64_t rounds = (a.Hq + subs - 1) / subs + 2u * ((a.g.H + subs - 1) / subs);
   uint64_t per = rounds * a.b.n_tokens / (16ull * sm_count);
@@ -717,8 +722,8 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, int sm_count, cudaStre
 #define IBP_CALL(L, B)                                                                    \
   do {                                                                                    \
     if (per >= 2u) {                                                                      \
-      if (a.pairs) k_paged_append<L, 4, B, true><<<grid, 128, 0, st>>>(a, (uint32_t)per); \
-      else k_paged_append<L, 4, B, false><<<grid, 128, 0, st>>>(a, (uint32_t)per);        \
+      if (a.pairs) k_paged_append<L, 3, B, true><<<grid, 128, 0, st>>>(a, (uint32_t)per); \
+      else k_paged_append<L, 3, B, false><<<grid, 128, 0, st>>>(a, (uint32_t)per);        \
     } else {                                                                              \
       if (a.pairs) k_paged_append<L, 1, B, true><<<grid, 128, 0, st>>>(a, (uint32_t)per); \
       else k_paged_append<L, 1, B, false><<<grid, 128, 0, st>>>(a, (uint32_t)per);        \
@@ -751,7 +756,7 @@ cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, con
   if (tiles > 0x7FFFFFFFull) return cudaErrorInvalidValue;
   // A row's groups of pages go to as many CTAs as the GPU holds at a time (three to an SM),
   // so that what a CTA looks up first is paid once: 16 tokens x 8 heads x 2048 pages in
-  // 34.9 us with a group to a warp.  (Tiles that hold rows: the numbers leave gaps.)
+  // 33.4 us; six to an SM 35.9, two 38.9, one 49.7.  (Tiles that hold rows: the numbers leave gaps.)
   const uint64_t full = b.n_tokens < (uint64_t)tpt * b.n_seqs
                             ? (b.n_tokens < b.n_seqs ? b.n_tokens : b.n_seqs)
                             : (b.n_tokens + tpt - 1u) / tpt;
@@ -784,7 +789,8 @@ cudaError_t launch_paged_select(const PagedGeom& g, const PagedBatchView& b, con
                                 uint32_t n_sel, int32_t* selected, int sm_count,
                                 cudaStream_t st) {
   // One warp to a row when there are rows for every SM's issue slots (16 warps) and its
-  // registers hold them; else 8 warps.
+  // registers hold them: 7960 rows of 1001 in 23 us, 67 with 8 warps to each.  Else 8
+  // warps: 128 rows of 2048 in 6.1 us, 9.1 with one.
   const uint64_t rows = (uint64_t)b.n_tokens * g.H;
   const uint32_t most = b.max_pages;
 #define IBP_PICK(W, P, BLOCKS)                                                             \

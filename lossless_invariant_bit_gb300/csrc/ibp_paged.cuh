@@ -41,7 +41,7 @@ struct PagedAttnArgs {
   uint32_t causal, window, G;
   const int32_t* selected;  // NULL or [n_tokens, H, n_sel]
   uint32_t n_sel;
-  uint32_t max_rows;        // rows of a sequence: the step kernel's most, one less than the chunk kernel's least
+  uint32_t max_rows;        // of a sequence: the step kernel's most, the chunk kernel takes more
   uint8_t* ws;
 };
 
@@ -71,7 +71,9 @@ cudaError_t launch_paged_select(const PagedGeom& g, const PagedBatchView& b, con
                                 uint32_t n_sel, int32_t* selected, int sm_count,
                                 cudaStream_t st);
 // Sequences with at most a.max_rows rows (new tokens x query heads of a K/V
-// head), or tokens with a page list each.
+// head), or tokens with a page list each.  At one row for each of 640 heads of 1984 keys
+// this kernel takes 104 us and the chunk kernel 158 (a tile of 128 rows computes 1);
+// past 16 rows a second tile would read the keys again.
 constexpr uint32_t kStepRows = 16;
 // behind: it may start while the chunk kernel of the same call ends.
 cudaError_t launch_paged_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count, bool behind,

@@ -29,6 +29,13 @@
 //
 // The blocks of all tiles are one list, cut into equal runs, one per CTA; a tile
 // that is cut is joined from its pieces by a second kernel, in order.
+//
+// Measured: 2048 tokens behind 6144, 64 query heads of 128 on 8, causal: 338 us, 1.43
+// PFLOP/s, bound by the scores' products (both operands from shared memory: 740 to
+// 830 cycles a block against 520 for the values') and the turns between the slots.
+// Without turns (both issuers at will) 438 us; a tile's memory released by the
+// tensor cores' own commits 338, by the waiting warp 346 to 357; weights written before
+// the turn is taken 345 to 365.
 #include "ibp_paged.cuh"
 #include "ibp_sm103.cuh"
 #include "ibp_tma.cuh"
@@ -555,7 +562,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool go = true;
       // S = Q K^T; the other slot's turn begins with the last of it, since a turn takes
       // as long to pass on as two products to run
-      auto release = [&](uint32_t e, bool twice) {  // once its products are done; twice: for both slots
+      // once its products are done; twice: for both slots
+      auto release = [&](uint32_t e, bool twice) {
         commit(empty + e % kRing);
         if (twice) commit(empty + e % kRing);
       };
@@ -858,7 +866,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto weights = [&](const int j, uint32_t (&w2)[32]) {  // 4 keys
           float p0, p1, p2, p3;
           halves2(fma2(pair2(__uint_as_float(sv[j]), __uint_as_float(sv[j + 1])), c2, b2), p0, p1);
-          halves2(fma2(pair2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3])), c2, b2), p2, p3);
+          halves2(fma2(pair2(__uint_as_float(sv[j + 2]), __uint_as_float(sv[j + 3])), c2, b2), p2,
+                  p3);
           p0 = ex2(p0), p1 = ex2(p1), p2 = ex2(p2), p3 = ex2(p3);
           l0 = add2(l0, pair2(p0, p1));
           l1 = add2(l1, pair2(p2, p3));

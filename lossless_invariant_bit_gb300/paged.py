@@ -183,7 +183,8 @@ class PagedCache:
             qs = self._heads("q", q, batch, None)
             heads = q.shape[1]
             if q_out is None:
-                q_out = q.new_empty((batch.n_tokens, heads, self.head_dim))
+                q_out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=q.dtype,
+                                    device=q.device)
                 os = heads * self.head_dim * 2
             else:
                 os = self._heads("q_out", q_out, batch, heads)
@@ -220,10 +221,12 @@ class PagedCache:
         qs = self._heads("q", q, batch, None)
         heads = q.shape[1]
         if out is None:
-            out = q.new_empty((batch.n_tokens, heads, self.head_dim))
+            out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=q.dtype,
+                              device=q.device)
         elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out must be contiguous, of q's shape and type")
-        total = q.new_empty((batch.n_tokens, heads), dtype=torch.float32) if lse else None
+        total = (torch.empty((batch.n_tokens, heads), dtype=torch.float32, device=q.device)
+                 if lse else None)
         n = 0
         if pages is not None:
             if (pages.dim() != 3 or pages.shape[:2] != (batch.n_tokens, self.kv_heads)
@@ -268,7 +271,7 @@ class PagedCache:
         qs = self._heads("q", q, batch, None)
         shape = (batch.n_tokens, self.kv_heads, batch.max_pages)
         if out is None:
-            out = q.new_empty(shape, dtype=torch.float32)
+            out = torch.empty(shape, dtype=torch.float32, device=q.device)
         elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous():
             raise ValueError("out must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
         ibp._check(self._lib.ibp_paged_scores(
@@ -289,7 +292,7 @@ class PagedCache:
             raise ValueError("scores must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
         shape = (batch.n_tokens, self.kv_heads, n)
         if out is None:
-            out = scores.new_empty(shape, dtype=torch.int32)
+            out = torch.empty(shape, dtype=torch.int32, device=scores.device)
         elif out.shape != shape or out.dtype != torch.int32 or not out.is_contiguous():
             raise ValueError("out must be a contiguous int32 [n_tokens, kv_heads, n]")
         ibp._check(self._lib.ibp_paged_select(self.handle, batch.address, scores.data_ptr(), n,
