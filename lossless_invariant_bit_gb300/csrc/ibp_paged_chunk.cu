@@ -27,10 +27,11 @@
 // A tile of at most 128 rows gives both slots the same rows, slot 0 the even
 // blocks of keys and slot 1 the odd ones, and joins them at its end.
 //
-// The blocks of all tiles are one list, cut into equal runs, one per CTA; a tile
-// that is cut is joined from its pieces by a second kernel, in order.
+// The blocks of all tiles, with some units in front of each for the tile itself, are one
+// list, cut into equal runs, one per CTA; a tile that is cut is joined from its pieces
+// by a second kernel, in order.
 //
-// Measured: 2048 tokens behind 6144, 64 query heads of 128 on 8, causal: 338 us, 1.43
+// Measured: 2048 tokens behind 6144, 64 query heads of 128 on 8, causal: 333 us, 1.45
 // PFLOP/s, bound by the scores' products (both operands from shared memory: 740 to
 // 830 cycles a block against 520 for the values') and the turns between the slots.
 // Without turns (both issuers at will) 438 us; a tile's memory released by the
@@ -45,6 +46,10 @@ namespace {
 
 constexpr uint32_t kRows = 128, kTileRows = 256, kKeys = 128, kRing = 5, kThreads = 384;
 constexpr uint32_t kMaxCtas = 192;
+// What a tile costs beside its blocks of keys, in blocks: its queries, its first scores and
+// its output take about 8000 cycles, a block 2800.  (24 sequences of 1 to 333 tokens, 32
+// heads of 64 on 4: 79.8 us; 85.7 with none, 81.0 with 6.)
+constexpr uint32_t kTileUnits = 3;
 constexpr uint64_t kWsBytes = IBP_PAGED_WORKSPACE_BYTES - kStepWsBytes;
 
 template <int kDP>
@@ -81,12 +86,12 @@ struct Tile {
   bool two;               // the slots take alternate blocks of the same rows
 };
 
-// The blocks of tile t of a sequence.
+// The blocks of a sequence's tile whose rows are of the tokens tok0 to tok1.
 __device__ __forceinline__ void tile_keys(const PagedAttnArgs& a, uint32_t n, uint32_t L,
-                                          uint32_t row0, uint32_t rows, uint32_t& lo,
+                                          uint32_t tok0, uint32_t tok1, uint32_t& lo,
                                           uint32_t& hi, uint32_t& b0, uint32_t& nb) {
-  const int64_t first = (int64_t)L - n + row0 / a.G;
-  const int64_t last = (int64_t)L - n + (row0 + rows - 1u) / a.G;
+  const int64_t first = (int64_t)L - n + tok0;
+  const int64_t last = (int64_t)L - n + tok1;
   const int64_t h = a.causal ? last + 1 : (int64_t)L;
   const int64_t l = a.window ? first + 1 - (int64_t)a.window : 0;
   hi = h < 0 ? 0u : (uint32_t)h;
@@ -96,15 +101,22 @@ __device__ __forceinline__ void tile_keys(const PagedAttnArgs& a, uint32_t n, ui
   nb = b1 > b0 ? b1 - b0 : 1u;
 }
 
-// Blocks of one head's tiles of a sequence.
-__device__ __forceinline__ uint64_t seq_blocks(const PagedAttnArgs& a, const PagedSeq& q) {
+// Units of one head's tiles of a sequence.
+__device__ __forceinline__ uint64_t seq_units(const PagedAttnArgs& a, const PagedSeq& q) {
   const uint32_t R = q.n * a.G;
   if (q.n == 0 || R <= a.max_rows) return 0;
+  // the tiles' first tokens without a division for each
+  const uint32_t per = kTileRows / a.G, rest = kTileRows % a.G;
   uint64_t sum = 0;
+  uint32_t tok = 0, odd = 0;  // row r is query `odd` of token `tok`
   for (uint32_t r = 0; r < R; r += kTileRows) {
+    uint32_t next = tok + per, more = odd + rest;
+    if (more >= a.G) more -= a.G, ++next;
     uint32_t lo, hi, b0, nb;
-    tile_keys(a, q.n, q.L, r, min(kTileRows, R - r), lo, hi, b0, nb);
-    sum += nb;
+    tile_keys(a, q.n, q.L, tok, R - r <= kTileRows ? q.n - 1u : next - (more == 0u), lo, hi, b0,
+              nb);
+    sum += nb + kTileUnits;
+    tok = next, odd = more;
   }
   return sum;
 }
@@ -112,7 +124,7 @@ __device__ __forceinline__ uint64_t seq_blocks(const PagedAttnArgs& a, const Pag
 __device__ __forceinline__ void set_tile(const PagedAttnArgs& a, Tile& t) {
   t.row0 = t.t * kTileRows;
   t.rows = min(kTileRows, t.n * a.G - t.row0);
-  tile_keys(a, t.n, t.L, t.row0, t.rows, t.lo, t.hi, t.b0, t.nb);
+  tile_keys(a, t.n, t.L, t.row0 / a.G, (t.row0 + t.rows - 1u) / a.G, t.lo, t.hi, t.b0, t.nb);
   t.two = t.rows <= kRows;
 }
 
@@ -142,8 +154,9 @@ __device__ __forceinline__ void next_tile(const PagedAttnArgs& a, Tile& t) {
 // A run of blocks of one tile: [blk, blk + count) of its t.nb.
 struct Walk {
   Tile t;
+  uint32_t at;  // the tile's unit at u
   uint32_t blk, count;
-  uint64_t u, u1;  // position in the list of blocks, end of this CTA's run
+  uint64_t u, u1;  // position in the list of units, end of this CTA's run
   bool fresh;
 };
 
@@ -177,14 +190,17 @@ __device__ __forceinline__ bool walk(const PagedAttnArgs& a, Walk& w) {
   if (w.u >= w.u1) return false;
   if (!w.fresh) {
     next_tile(a, w.t);
-    w.blk = 0;
+    w.at = 0;
   }
   w.fresh = false;
   const uint64_t left = w.u1 - w.u;
-  w.count = w.t.nb - w.blk;
-  if (w.count > left) w.count = (uint32_t)left;
-  w.u += w.count;
-  return true;
+  const uint32_t all = w.t.nb + kTileUnits - w.at;  // units of the tile that are left
+  const uint32_t take = all > left ? (uint32_t)left : all, to = w.at + take;
+  w.blk = w.at > kTileUnits ? w.at - kTileUnits : 0u;
+  w.count = to > kTileUnits ? to - kTileUnits - w.blk : 0u;
+  w.u += take;
+  w.at = to;
+  return w.count > 0;  // (a run that ends before a tile's first block has ended)
 }
 
 // The matrix instructions of a block, as one run of code: the whole warp comes here
@@ -376,12 +392,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // what comes behind may take the SMs that have ended (it waits for this grid itself)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // ---- the list of blocks and this CTA's run of it
-  uint64_t mine = 0, total = 0;
+  // ---- the list of units and this CTA's run of it
+  uint64_t mine = 0, total = 0, mine0 = 0;
   for (uint32_t s = tid; s < a.b.n_seqs; s += kThreads) {
     const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
     if (!q.ok) set_status(a.g.status, IBP_ERANGE);
-    mine += seq_blocks(a, q);
+    mine += seq_units(a, q);
+    if (s == tid) mine0 = mine;
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
@@ -400,8 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     w0.u1 = total * (blockIdx.x + 1u) / ctas;
     uint64_t base = 0;
     for (uint32_t c = 0; c < a.b.n_seqs; c += kThreads) {
-      uint64_t nb = 0;
-      if (c + tid < a.b.n_seqs) nb = seq_blocks(a, paged_seq(a.b, a.g.page_lg, c + tid));
+      uint64_t nb = mine0;
+      if (c) nb = c + tid < a.b.n_seqs ? seq_units(a, paged_seq(a.b, a.g.page_lg, c + tid)) : 0;
       uint64_t inc = nb;
 #pragma unroll
       for (uint32_t d = 1; d < 32u; d <<= 1) {
@@ -433,12 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t rem = in % per_head;
     w0.t.t = 0;
     set_tile(a, w0.t);
-    while (rem >= w0.t.nb) {
-      rem -= w0.t.nb;
+    while (rem >= w0.t.nb + kTileUnits) {
+      rem -= w0.t.nb + kTileUnits;
       ++w0.t.t;
       set_tile(a, w0.t);
     }
-    w0.blk = (uint32_t)rem;
+    w0.at = (uint32_t)rem;
     w0.u = u0;
     w0.fresh = true;
   }
@@ -462,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool more = walk(a, w);
       if (lane == 0) {
         Info* x = s_info + tiles % kInfos;
-        const uint64_t tile_u = w.u - w.count - w.blk;  // the tile's first block in the list
+        const uint64_t tile_u = w.u - w.at + kTileUnits;  // the tile's first block in the list
         const bool whole = w.blk == 0 && w.count == w.t.nb;
         x->count = more ? w.count : 0u;
         x->two = w.t.two;
@@ -476,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         x->hi = w.t.hi;
         x->key0 = (w.t.b0 + w.blk) * kKeys;
         x->whole = whole;
-        x->place = tile_u >= u0 ? 1u : 0u;
+        x->place = w.blk == 0u ? 1u : 0u;
         x->s = w.t.s;
         {
           const int32_t first = (int32_t)(w.t.L - w.t.n + w.t.row0 / a.G);
