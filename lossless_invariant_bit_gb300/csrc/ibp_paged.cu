@@ -216,6 +216,8 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
 template <int kLanes, bool kBf16>
 __global__ void __launch_bounds__(128)
     k_paged_bounds(PagedGeom g, PagedBatchView b, uint8_t* bounds) {
+  // the scores' CTAs may come up beside this kernel (they wait for its end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t lane = threadIdx.x & 31u, sub = lane & (kLanes - 1u), row = lane / kLanes;
   const uint64_t id = (uint64_t)blockIdx.x * 4u + (threadIdx.x >> 5);
   const uint32_t tile = (uint32_t)(id / g.H), h = (uint32_t)(id % g.H);
@@ -294,6 +296,7 @@ __global__ void __launch_bounds__(128, 3)
   constexpr int kC = kDP / 32;  // 16-byte chunks per lane
   extern __shared__ __align__(128) uint8_t s_bounds[];
   __shared__ float s_c[4][16][kScoreGroup + 1];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
   const uint32_t quad = lane & 3u, r0 = lane >> 2;
   const uint32_t tpt = G >= 16u ? 1u : 16u / G;  // tokens of a tile
@@ -765,14 +768,23 @@ cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, con
   const uint64_t per = (groups + 4u * z - 1) / (4u * z);
   z = (groups + 4u * per - 1) / (4u * per);
   if (z > 65535u) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)tiles, g.H, (unsigned)z);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)tiles, g.H, (unsigned)z);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
 #define IBP_SCORES(B, DP)                                                                    \
   do {                                                                                       \
     const cudaError_t e =                                                                    \
         smem_limit(reinterpret_cast<const void*>(k_paged_scores<B, DP>), score_smem<DP>());  \
     if (e != cudaSuccess) return e;                                                          \
-    k_paged_scores<B, DP><<<grid, 128, 4u * kScoreGroup * (g.D * 4u + 16u), st>>>(           \
-        g, b, q, q_stride, G, bounds, scores, (uint32_t)per);                                \
+    cfg.dynamicSmemBytes = 4u * kScoreGroup * (g.D * 4u + 16u);                              \
+    return cudaLaunchKernelEx(&cfg, k_paged_scores<B, DP>, g, b, q, q_stride, G, bounds,     \
+                              scores, (uint32_t)per);                                        \
   } while (0)
   if (g.D <= 64u) {
     if (g.bf16) IBP_SCORES(true, 64);

@@ -1054,8 +1054,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Joins the pieces of the tile that CTA blockIdx.x of the first kernel ended, in the
 // pieces' order: 32 rows per CTA (lane = row), 16 channels per warp.
 template <int kDP, bool kBf16>
-__global__ void __launch_bounds__(kDP * 2) k_paged_chunk_join(PagedAttnArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void join_tile(const PagedAttnArgs& a) {
   const Join* joins = reinterpret_cast<const Join*>(a.ws + IBP_PAGED_WORKSPACE_BYTES -
                                                     kMaxCtas * sizeof(Join));
   const Piece<kDP>* pieces = reinterpret_cast<const Piece<kDP>*>(a.ws + kStepWsBytes);
@@ -1097,6 +1096,16 @@ __global__ void __launch_bounds__(kDP * 2) k_paged_chunk_join(PagedAttnArgs a) {
   dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
   dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
   if (a.lse && d0 == 0) a.lse[at] = some ? (mx + log2f(ll)) * 0.69314718056f : -INFINITY;
+}
+
+// Behind the step kernel's join (max_rows is set) every piece is there when this starts,
+// since that join lets it start after its own wait: it waits at its end, so that what
+// follows may count on both.
+template <int kDP, bool kBf16>
+__global__ void __launch_bounds__(kDP * 2) k_paged_chunk_join(PagedAttnArgs a) {
+  if (!a.max_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
+  join_tile<kDP, kBf16>(a);
+  if (a.max_rows) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int kDP, bool kBf16>

@@ -674,6 +674,8 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
 template <int kDP, bool kBf16>
 __global__ void __launch_bounds__(128) k_paged_step_join(PagedAttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  // from here the chunk kernel's join may run beside this one
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const Join* joins =
       reinterpret_cast<const Join*>(a.ws + kStepWsBytes - kMaxCtas * sizeof(Join));
   const Piece<kDP>* pieces = reinterpret_cast<const Piece<kDP>*>(a.ws);
