@@ -200,6 +200,20 @@ def test_attention_cut_tiles(q_lens, kv_lens, G, H, D):
         attend(Setup(q_lens, kv_lens, G=G, H=H, D=D, dtype=dtype, seed=len(q_lens)))
 
 
+@pytest.mark.parametrize("q_lens,kv_lens,G,H,window", [
+    ([17] * 61, [17 + 5 * i for i in range(61)], 1, 3, 0),   # tiles of one to three blocks
+    ([20] * 450, [20 + 7 * i % 200 for i in range(450)], 1, 1, 0),  # more than a CTA has threads
+    ([90, 1, 45, 18], [90, 700, 1900, 18], 11, 2, 0),        # G that divides no tile
+    ([150, 33], [4000, 50], 13, 1, 300),
+])
+def test_attention_of_many_short_tiles(q_lens, kv_lens, G, H, window):
+    """Each tile stands for some blocks more than it has in the list that is cut
+    into runs: runs end before a tile's first block, and with it."""
+    for D, dtype in ((64, torch.float16), (128, torch.bfloat16)):
+        attend(Setup(q_lens, kv_lens, G=G, H=H, D=D, dtype=dtype, seed=len(q_lens) + G),
+               window=window)
+
+
 def test_attention_large_scores_move_the_reference():
     """Keys that grow along the sequence: the running maximum outgrows every
     reference taken before, by far."""
