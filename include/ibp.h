@@ -550,7 +550,9 @@ IBP_API ibp_status ibp_paged_append(const ibp_paged* cache, const ibp_paged_batc
  *        K/V head h sees only the keys of the pages selected[i][h][...] (numbers
  *        of the sequence's pages, no page twice; negative entries and those
  *        beyond the row's position are passed over).  Causal, without window.
- *   workspace  device, IBP_PAGED_WORKSPACE_BYTES, 16-byte aligned
+ *   workspace  device, IBP_PAGED_WORKSPACE_BYTES, 16-byte aligned: the call's until its
+ *        work is done.  Calls on one stream may share one, from several threads too
+ *        (they are enqueued one after the other); calls on different streams may not
  * Scores, softmax and sums in fp32, the weights rounded to the 16-bit type
  * before they multiply the values.  Errors: IBP_EINVAL, IBP_EALIGN,
  * IBP_ECUDA; a device wait that gave up sets IBP_ETIMEOUT. */

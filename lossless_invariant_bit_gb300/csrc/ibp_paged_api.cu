@@ -65,6 +65,22 @@ void give_status(int device, int at) {
 
 }  // namespace
 
+// The launches of one attention call hand pieces to each other through its workspace, so
+// calls that share one (several threads on one stream) are enqueued one after the other:
+// a lock for each workspace, found by its address.
+namespace {
+
+constexpr size_t kLocks = 256;
+std::mutex g_call_mu[kLocks];
+
+std::mutex& call_lock(const void* workspace) {
+  uint64_t x = reinterpret_cast<uintptr_t>(workspace);
+  x = (x >> 4) * 0x9E3779B97F4A7C15ull;  // (workspaces lie far apart: the upper bits tell)
+  return g_call_mu[x >> 56];
+}
+
+}  // namespace
+
 struct ibp_paged {
   int status_at;
   ibp::PagedGeom g;
@@ -276,6 +292,7 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
   const bool few = selected || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
   const bool both = !few && b->n_seqs > 1u;
   a.max_rows = few || both ? ibp::kStepRows : 0u;
+  std::lock_guard<std::mutex> lock(call_lock(workspace));
   cudaError_t ce = few ? cudaSuccess : ibp::launch_paged_chunk(a, c->maps, c->sm_count, st);
   if (ce == cudaSuccess && (few || both))
     ce = ibp::launch_paged_step(a, c->maps, c->sm_count, both, st);

@@ -32,7 +32,8 @@ _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 _raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device
 
 
-# Attention's workspace of each (device, stream): calls on one stream follow one another.
+# Attention's workspace of each (device, stream): calls on one stream follow one another
+# there, and the library enqueues those of several threads one after the other.
 _workspaces = {}
 
 
@@ -41,8 +42,8 @@ def _workspace(device: torch.device, raw: int) -> torch.Tensor:
         return torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
     ws = _workspaces.get((device.index, raw))
     if ws is None:
-        ws = torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device)
-        _workspaces[device.index, raw] = ws
+        ws = _workspaces.setdefault((device.index, raw), torch.empty(
+            ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8, device=device))
     return ws
 
 
