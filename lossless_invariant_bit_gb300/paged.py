@@ -54,7 +54,8 @@ def _as_stream(stream) -> torch.cuda.Stream:
 class PagedBatch:
     """The sequences of one step; keeps its tensors alive."""
 
-    __slots__ = ("desc", "address", "page_table", "kv_lens", "q_starts", "n_tokens", "max_pages")
+    __slots__ = ("desc", "address", "page_table", "kv_lens", "q_starts", "n_tokens", "max_pages",
+                 "index")
 
     def __init__(self, page_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor,
                  n_tokens: int, max_q_tokens: int):
@@ -62,6 +63,9 @@ class PagedBatch:
         for name, t in (("page_table", page_table), ("kv_lens", kv_lens), ("q_starts", q_starts)):
             if t.dtype != torch.int32 or not t.is_cuda:
                 raise ValueError("%s must be an int32 device tensor" % name)
+        self.index = kv_lens.get_device()
+        if page_table.get_device() != self.index or q_starts.get_device() != self.index:
+            raise ValueError("page_table, kv_lens and q_starts must be on one device")
         if (page_table.dim() != 2 or page_table.shape[0] != n or q_starts.numel() != n + 1
                 or not kv_lens.is_contiguous() or not q_starts.is_contiguous()
                 or (page_table.shape[1] > 1 and page_table.stride(1) != 1)):
@@ -99,8 +103,8 @@ class PagedCache:
             if tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or t.stride(3) != 1:
                 raise ValueError("k and v must be device tensors [n_pages, page_tokens, kv_heads, "
                                  "head_dim] of the cache's type, each head contiguous")
-        if k.stride() != v.stride():
-            raise ValueError("k and v must have the same strides")
+        if k.stride() != v.stride() or k.device != v.device:
+            raise ValueError("k and v must have the same strides and device")
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.n_pages, self.dtype, self.k, self.v = n_pages, dtype, k, v
         self.device, self._index = k.device, k.device.index
@@ -147,6 +151,13 @@ class PagedCache:
         return self._rows(self.v)
 
     # -- calls
+    def _here(self, *tensors) -> None:
+        """Batches and tensors that are not on the cache's device are refused (a kernel
+        would take their addresses for this device's)."""
+        for t in tensors:
+            if (t.index if type(t) is PagedBatch else t.get_device()) != self._index:
+                raise ValueError("every tensor must be on the cache's device, %s" % self.device)
+
     def batch(self, page_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor,
               n_tokens: int, max_q_tokens: int) -> PagedBatch:
         """A step's sequences: page_table [n, pages], kv_lens [n] (tokens in the
@@ -159,10 +170,10 @@ class PagedCache:
         """Checks a [n_tokens, heads, head_dim] tensor; its token stride in bytes."""
         s, st = t.shape, t.stride()
         if (len(s) != 3 or s[0] != batch.n_tokens or s[2] != self.head_dim
-                or t.dtype is not self.dtype or not t.is_cuda or st[2] != 1
+                or t.dtype is not self.dtype or t.get_device() != self._index or st[2] != 1
                 or (heads is not None and s[1] != heads) or (s[1] > 1 and st[1] != s[2])):
-            raise ValueError("%s must be a device tensor [n_tokens, heads, head_dim] of the "
-                             "cache's type whose heads lie side by side" % name)
+            raise ValueError("%s must be a tensor [n_tokens, heads, head_dim] of the cache's type "
+                             "and device whose heads lie side by side" % name)
         return st[0] * 2 if s[0] > 1 else s[1] * s[2] * 2
 
     def append(self, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor,
@@ -176,6 +187,7 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.append(batch, k, v, q, q_norm, k_norm, eps, cos_sin, pairs, q_out)
+        self._here(batch)
         ks = self._heads("k", k, batch, self.kv_heads)
         if self._heads("v", v, batch, self.kv_heads) != ks:
             raise ValueError("k and v must have the same token stride")
@@ -192,11 +204,12 @@ class PagedCache:
         for name, w in ((("q_norm", q_norm), ("k_norm", k_norm))
                         if q_norm is not None or k_norm is not None else ()):
             if w is not None and (w.shape != (self.head_dim,) or w.dtype != self.dtype
-                                  or not w.is_cuda or not w.is_contiguous()):
-                raise ValueError("%s must be [head_dim] of the cache's type" % name)
+                                  or w.get_device() != self._index or not w.is_contiguous()):
+                raise ValueError("%s must be [head_dim] of the cache's type and device" % name)
         n_pos = rot = 0
         if cos_sin is not None:
-            if (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_cuda
+            self._here(cos_sin)
+            if (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32
                     or not cos_sin.is_contiguous()):
                 raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim]")
             n_pos, rot = cos_sin.shape
@@ -219,20 +232,21 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.attention(batch, q, scale, causal, window, pages, lse, out)
+        self._here(batch)
         qs = self._heads("q", q, batch, None)
         heads = q.shape[1]
         if out is None:
             out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=q.dtype,
                               device=q.device)
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-            raise ValueError("out must be contiguous, of q's shape and type")
+        elif out.get_device() != self._index or out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+            raise ValueError("out must be contiguous, of q's shape, type and device")
         total = (torch.empty((batch.n_tokens, heads), dtype=torch.float32, device=q.device)
                  if lse else None)
         n = 0
         if pages is not None:
+            self._here(pages)
             if (pages.dim() != 3 or pages.shape[:2] != (batch.n_tokens, self.kv_heads)
-                    or pages.dtype != torch.int32 or not pages.is_cuda
-                    or not pages.is_contiguous()):
+                    or pages.dtype != torch.int32 or not pages.is_contiguous()):
                 raise ValueError("pages must be a contiguous int32 [n_tokens, kv_heads, n]")
             n = pages.shape[2]
         raw = _raw_stream(self._index)
@@ -246,9 +260,9 @@ class PagedCache:
         return (out, total) if lse else out
 
     def _bounds(self, bounds: torch.Tensor) -> None:
+        self._here(bounds)
         if (bounds.shape != (self.n_pages, self.kv_heads, 2, self.head_dim)
-                or bounds.dtype != self.dtype or not bounds.is_cuda
-                or not bounds.is_contiguous()):
+                or bounds.dtype != self.dtype or not bounds.is_contiguous()):
             raise ValueError("bounds must be a contiguous [n_pages, kv_heads, 2, head_dim] of the "
                              "cache's type")
 
@@ -258,6 +272,7 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.update_bounds(batch, bounds)
+        self._here(batch)
         self._bounds(bounds)
         ibp._check(self._lib.ibp_paged_bounds(self.handle, batch.address, bounds.data_ptr(),
                                               _raw_stream(self._index)), "ibp_paged_bounds")
@@ -268,13 +283,16 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.page_scores(batch, q, bounds, out)
+        self._here(batch)
         self._bounds(bounds)
         qs = self._heads("q", q, batch, None)
         shape = (batch.n_tokens, self.kv_heads, batch.max_pages)
         if out is None:
             out = torch.empty(shape, dtype=torch.float32, device=q.device)
-        elif out.shape != shape or out.dtype != torch.float32 or not out.is_contiguous():
-            raise ValueError("out must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
+        elif (out.get_device() != self._index or out.shape != shape or out.dtype != torch.float32
+              or not out.is_contiguous()):
+            raise ValueError("out must be a contiguous float32 [n_tokens, kv_heads, max_pages] on "
+                             "the cache's device")
         ibp._check(self._lib.ibp_paged_scores(
             self.handle, batch.address, q.data_ptr(), qs, q.shape[1], bounds.data_ptr(),
             out.data_ptr(), _raw_stream(self._index)), "ibp_paged_scores")
@@ -287,15 +305,17 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.select_pages(batch, scores, n, out)
+        self._here(batch, scores)
         if (scores.shape != (batch.n_tokens, self.kv_heads, batch.max_pages)
-                or scores.dtype != torch.float32 or not scores.is_cuda
-                or not scores.is_contiguous()):
+                or scores.dtype != torch.float32 or not scores.is_contiguous()):
             raise ValueError("scores must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
         shape = (batch.n_tokens, self.kv_heads, n)
         if out is None:
             out = torch.empty(shape, dtype=torch.int32, device=scores.device)
-        elif out.shape != shape or out.dtype != torch.int32 or not out.is_contiguous():
-            raise ValueError("out must be a contiguous int32 [n_tokens, kv_heads, n]")
+        elif (out.get_device() != self._index or out.shape != shape or out.dtype != torch.int32
+              or not out.is_contiguous()):
+            raise ValueError("out must be a contiguous int32 [n_tokens, kv_heads, n] on the "
+                             "cache's device")
         ibp._check(self._lib.ibp_paged_select(self.handle, batch.address, scores.data_ptr(), n,
                                               out.data_ptr(), _raw_stream(self._index)), "ibp_paged_select")
         return out
