@@ -84,7 +84,8 @@ class PagedCache:
     (any strides of whole heads; allocated when not given).
 
     Calls run on the current stream, or on `stream` (a torch stream or a
-    cudaStream_t), on which their outputs and workspaces are then allocated too."""
+    cudaStream_t), on which their outputs and workspaces are then allocated too.
+    The pages' device has to be the current one."""
 
     def __init__(self, kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
                  dtype: torch.dtype = torch.bfloat16, k: Optional[torch.Tensor] = None,
@@ -112,9 +113,10 @@ class PagedCache:
         row = head_dim * 2
         st = [s * 2 if n > 1 else max(s * 2, row) for s, n in zip(k.stride(), shape)]
         self._lib = ibp._lib_handle()
-        self.handle = ibp.ibp_paged_create(ibp.ibp_paged_desc(
-            k.data_ptr(), v.data_ptr(), st[0], st[2], st[1], n_pages, page_tokens, kv_heads,
-            head_dim, _DTYPES[dtype]))
+        with torch.cuda.device(self._index):  # the handle belongs to the pages' device
+            self.handle = ibp.ibp_paged_create(ibp.ibp_paged_desc(
+                k.data_ptr(), v.data_ptr(), st[0], st[2], st[1], n_pages, page_tokens, kv_heads,
+                head_dim, _DTYPES[dtype]))
 
     # -- lifetime
     def close(self) -> None:

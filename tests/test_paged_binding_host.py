@@ -1,5 +1,7 @@
 """PagedCache's checks of its arguments, without a GPU: tensors that only say what
 they are, and a library that counts its calls."""
+import contextlib
+
 import pytest
 import torch
 
@@ -59,6 +61,7 @@ def lib(monkeypatch):
     monkeypatch.setattr(ibp, "_lib_handle", lambda: fake)
     monkeypatch.setattr(ibp, "ibp_paged_create", lambda desc: 1)
     monkeypatch.setattr(ibp, "ibp_paged_destroy", lambda h: None)
+    monkeypatch.setattr(torch.cuda, "device", lambda index: contextlib.nullcontext())
     monkeypatch.setattr(paged, "_raw_stream", lambda index: 0)
     monkeypatch.setattr(paged, "_workspace", lambda device, raw: Said((16,), torch.uint8))
     return fake
@@ -122,6 +125,26 @@ def test_calls_refuse_what_is_elsewhere(lib, name, which, index):
     with pytest.raises(ValueError):
         call(a_cache(), arguments(**{which: index}))
     assert not lib.called
+
+
+def test_the_handle_is_made_on_the_pages_device(lib, monkeypatch):
+    current, made = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            current.append(self.index)
+
+        def __exit__(self, *exc):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(ibp, "ibp_paged_create", lambda desc: made.append(current[-1]) or 1)
+    a_cache(k=1, v=1)
+    a_cache()
+    assert made == [1, 0] and current == [0]
 
 
 @pytest.mark.parametrize("kw", [dict(table=1), dict(lens=1), dict(starts=1), dict(table=-1)])
