@@ -327,6 +327,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// A barrier of the slots' eight warps, and whether all of them say so.
+__device__ __forceinline__ bool all_of_eight(bool mine) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
+      " barrier.cta.red.and.pred q, 2, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(all)
+      : "r"((uint32_t)mine)
+      : "memory");
+  return all != 0u;
+}
+
 template <int kDP, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     k_paged_chunk(const __grid_constant__ CUtensorMap map_k,
@@ -346,8 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_full = turn + 2;       // the tile's queries are there
   uint64_t* o_full = q_full + 1;     // every product of the tile is done
   uint64_t* done = o_full + 1;       // per slot, after a failure: its products are done
-  uint64_t* ended = done + 2;        // both slots' warps have ended the tile
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(ended + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 2);
   uint32_t* s_fail = s_tmem + 1;
   uint32_t* s_bad = s_fail + 1;      // 8 blocks: bit per page with an id out of range
   __shared__ Info s_info[kInfos];
@@ -377,7 +388,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (uint32_t i = 0; i < kInfos; ++i) mbar_init(info_full + i, 1);
     mbar_init(q_full, 8);
     mbar_init(o_full, 2);
-    mbar_init(ended, 8);
     *s_fail = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -813,10 +823,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     uint32_t sn = 0, tiles = 0, blocks = 0, e0 = 0;
-    bool go = true;
-    while (go) {
+    while (true) {
+      bool go = true;
       const Info* t = info_of(tiles);
-      if (!t) break;
+      if (!t) {
+        all_of_eight(false);
+        break;
+      }
       load_q(t);
       const bool both = t->two != 0u;
       const uint32_t count = t->count;
@@ -952,11 +965,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       e0 += 2u * count;
       go = go && wait_or_fail(o_full, tiles & 1u, s_fail);
       ++tiles;
-      // both slots say that they are here before either counts on the other below
-      if (go && lane == 0) mbar_arrive(ended);
-      __syncwarp();
-      go = go && wait_or_fail(ended, (tiles - 1u) & 1u, s_fail);
-      if (!go) break;
+      // The slots count on each other below: all eight warps go on, or all leave.  (Each
+      // comes here, also one that gave up a wait which another saw end.)
+      if (!all_of_eight(go)) break;
       tc_after();
       const bool whole = t->whole != 0u;
       const Odd& odd = s_odd[(tiles - 1u) & 1u];
