@@ -361,6 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 2);
   uint32_t* s_fail = s_tmem + 1;
   uint32_t* s_bad = s_fail + 1;      // 8 blocks: bit per page with an id out of range
+  uint32_t* s_loads = s_bad + 8;     // ring entries that were filled
   __shared__ Info s_info[kInfos];
   __shared__ uint64_t info_full[kInfos];
   __shared__ Odd s_odd[2];  // of this tile and the next
@@ -562,11 +563,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0) joins[blockIdx.x] = join;
-    // after a failure: the copies in flight land (or their waits give up too)
-    if (!go)
-      for (uint32_t i = e > kRing ? e - kRing : 0u; i < e; ++i)
-        mbar_wait(full + i % kRing, (i / kRing) & 1u);
+    if (lane == 0) {
+      joins[blockIdx.x] = join;
+      *s_loads = e;
+    }
   } else if (warp == 9 || warp == 10) {
     reg_dec();
     // ---------------- a slot's matrix products
@@ -659,10 +659,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit(o_full);
         e0 += 2u * nb;
         ++tiles;
-      }
-      if (!go) {  // products in flight finish before the tensor memory goes
-        commit(done + slot);
-        mbar_wait(done + slot, 0);
       }
     }
   } else if (warp == 11) {
@@ -1056,6 +1052,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
+  // After a failure, whosever it was: the copies in flight land and the products end
+  // before the shared and the tensor memory go (or these waits give up too).
+  if (*s_fail) {
+    if (warp == 8) {
+      const uint32_t e = *s_loads;
+      for (uint32_t i = e > kRing ? e - kRing : 0u; i < e; ++i)
+        mbar_wait(full + i % kRing, (i / kRing) & 1u);
+    } else if (warp == 9 || warp == 10) {
+      commit(done + (warp - 9u));
+      mbar_wait(done + (warp - 9u), 0);
+    }
+    __syncthreads();
+  }
   if (warp == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                  : "memory");

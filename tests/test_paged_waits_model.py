@@ -1,7 +1,8 @@
 """How warps that wait on one another leave the attention kernel of chunks when a wait
 gives up, as a model: every interleaving of the warps' steps, every wait that is not
 over free to give up.  A barrier has no limit of its own, so none may be left with a warp
-in it and another gone."""
+in it and another gone; and a CTA whose waits gave up waits once more for the copies that
+it has asked for (again with a limit) before it leaves."""
 import pytest
 
 TILES = 2
@@ -112,3 +113,49 @@ def test_every_warp_leaves_after_the_last_tile():
         w, new = next(iter(moves(state)))
         state = tuple(new if i == w else s for i, s in enumerate(state))
     assert all(s[1] == TILES for s in state)
+
+
+def left_with_copies(blocks, ring, drain):
+    """Whether a CTA can leave with a copy in flight for which no wait was begun.  A
+    producer asks for `blocks` copies into `ring` places, a consumer takes them in order;
+    any wait that is not over may give up, and sets the CTA's word of failure.
+    drain(producer_failed, failed): whether the last `ring` copies are waited for before
+    the CTA leaves."""
+    # asked, landed, taken, producer: go / failed / done, consumer: the same
+    start = (0, 0, 0, "go", "go")
+    seen, todo = {start}, [start]
+    while todo:
+        asked, landed, taken, prod, cons = todo.pop()
+        failed = "failed" in (prod, cons)
+        after = []
+        if landed < asked:
+            after.append((asked, landed + 1, taken, prod, cons))
+        if prod == "go":
+            if asked == blocks:
+                after.append((asked, landed, taken, "done", cons))
+            elif asked - taken < ring:
+                after.append((asked + 1, landed, taken, prod, cons))
+            else:
+                after.append((asked, landed, taken, "failed", cons))
+        if cons == "go":
+            if taken == blocks:
+                after.append((asked, landed, taken, prod, "done"))
+            elif landed > taken:
+                after.append((asked, landed, taken + 1, prod, cons))
+            else:
+                after.append((asked, landed, taken, prod, "failed"))
+        if prod != "go" and cons != "go" and landed < asked:
+            if not drain(prod == "failed", failed):
+                return True
+        for x in after:
+            if x not in seen:
+                seen.add(x)
+                todo.append(x)
+    return False
+
+
+@pytest.mark.parametrize("blocks,ring", [(1, 3), (3, 3), (7, 3), (9, 5)])
+def test_copies_in_flight_are_waited_for(blocks, ring):
+    assert not left_with_copies(blocks, ring, lambda producer, anyone: anyone)
+    # the planted mistake: only where the producer itself gave up
+    assert left_with_copies(blocks, ring, lambda producer, anyone: producer)
