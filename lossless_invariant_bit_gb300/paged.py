@@ -48,7 +48,10 @@ def _workspace(device: torch.device, raw: int) -> torch.Tensor:
 
 
 def _as_stream(stream) -> torch.cuda.Stream:
-    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if not isinstance(stream, int):
+        return stream
+    # (an ExternalStream of 0 is a new stream, not the default one)
+    return torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
 
 
 class PagedBatch:

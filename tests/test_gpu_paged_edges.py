@@ -5,6 +5,7 @@ import threading
 import pytest
 import torch
 
+from lossless_invariant_bit_gb300 import paged
 from tests.test_gpu_paged import Setup
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +36,13 @@ def test_two_threads_on_one_stream():
         t.join()
     assert not wrong
     assert all(st.cache.status() == 0 for st in sets)
+
+
+def test_stream_handle_zero_is_the_default_stream():
+    assert paged._as_stream(0).cuda_stream == 0
+    side = torch.cuda.Stream()
+    assert paged._as_stream(side.cuda_stream).cuda_stream == side.cuda_stream
+    assert paged._as_stream(side) is side
+    st = Setup([1, 9], [40, 30], G=2, D=64)
+    want = st.cache.attention(st.batch, st.q)
+    assert torch.equal(st.cache.attention(st.batch, st.q, stream=0), want)
