@@ -200,6 +200,8 @@ class PagedCache:
         if q is not None:
             qs = self._heads("q", q, batch, None)
             heads = q.shape[1]
+            if heads == 0:
+                raise ValueError("q has no heads")
             if q_out is None:
                 q_out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=q.dtype,
                                     device=q.device)
@@ -218,6 +220,8 @@ class PagedCache:
                     or not cos_sin.is_contiguous()):
                 raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim]")
             n_pos, rot = cos_sin.shape
+            if n_pos == 0 or rot == 0:  # its null pointer would say that there is none
+                raise ValueError("cos_sin has no elements")
         ibp._check(self._lib.ibp_paged_append(
             self.handle, batch.address, k.data_ptr(), v.data_ptr(), ks,
             None if q is None else q.data_ptr(), qs, None if q is None else q_out.data_ptr(), os,
@@ -254,6 +258,8 @@ class PagedCache:
                     or pages.dtype != torch.int32 or not pages.is_contiguous()):
                 raise ValueError("pages must be a contiguous int32 [n_tokens, kv_heads, n]")
             n = pages.shape[2]
+            if n == 0:  # its null pointer would say that there are no lists
+                raise ValueError("pages lists no pages")
         raw = _raw_stream(self._index)
         ws = _workspace(self.device, raw)
         ibp._check(self._lib.ibp_paged_attention(

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from lossless_invariant_bit_gb300 import paged
+from tests.gpu_util import DEV
 from tests.test_gpu_paged import Setup
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +47,18 @@ def test_stream_handle_zero_is_the_default_stream():
     st = Setup([1, 9], [40, 30], G=2, D=64)
     want = st.cache.attention(st.batch, st.q)
     assert torch.equal(st.cache.attention(st.batch, st.q, stream=0), want)
+
+
+def test_empty_arguments_are_not_absent_ones():
+    """A tensor without elements has a null pointer, which tells the library that it
+    was not given: attention over no pages is not attention over every key."""
+    st = Setup([2], [40], G=2, D=64, poison=False)
+    k = torch.zeros((2, 2, 64), dtype=st.dtype, device=DEV)
+    with pytest.raises(ValueError):
+        st.cache.attention(st.batch, st.q, pages=torch.zeros((2, 2, 0), dtype=torch.int32,
+                                                             device=DEV))
+    for shape in ((0, 64), (64, 0)):
+        with pytest.raises(ValueError):
+            st.cache.append(st.batch, k, k, q=st.q, cos_sin=torch.zeros(shape, device=DEV))
+    with pytest.raises(ValueError):
+        st.cache.append(st.batch, k, k, q=st.q[:, :0])
