@@ -156,13 +156,8 @@ class PagedCache:
         return self._rows(self.v)
 
     # -- calls
-    def _here(self, *tensors) -> None:
-        """Batches and tensors that are not on the cache's device are refused (a kernel
-        would take their addresses for this device's)."""
-        for t in tensors:
-            if (t.index if type(t) is PagedBatch else t.get_device()) != self._index:
-                raise ValueError("every tensor must be on the cache's device, %s" % self.device)
-
+    # Tensors that are not on the cache's device are refused: a kernel would take their
+    # addresses for this device's.
     def batch(self, page_table: torch.Tensor, kv_lens: torch.Tensor, q_starts: torch.Tensor,
               n_tokens: int, max_q_tokens: int) -> PagedBatch:
         """A step's sequences: page_table [n, pages], kv_lens [n] (tokens in the
@@ -174,11 +169,11 @@ class PagedCache:
     def _heads(self, name: str, t: torch.Tensor, batch: PagedBatch, heads: Optional[int]) -> int:
         """Checks a [n_tokens, heads, head_dim] tensor; its token stride in bytes."""
         s, st = t.shape, t.stride()
-        if (len(s) != 3 or s[0] != batch.n_tokens or s[2] != self.head_dim
+        if (batch.index != self._index or len(s) != 3 or s[0] != batch.n_tokens or s[2] != self.head_dim
                 or t.dtype is not self.dtype or t.get_device() != self._index or st[2] != 1
                 or (heads is not None and s[1] != heads) or (s[1] > 1 and st[1] != s[2])):
             raise ValueError("%s must be a tensor [n_tokens, heads, head_dim] of the cache's type "
-                             "and device whose heads lie side by side" % name)
+                             "and device (as the batch) whose heads lie side by side" % name)
         return st[0] * 2 if s[0] > 1 else s[1] * s[2] * 2
 
     def append(self, batch: PagedBatch, k: torch.Tensor, v: torch.Tensor,
@@ -192,7 +187,6 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.append(batch, k, v, q, q_norm, k_norm, eps, cos_sin, pairs, q_out)
-        self._here(batch)
         ks = self._heads("k", k, batch, self.kv_heads)
         if self._heads("v", v, batch, self.kv_heads) != ks:
             raise ValueError("k and v must have the same token stride")
@@ -215,10 +209,10 @@ class PagedCache:
                 raise ValueError("%s must be [head_dim] of the cache's type and device" % name)
         n_pos = rot = 0
         if cos_sin is not None:
-            self._here(cos_sin)
             if (cos_sin.dim() != 2 or cos_sin.dtype != torch.float32
-                    or not cos_sin.is_contiguous()):
-                raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim]")
+                    or cos_sin.get_device() != self._index or not cos_sin.is_contiguous()):
+                raise ValueError("cos_sin must be a contiguous float32 [positions, rot_dim] on "
+                                 "the cache's device")
             n_pos, rot = cos_sin.shape
             if n_pos == 0 or rot == 0:  # its null pointer would say that there is none
                 raise ValueError("cos_sin has no elements")
@@ -241,7 +235,6 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.attention(batch, q, scale, causal, window, pages, lse, out)
-        self._here(batch)
         qs = self._heads("q", q, batch, None)
         heads = q.shape[1]
         if out is None:
@@ -253,10 +246,11 @@ class PagedCache:
                  if lse else None)
         n = 0
         if pages is not None:
-            self._here(pages)
             if (pages.dim() != 3 or pages.shape[:2] != (batch.n_tokens, self.kv_heads)
-                    or pages.dtype != torch.int32 or not pages.is_contiguous()):
-                raise ValueError("pages must be a contiguous int32 [n_tokens, kv_heads, n]")
+                    or pages.dtype != torch.int32 or pages.get_device() != self._index
+                    or not pages.is_contiguous()):
+                raise ValueError("pages must be a contiguous int32 [n_tokens, kv_heads, n] on the "
+                                 "cache's device")
             n = pages.shape[2]
             if n == 0:  # its null pointer would say that there are no lists
                 raise ValueError("pages lists no pages")
@@ -270,12 +264,13 @@ class PagedCache:
             ibp.PAGED_WORKSPACE_BYTES, raw), "ibp_paged_attention")
         return (out, total) if lse else out
 
-    def _bounds(self, bounds: torch.Tensor) -> None:
-        self._here(bounds)
-        if (bounds.shape != (self.n_pages, self.kv_heads, 2, self.head_dim)
-                or bounds.dtype != self.dtype or not bounds.is_contiguous()):
+    def _bounds(self, batch: PagedBatch, bounds: torch.Tensor) -> None:
+        if (batch.index != self._index
+                or bounds.shape != (self.n_pages, self.kv_heads, 2, self.head_dim)
+                or bounds.dtype != self.dtype or bounds.get_device() != self._index
+                or not bounds.is_contiguous()):
             raise ValueError("bounds must be a contiguous [n_pages, kv_heads, 2, head_dim] of the "
-                             "cache's type")
+                             "cache's type and device (as the batch)")
 
     def update_bounds(self, batch: PagedBatch, bounds: torch.Tensor, stream=None) -> None:
         """Smallest and largest keys of the pages that the new tokens went into,
@@ -283,8 +278,7 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.update_bounds(batch, bounds)
-        self._here(batch)
-        self._bounds(bounds)
+        self._bounds(batch, bounds)
         ibp._check(self._lib.ibp_paged_bounds(self.handle, batch.address, bounds.data_ptr(),
                                               _raw_stream(self._index)), "ibp_paged_bounds")
 
@@ -294,8 +288,7 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.page_scores(batch, q, bounds, out)
-        self._here(batch)
-        self._bounds(bounds)
+        self._bounds(batch, bounds)
         qs = self._heads("q", q, batch, None)
         shape = (batch.n_tokens, self.kv_heads, batch.max_pages)
         if out is None:
@@ -316,10 +309,11 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.select_pages(batch, scores, n, out)
-        self._here(batch, scores)
-        if (scores.shape != (batch.n_tokens, self.kv_heads, batch.max_pages)
-                or scores.dtype != torch.float32 or not scores.is_contiguous()):
-            raise ValueError("scores must be a contiguous float32 [n_tokens, kv_heads, max_pages]")
+        if (batch.index != self._index or scores.shape != (batch.n_tokens, self.kv_heads, batch.max_pages)
+                or scores.dtype != torch.float32 or scores.get_device() != self._index
+                or not scores.is_contiguous()):
+            raise ValueError("scores must be a contiguous float32 [n_tokens, kv_heads, max_pages] "
+                             "on the cache's device (as the batch)")
         shape = (batch.n_tokens, self.kv_heads, n)
         if out is None:
             out = torch.empty(shape, dtype=torch.int32, device=scores.device)
