@@ -169,8 +169,8 @@ class PagedCache:
     def _heads(self, name: str, t: torch.Tensor, batch: PagedBatch, heads: Optional[int]) -> int:
         """Checks a [n_tokens, heads, head_dim] tensor; its token stride in bytes."""
         s, st = t.shape, t.stride()
-        if (batch.index != self._index or len(s) != 3 or s[0] != batch.n_tokens or s[2] != self.head_dim
-                or t.dtype is not self.dtype or t.get_device() != self._index or st[2] != 1
+        if (batch.index != self._index or len(s) != 3 or s[0] != batch.n_tokens
+                or s[2] != self.head_dim or t.dtype is not self.dtype or t.get_device() != self._index or st[2] != 1
                 or (heads is not None and s[1] != heads) or (s[1] > 1 and st[1] != s[2])):
             raise ValueError("%s must be a tensor [n_tokens, heads, head_dim] of the cache's type "
                              "and device (as the batch) whose heads lie side by side" % name)
@@ -240,7 +240,8 @@ class PagedCache:
         if out is None:
             out = torch.empty((batch.n_tokens, heads, self.head_dim), dtype=q.dtype,
                               device=q.device)
-        elif out.get_device() != self._index or out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        elif (out.get_device() != self._index or out.shape != q.shape or out.dtype != q.dtype
+              or not out.is_contiguous()):
             raise ValueError("out must be contiguous, of q's shape, type and device")
         total = (torch.empty((batch.n_tokens, heads), dtype=torch.float32, device=q.device)
                  if lse else None)
@@ -309,7 +310,8 @@ class PagedCache:
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.select_pages(batch, scores, n, out)
-        if (batch.index != self._index or scores.shape != (batch.n_tokens, self.kv_heads, batch.max_pages)
+        if (batch.index != self._index
+                or scores.shape != (batch.n_tokens, self.kv_heads, batch.max_pages)
                 or scores.dtype != torch.float32 or scores.get_device() != self._index
                 or not scores.is_contiguous()):
             raise ValueError("scores must be a contiguous float32 [n_tokens, kv_heads, max_pages] "
@@ -322,5 +324,6 @@ class PagedCache:
             raise ValueError("out must be a contiguous int32 [n_tokens, kv_heads, n] on the "
                              "cache's device")
         ibp._check(self._lib.ibp_paged_select(self.handle, batch.address, scores.data_ptr(), n,
-                                              out.data_ptr(), _raw_stream(self._index)), "ibp_paged_select")
+                                              out.data_ptr(), _raw_stream(self._index)),
+                   "ibp_paged_select")
         return out
