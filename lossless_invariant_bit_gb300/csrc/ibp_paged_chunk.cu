@@ -357,11 +357,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* turn = p2_full + 2;      // per slot: the other has issued its products
   uint64_t* q_full = turn + 2;       // the tile's queries are there
   uint64_t* o_full = q_full + 1;     // every product of the tile is done
-  uint64_t* done = o_full + 1;       // per slot, after a failure: its products are done
+  uint64_t* done = o_full + 1;       // per slot: its last products are done
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(done + 2);
   uint32_t* s_fail = s_tmem + 1;
   uint32_t* s_bad = s_fail + 1;      // 8 blocks: bit per page with an id out of range
-  uint32_t* s_loads = s_bad + 8;     // ring entries that were filled
   __shared__ Info s_info[kInfos];
   __shared__ uint64_t info_full[kInfos];
   __shared__ Odd s_odd[2];  // of this tile and the next
@@ -563,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (lane == 0) {
-      joins[blockIdx.x] = join;
-      *s_loads = e;
-    }
+    if (lane == 0) joins[blockIdx.x] = join;
+    // whosever wait gave up: the copies in flight land (or these waits give up too)
+    for (uint32_t i = e > kRing ? e - kRing : 0u; i < e; ++i)
+      mbar_wait(full + i % kRing, (i / kRing) & 1u);
   } else if (warp == 9 || warp == 10) {
     reg_dec();
     // ---------------- a slot's matrix products
@@ -660,6 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         e0 += 2u * nb;
         ++tiles;
       }
+      // whosever wait gave up: products in flight end before the tensor memory goes
+      commit(done + slot);
+      mbar_wait(done + slot, 0);
     }
   } else if (warp == 11) {
     reg_dec();
@@ -1052,19 +1054,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_before();
   __syncthreads();
   tc_after();
-  // After a failure, whosever it was: the copies in flight land and the products end
-  // before the shared and the tensor memory go (or these waits give up too).
-  if (*s_fail) {
-    if (warp == 8) {
-      const uint32_t e = *s_loads;
-      for (uint32_t i = e > kRing ? e - kRing : 0u; i < e; ++i)
-        mbar_wait(full + i % kRing, (i / kRing) & 1u);
-    } else if (warp == 9 || warp == 10) {
-      commit(done + (warp - 9u));
-      mbar_wait(done + (warp - 9u), 0);
-    }
-    __syncthreads();
-  }
   if (warp == 9)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                  : "memory");

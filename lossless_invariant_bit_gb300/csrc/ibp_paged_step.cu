@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
   __shared__ uint64_t s_found[2];
   __shared__ uint32_t s_pos[S::kStages][16];  // first position of each box of a block
   __shared__ Info s_info[kInfos];
-  __shared__ uint32_t s_fail, s_loads;  // a wait gave up; blocks that were asked for
+  __shared__ uint32_t s_fail;
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, tid = threadIdx.x;
   float* merge = reinterpret_cast<float*>(smem + S::kRing);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kRing + S::kMerge);
@@ -408,10 +408,11 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
       }
       u += count;
     }
-    if (lane == 0) {
-      joins[blockIdx.x] = join;
-      s_loads = blocks;
-    }
+    if (lane == 0) joins[blockIdx.x] = join;
+    // whosever wait gave up: the copies in flight land before the CTA leaves (or these
+    // waits give up too)
+    for (uint32_t i = blocks > S::kStages ? blocks - S::kStages : 0u; i < blocks; ++i)
+      mbar_wait(full + i % S::kStages, (i / S::kStages) & 1u);
   } else {
     // ---------------- 32 keys of each block
     const uint32_t r0 = lane >> 2, quad = lane & 3u;
@@ -662,15 +663,7 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
     }
   }
   __syncthreads();
-  if (s_fail) {
-    // whosever wait it was: the copies in flight land before the CTA leaves (or these
-    // waits give up too)
-    if (warp == kWarps)
-      for (uint32_t i = s_loads > S::kStages ? s_loads - S::kStages : 0u; i < s_loads; ++i)
-        mbar_wait(full + i % S::kStages, (i / S::kStages) & 1u);
-    if (tid == 0) set_status(a.g.status, IBP_ETIMEOUT);
-    __syncthreads();
-  }
+  if (tid == 0 && s_fail) set_status(a.g.status, IBP_ETIMEOUT);
   // launched behind the chunk kernel of the same call, it ends after it: what follows
   // this kernel may count on both
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -170,7 +170,8 @@ class PagedCache:
         """Checks a [n_tokens, heads, head_dim] tensor; its token stride in bytes."""
         s, st = t.shape, t.stride()
         if (batch.index != self._index or len(s) != 3 or s[0] != batch.n_tokens
-                or s[2] != self.head_dim or t.dtype is not self.dtype or t.get_device() != self._index or st[2] != 1
+                or s[2] != self.head_dim or t.dtype is not self.dtype
+                or t.get_device() != self._index or st[2] != 1
                 or (heads is not None and s[1] != heads) or (s[1] > 1 and st[1] != s[2])):
             raise ValueError("%s must be a tensor [n_tokens, heads, head_dim] of the cache's type "
                              "and device (as the batch) whose heads lie side by side" % name)

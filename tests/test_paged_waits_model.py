@@ -1,8 +1,8 @@
 """How warps that wait on one another leave the attention kernel of chunks when a wait
 gives up, as a model: every interleaving of the warps' steps, every wait that is not
 over free to give up.  A barrier has no limit of its own, so none may be left with a warp
-in it and another gone; and a CTA whose waits gave up waits once more for the copies that
-it has asked for (again with a limit) before it leaves."""
+in it and another gone; and a CTA waits for the copies that it has asked for (again with a
+limit) before it leaves, whoever gave up."""
 import pytest
 
 TILES = 2
@@ -156,6 +156,6 @@ def left_with_copies(blocks, ring, drain):
 
 @pytest.mark.parametrize("blocks,ring", [(1, 3), (3, 3), (7, 3), (9, 5)])
 def test_copies_in_flight_are_waited_for(blocks, ring):
-    assert not left_with_copies(blocks, ring, lambda producer, anyone: anyone)
+    assert not left_with_copies(blocks, ring, lambda producer, anyone: True)
     # the planted mistake: only where the producer itself gave up
     assert left_with_copies(blocks, ring, lambda producer, anyone: producer)
