@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
       uint32_t qf[kKs][4];
       float o[2 * kKs][4];
       float m[2], l[2];
-      bool bad = false;
+      bool bad[2] = {false, false};  // rows that see a page that cannot be read
 #pragma unroll
       for (int e = 0; e < 2; ++e) {  // the tile's queries, as the left operand
         const uint32_t r = r0 + 8u * e;
@@ -462,9 +462,20 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
         {
           const uint32_t at = warp * kWarpKeys + lane;
           const uint32_t first = s_pos[st][at >> box_lg];
-          if (first == kBadPage) {
-            set_status(a.g.status, IBP_ERANGE);
-            bad = true;
+          const uint32_t own = key0 + lane;  // (without a page list)
+          const uint32_t lost = __ballot_sync(
+              0xFFFFFFFFu, first == kBadPage && (kSel || (own < L && own >= lo)));
+          if (lost) {
+            if (lane == 0) set_status(a.g.status, IBP_ERANGE);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // those of its keys that the row sees
+              const int32_t pos = (int32_t)(L - n + (row0 + r0 + 8u * e) / a.G);
+              const int32_t end = kSel || !a.causal ? 32 : pos + 1 - (int32_t)key0;
+              const int32_t from = a.window ? pos + 1 - (int32_t)a.window - (int32_t)key0 : 0;
+              const uint32_t below = end <= 0 ? 0u : end >= 32 ? ~0u : (1u << end) - 1u;
+              const uint32_t above = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
+              bad[e] = bad[e] || (lost & below & above) != 0u;
+            }
           }
           const uint32_t key = first + (at & ((1u << box_lg) - 1u));
           there = __ballot_sync(0xFFFFFFFFu, first < kBadPage && key < L && key >= lo);
@@ -613,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
         __syncwarp();  // every lane has read the block
         if (lane == 0) mbar_arrive(empty + st);
       }
-      if (!go) bad = true;
+      if (!go) bad[0] = bad[1] = true;
       // ---- end of the tile, or of this CTA's run: join the four warps
       float* mw = merge + warp * 16u * (kDP + 4u);
 #pragma unroll
@@ -621,20 +632,22 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
         l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
         l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
         float* row = mw + (r0 + 8u * e) * (kDP + 4u);
-        if (quad == 0) row[kDP] = m[e], row[kDP + 1] = l[e];
+        if (quad == 0) row[kDP] = m[e], row[kDP + 1] = l[e], row[kDP + 2] = bad[e] ? 1.f : 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * kKs; ++i)
           *reinterpret_cast<float2*>(row + 8 * i + 2u * quad) =
               make_float2(o[i][2 * e], o[i][2 * e + 1]);
       }
-      const bool isbad = any_of_four(bad);
+      asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
       Piece<kDP>* piece = pieces + 2u * blockIdx.x + t->place;
       for (uint32_t r = warp; r < rows; r += kWarps) {
         float mm[kWarps], mx = -INFINITY, ll = 0.f, ov[kDP / 32];
+        bool isbad = false;
 #pragma unroll
         for (uint32_t w = 0; w < kWarps; ++w) {
           mm[w] = merge[(w * 16u + r) * (kDP + 4u) + kDP];
           mx = fmaxf(mx, mm[w]);
+          isbad = isbad || merge[(w * 16u + r) * (kDP + 4u) + kDP + 2u] != 0.f;
         }
         const float base = mx == -INFINITY ? 0.f : mx;
 #pragma unroll

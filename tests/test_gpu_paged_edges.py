@@ -1,11 +1,12 @@
 """The paged K/V cache at its edges, against plain 64-bit implementations with the
 bounds of test_gpu_paged.py."""
+import math
 import threading
 
 import pytest
 import torch
 
-from lossless_invariant_bit_gb300 import paged
+from lossless_invariant_bit_gb300 import ibp, paged
 from tests.gpu_util import DEV
 from tests.test_gpu_paged import Setup
 
@@ -62,3 +63,51 @@ def test_empty_arguments_are_not_absent_ones():
             st.cache.append(st.batch, k, k, q=st.q, cos_sin=torch.zeros(shape, device=DEV))
     with pytest.raises(ValueError):
         st.cache.append(st.batch, k, k, q=st.q[:, :0])
+
+
+# 4 new tokens at positions 30 to 33 of pages of 16: the last page begins with the third of
+# them.  4 x 4 rows of a K/V head go to the step kernel, 4 x 16 to the chunk kernel.
+@pytest.mark.parametrize("G", [1, 4, 16, 40])
+@pytest.mark.parametrize("bad", [-1, 1 << 20])
+def test_a_bad_page_zeroes_only_rows_that_see_it(G, bad):
+    for window, page, need in ((0, 2, [2, 3]), (0, 0, [0, 1, 2, 3]), (16, 0, [0]),
+                               (18, 0, [0, 1, 2]), (15, 0, [])):
+        st = Setup([4, 1], [34, 50], G=G, D=64, P=16, seed=G)
+        want, lse0 = st.cache.attention(st.batch, st.q, lse=True, window=window)
+        st.table[0, page] = bad
+        out, lse = st.cache.attention(st.batch, st.q, lse=True, window=window)
+        assert st.cache.status() == (ibp.IBP_ERANGE if need else ibp.IBP_OK)
+        for t in range(5):
+            if t in need:
+                assert not bool(out[t].any()) and bool((lse[t] == -math.inf).all()), (window, t)
+            else:
+                assert torch.equal(out[t], want[t]) and torch.equal(lse[t], lse0[t]), (window, t)
+
+
+@pytest.mark.parametrize("G,n,bad", [(4, 4, 1), (4, 4, 1249), (8, 30, 1), (8, 30, 1249)])
+def test_a_bad_page_of_a_cut_tile_zeroes_only_rows_that_see_it(G, n, bad):
+    """The sequence's blocks are cut over all CTAs: pieces that saw the page and pieces
+    that did not are joined.  Pages from `bad` on are out of range."""
+    L = 20002
+    st = Setup([n], [L], G=G, H=1, D=128, P=16, dtype=torch.bfloat16, seed=G)
+    want, lse0 = st.cache.attention(st.batch, st.q, lse=True)
+    first = (L - n) // 16 + 1 if bad > 1 else 1  # the first page that begins among new tokens
+    see = torch.arange(L - n, L, device=DEV) >= first * 16
+    assert bool(see.any())
+    st.table[0, first:] = -1
+    out, lse = st.cache.attention(st.batch, st.q, lse=True)
+    assert st.cache.status() == ibp.IBP_ERANGE
+    assert not bool(out[see].any()) and bool((lse[see] == -math.inf).all())
+    assert torch.equal(out[~see], want[~see]) and torch.equal(lse[~see], lse0[~see])
+
+
+def test_a_bad_page_of_a_list_zeroes_its_token():
+    st = Setup([3, 1], [60, 50], G=20, D=64, P=16, seed=2)
+    pages = torch.tensor([[0, 2], [1, 3], [0, 1], [0, 3]], dtype=torch.int32, device=DEV)
+    pages = pages[:, None].expand(4, 2, 2).contiguous()
+    want = st.cache.attention(st.batch, st.q, pages=pages)
+    st.table[0, 3] = -1
+    out = st.cache.attention(st.batch, st.q, pages=pages)
+    assert st.cache.status() == ibp.IBP_ERANGE
+    assert not bool(out[1].any())
+    assert all(torch.equal(out[t], want[t]) for t in (0, 2, 3))
