@@ -456,7 +456,8 @@ IBP_API ibp_status ibp_project_compress(ibp_store* store, const void* x, uint64_
  * kv_lens[s] tokens in the cache, of which the last q_starts[s + 1] -
  * q_starts[s] are new; new token i (row q_starts[s] + i of the call's [n_tokens,
  * heads, head_dim] arrays) sits at position kv_lens[s] - (number of new
- * tokens) + i; rows of no sequence are left alone.  The arrays are read on the device, so a
+ * tokens) + i (before the first position where kv_lens[s] is smaller: such a token sees
+ * no key, and is not appended); rows of no sequence are left alone.  The arrays are read on the device, so a
  * captured call follows their contents.  Positions stay below 2^30.  A handle
  * knows the geometry and owns a status word; it may be
  * used on several streams at once.

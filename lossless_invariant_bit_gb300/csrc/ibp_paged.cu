@@ -75,8 +75,8 @@ __global__ void __launch_bounds__(128, 10) k_paged_append(PagedAppendArgs a, uin
   const uint32_t s = paged_find(a.b, t);
   if (s == a.b.n_seqs) return;  // a row of no sequence
   const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
-  const uint32_t pos = q.L - q.n + (t - q.q0);
-  bool ok = q.ok && q.L >= q.n && (!a.cos_sin || pos < a.n_pos);
+  const uint32_t pos = q.L - q.n + (t - q.q0);  // (as a signed number: negative before the first)
+  bool ok = q.ok && (int32_t)pos >= 0 && (!a.cos_sin || pos < a.n_pos);
   uint8_t *kd = nullptr, *vd = nullptr;
   if (ok) {
     const int32_t page = __ldg(a.b.table + s * a.b.table_stride + (pos >> a.g.page_lg));
@@ -225,12 +225,13 @@ __global__ void __launch_bounds__(128)
   uint32_t first;
   const uint32_t s = paged_find_tile(b, P, 2u, tile, first);
   const PagedSeq q = paged_seq(b, g.page_lg, s);
-  if (!q.ok || q.L < q.n) {
+  if (!q.ok) {
     if (lane == 0) set_status(g.status, IBP_ERANGE);
     return;
   }
-  if (q.n == 0 || tile < first) return;
-  const uint32_t p = ((q.L - q.n) >> g.page_lg) + (tile - first);
+  if (q.n == 0 || q.L == 0 || tile < first) return;
+  const uint32_t from = q.L > q.n ? q.L - q.n : 0u;  // the first new token that has a position
+  const uint32_t p = (from >> g.page_lg) + (tile - first);
   if (p > (q.L - 1u) >> g.page_lg) return;
   const int32_t page = __ldg(b.table + s * b.table_stride + p);
   if (page < 0 || (uint32_t)page >= g.n_pages) {

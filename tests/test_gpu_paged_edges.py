@@ -8,7 +8,7 @@ import torch
 
 from lossless_invariant_bit_gb300 import ibp, paged
 from tests.gpu_util import DEV
-from tests.test_gpu_paged import Setup
+from tests.test_gpu_paged import Setup, near, rope_table, turn
 
 pytestmark = pytest.mark.gpu
 
@@ -111,3 +111,38 @@ def test_a_bad_page_of_a_list_zeroes_its_token():
     assert st.cache.status() == ibp.IBP_ERANGE
     assert not bool(out[1].any())
     assert all(torch.equal(out[t], want[t]) for t in (0, 2, 3))
+
+
+def test_append_and_bounds_with_tokens_before_the_first_position():
+    """More new tokens than the sequence has positions: the tokens at positions 0 on
+    are appended (attention, scores and selection serve them), the others refused."""
+    q_lens, kv_lens, G, D, P = [5, 3, 2, 20], [2, 0, 40, 19], 2, 64, 8
+    st = Setup(q_lens, kv_lens, G=G, D=D, P=P, seed=1, poison=False)
+    H, T = st.H, st.T
+    k = torch.randn((T, H, D), generator=st.g, device=DEV).to(st.dtype)
+    v = torch.randn((T, H, D), generator=st.g, device=DEV).to(st.dtype)
+    cs = rope_table(64, D)
+    kb, vb = st.k.clone(), st.v.clone()
+    q = st.cache.append(st.batch, k, v, q=st.q, cos_sin=cs)
+    assert st.cache.status() == ibp.IBP_ERANGE
+    wrote = torch.zeros((st.n_pages, P), dtype=torch.bool, device=DEV)
+    for s, (n, L) in enumerate(zip(q_lens, kv_lens)):
+        lo, before = st.starts[s], max(0, n - L)
+        assert not bool(q[lo:lo + before].any())
+        pos = torch.arange(L - n + before, L, device=DEV)
+        rows = slice(lo + before, lo + n)
+        page, slot = st.table[s, pos // P].long(), pos % P
+        wrote[page, slot] = True
+        near(q[rows], *turn(st.q[rows], None, cs[pos], D, False), st.dtype, D)
+        near(st.k[page, slot], *turn(k[rows], None, cs[pos], D, False), st.dtype, D)
+        assert torch.equal(st.v[page, slot], v[rows])
+    assert torch.equal(st.k[~wrote], kb[~wrote]) and torch.equal(st.v[~wrote], vb[~wrote])
+    bounds = torch.full((st.n_pages, H, 2, D), 7.0, dtype=st.dtype, device=DEV)
+    ref = bounds.clone()
+    st.cache.update_bounds(st.batch, bounds)
+    assert st.cache.status() == ibp.IBP_OK
+    for s, (n, L) in enumerate(zip(q_lens, kv_lens)):
+        for p in range(max(0, L - n) // P, -(-L // P)):
+            kk = st.k[st.table[s, p].long()][:min(P, L - p * P)]
+            ref[st.table[s, p].long()] = torch.stack([kk.amin(0), kk.amax(0)], 1)
+    assert torch.equal(bounds, ref)
