@@ -555,7 +555,8 @@ IBP_API ibp_status ibp_paged_append(const ibp_paged* cache, const ibp_paged_batc
  *        work is done.  Calls on one stream may share one, from several threads too
  *        (they are enqueued one after the other); calls on different streams may not
  * Scores, softmax and sums in fp32, the weights rounded to the 16-bit type
- * before they multiply the values.  Errors: IBP_EINVAL, IBP_EALIGN,
+ * before they multiply the values (weights down to 2^-25 of a row's largest with the
+ * type's full precision).  Errors: IBP_EINVAL, IBP_EALIGN,
  * IBP_ECUDA; a device wait that gave up sets IBP_ETIMEOUT. */
 IBP_API ibp_status ibp_paged_attention(const ibp_paged* cache, const ibp_paged_batch* batch,
                                        const void* q, uint64_t q_token_stride, uint32_t q_heads,

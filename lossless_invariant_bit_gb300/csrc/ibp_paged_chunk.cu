@@ -3,9 +3,11 @@
 //   S = Q K^T,  P = exp2(c S - c m),  O += P V,  l += rows of P
 //
 // over blocks of 128 keys, with m a reference maximum of each row that is moved
-// (and O, l rescaled) only when the running maximum has outgrown it by 2^8: the
+// (and O, l rescaled) only when the running maximum has outgrown it by 2^8 (fp16: 2^4): the
 // result does not depend on the reference, and P stays within the 16-bit
-// types.  Bound by the tensor cores and the exponentials together: 4 D
+// types.  P is rounded to them, as the tensor cores take it, l is the sum of the unrounded
+// weights.  In fp16 the reference lies 2^11 below the maximum that it was taken from, so that
+// weights down to 2^-25 of the largest are normal numbers (P is at most 2^15).  Bound by the tensor cores and the exponentials together: 4 D
 // operations a (row, key) against one exponential.
 //
 // One CTA per SM works on tiles of 256 rows of one (sequence, K/V head): row r is
@@ -916,8 +918,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         m = fmaxf(m, fmaxf(max3(x[0], x[1], x[2]), x[3]) * c);
         const bool none = l == 0.f;  // this row has seen no key: any reference will do
-        if (__any_sync(0xFFFFFFFFu, m > base + 8.f || (none && m != -INFINITY))) {
-          const float nb = none && m != -INFINITY ? m : fmaxf(m, base);
+        constexpr float kLift = kBf16 ? 0.f : 11.f, kMost = kBf16 ? 8.f : 15.f;
+        if (__any_sync(0xFFFFFFFFu, m > base + kMost || (none && m != -INFINITY))) {
+          const float nb = none && m != -INFINITY ? m - kLift : fmaxf(m - kLift, base);
           const float f = none ? 1.f : ex2(base - nb);
           base = nb;
           l *= f;

@@ -39,6 +39,15 @@ constexpr uint32_t kMaxCtas = 512;
 // in the place of a box's first position: nothing to read, a page id out of range
 constexpr uint32_t kNoPage = 0xFFFFFFFFu, kBadPage = 0xFFFFFFFEu;
 
+// Weights are rounded to 16 bits for the product with the values.  In fp16 they are 2^14
+// times the formula's, the sum with them (the result does not change): the largest is
+// 2^14, and what is 2^-28 of it still a normal number.  Unlifted, many keys of weights below
+// 2^-14 beside one large one lose their bits, and below 2^-25 all of it.
+template <bool kBf16>
+constexpr float step_lift() {
+  return kBf16 ? 0.f : 14.f;
+}
+
 // One piece of a cut (sequence, head): 16 rows of running maximum, sum, output.
 template <int kDP>
 struct Piece {
@@ -187,7 +196,8 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, uint64_t at, u
   for (int i = 0; i < kDP / 32; ++i)
     if (lane + 32u * i < a.g.D)
       dst[lane + 32u * i] = (uint16_t)pack2(some ? o[i] * inv : 0.f, 0.f, kBf16);
-  if (a.lse && lane == 0) a.lse[at] = some ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
+  if (a.lse && lane == 0)
+    a.lse[at] = some ? (m - step_lift<kBf16>() + log2f(l)) * 0.69314718056f : -INFINITY;
 }
 
 template <int kDP, bool kBf16, bool kSel>
@@ -545,11 +555,12 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
             const float base = mx == -INFINITY ? 0.f : mx;
             const float f = ex2(m[e] - base);
             m[e] = mx;
+            const float down = step_lift<kBf16>() - base;
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float p0 = ex2(fmaf(sc[i][2 * e], a.scale_log2, -base));
-              const float p1 = ex2(fmaf(sc[i][2 * e + 1], a.scale_log2, -base));
+              const float p0 = ex2(fmaf(sc[i][2 * e], a.scale_log2, down));
+              const float p1 = ex2(fmaf(sc[i][2 * e + 1], a.scale_log2, down));
               sum += p0 + p1;
               pf[i >> 1][e + 2 * (i & 1)] = pack2(p0, p1, kBf16);
             }

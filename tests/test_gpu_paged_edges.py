@@ -8,7 +8,7 @@ import torch
 
 from lossless_invariant_bit_gb300 import ibp, paged
 from tests.gpu_util import DEV
-from tests.test_gpu_paged import Setup, near, rope_table, turn
+from tests.test_gpu_paged import F64, U, Setup, near, rope_table, turn
 
 pytestmark = pytest.mark.gpu
 
@@ -146,3 +146,46 @@ def test_append_and_bounds_with_tokens_before_the_first_position():
             kk = st.k[st.table[s, p].long()][:min(P, L - p * P)]
             ref[st.table[s, p].long()] = torch.stack([kk.amin(0), kk.amax(0)], 1)
     assert torch.equal(bounds, ref)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,G,H,lists", [(1, 4, 160, False), (3, 4, 160, False),
+                                         (4, 4, 160, True), (40, 4, 1, False), (60, 1, 2, False)])
+@pytest.mark.parametrize("gap", [8.0, 14.0, 15.5, 16.0])
+def test_weights_far_below_the_largest(n, G, H, lists, gap, dtype):
+    """Four keys with score `gap` and values of zero, 3000 others with score 0: the
+    result is made of weights exp(-gap) alone (2^-23 at 16, below fp16's normal
+    numbers).  A weight may round by u, or by the subnormals' 2^-25 after the kernels have
+    lifted the largest to 2^11 at least."""
+    L, D, seqs = 3000, 64, 4 if H > 2 else 1
+    st = Setup([n] * seqs, [L] * seqs, G=G, H=H, D=D, P=16, dtype=dtype, seed=7)
+    st.q.zero_()
+    st.q[:, :, 5] = 4.0  # gap / 4 is exact
+    for s in range(seqs):
+        st.K[s].zero_()
+        st.K[s][:128:32, :, 5] = gap / 4
+        st.V[s] = (512 + 512 * torch.rand((L, H, D), generator=st.g, device=DEV)).to(dtype)
+        st.V[s][:128:32] = 0
+        st.put(s)
+    pages = None
+    if lists:
+        pages = torch.arange(st.cols, dtype=torch.int32, device=DEV)
+        pages = pages.expand(st.T, H, -1).contiguous()
+    out, lse = st.cache.attention(st.batch, st.q, scale=1.0, pages=pages, lse=True)
+    u, e = U[dtype], 2.0 ** -24
+    d = 2 * (2 * D * e * gap + 2.0 ** -20 * gap + 2.0 ** -20)
+    for s in range(seqs):
+        v = st.V[s].to(F64)
+        for t in range(n):
+            p = torch.full((L - n + t + 1,), math.exp(-gap), dtype=F64, device=DEV)
+            p[:128:32] = 1
+            ref = torch.einsum("k,khd->hd", p / p.sum(), v[:len(p)]).repeat_interleave(G, 0)
+            bound = u * ref + (u + 2 * d + 2.0 ** -20) * ref
+            if dtype == torch.float16:
+                bound = bound + len(p) * 2.0 ** -36 * v.max() + 2.0 ** -25
+            row = st.starts[s] + t
+            diff = (out[row].to(F64) - ref).abs()
+            assert bool((diff <= bound).all()), (s, t, (diff / ref).max().item())
+            total = gap + math.log(float(p.sum()))
+            assert float((lse[row].to(F64) - total).abs().max()) <= d / 2 + 2.0 ** -22 * total + \
+                2.0 ** -20
