@@ -472,9 +472,14 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
         {
           const uint32_t at = warp * kWarpKeys + lane;
           const uint32_t first = s_pos[st][at >> box_lg];
+          const uint32_t key = first + (at & ((1u << box_lg) - 1u));
+          there = __ballot_sync(0xFFFFFFFFu, first < kBadPage && key < L && key >= lo);
           const uint32_t own = key0 + lane;  // (without a page list)
-          const uint32_t lost = __ballot_sync(
-              0xFFFFFFFFu, first == kBadPage && (kSel || (own < L && own >= lo)));
+          const uint32_t lost =
+              there == 0xFFFFFFFFu
+                  ? 0u
+                  : __ballot_sync(0xFFFFFFFFu,
+                                  first == kBadPage && (kSel || (own < L && own >= lo)));
           if (lost) {
             if (lane == 0) set_status(a.g.status, IBP_ERANGE);
 #pragma unroll
@@ -487,8 +492,6 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
               bad[e] = bad[e] || (lost & below & above) != 0u;
             }
           }
-          const uint32_t key = first + (at & ((1u << box_lg) - 1u));
-          there = __ballot_sync(0xFFFFFFFFu, first < kBadPage && key < L && key >= lo);
         }
         if (there) {
           if (there != 0xFFFFFFFFu) {
