@@ -290,6 +290,24 @@ constexpr uint32_t score_smem() {
   return 4u * kScoreGroup * (kDP * 4u + 16u);
 }
 
+// The sum of one query and one page as it is written: where the products' sum is NaN, since
+// 0 * inf has come in (the bound that the other one outdoes is infinite).  Rare.
+template <bool kBf16>
+__device__ float score_as_written(const uint8_t* q, const uint8_t* bounds, uint32_t D) {
+  float sum = 0.f;
+#pragma unroll 1
+  for (uint32_t d = 0; d < D; d += 2u) {
+    const float2 x = unpack2(__ldg(reinterpret_cast<const uint32_t*>(q + d * 2u)), kBf16);
+    const float2 lo = unpack2(__ldg(reinterpret_cast<const uint32_t*>(bounds + d * 2u)), kBf16);
+    const float2 hi =
+        unpack2(__ldg(reinterpret_cast<const uint32_t*>(bounds + (D + d) * 2u)), kBf16);
+    auto larger = [](float u, float v) { return u > v || u != u ? u : v; };
+    sum += larger(x.x * lo.x, x.x * hi.x);
+    sum += larger(x.y * lo.y, x.y * hi.y);
+  }
+  return sum;
+}
+
 template <bool kBf16, int kDP>
 __global__ void __launch_bounds__(128, 3)
     k_paged_scores(PagedGeom g, PagedBatchView b, const uint8_t* q, uint64_t q_stride, uint32_t G,
@@ -433,15 +451,20 @@ __global__ void __launch_bounds__(128, 3)
       // page that was not copied is never looked at)
       const uint32_t rows = tpt == 1u ? min(16u, G - rb * 16u) : G;
       for (uint32_t tt = 0; tt < nt; ++tt) {
-        float m = s_c[warp][tt * G][lane];
-        for (uint32_t i = 1; i < rows; ++i) {
-          const float v = s_c[warp][tt * G + i][lane];
+        const int64_t pos = (int64_t)sq.L - sq.n + t0 + tt;
+        const bool seen = pos >= 0 && c0 + lane <= (uint32_t)(pos >> g.page_lg) && id >= 0;
+        float m = -INFINITY;
+        for (uint32_t i = 0; i < rows; ++i) {
+          float v = s_c[warp][tt * G + i][lane];
+          if (v != v && seen)
+            v = score_as_written<kBf16>(q + (uint64_t)(sq.q0 + t0 + tt) * q_stride +
+                                            ((uint64_t)h * G + rb * 16u + i) * g.D * 2u,
+                                        bounds + ((uint64_t)(uint32_t)id * g.H + h) * g.D * 4u,
+                                        g.D);
           m = (v > m || v != v) ? v : m;
         }
         if (rb) m = (best > m || best != best) ? best : m;
         best = m;
-        const int64_t pos = (int64_t)sq.L - sq.n + t0 + tt;
-        const bool seen = pos >= 0 && c0 + lane <= (uint32_t)(pos >> g.page_lg) && id >= 0;
         if (c0 + lane < b.max_pages && rb + 1u == blocks)
           scores[((uint64_t)(sq.q0 + t0 + tt) * g.H + h) * b.max_pages + c0 + lane] =
               seen ? m : hidden;

@@ -189,3 +189,42 @@ def test_weights_far_below_the_largest(n, G, H, lists, gap, dtype):
             total = gap + math.log(float(p.sum()))
             assert float((lse[row].to(F64) - total).abs().max()) <= d / 2 + 2.0 ** -22 * total + \
                 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("G,D", [(1, 64), (4, 128), (24, 80)])
+def test_scores_of_pages_with_infinite_keys(G, D, dtype):
+    """sum_d max(q lo, q hi) as it is written: an infinite bound that the other one
+    outdoes has no part in it; 0 * inf is NaN."""
+    P, L, n = 8, 700, 5
+    st = Setup([n], [L], G=G, D=D, P=P, dtype=dtype, seed=G)
+    K = st.K[0]
+    K[3, 0, 7] = math.inf
+    K[20, 1, 3] = -math.inf
+    K[40:48, 0, 9] = -math.inf  # both bounds of a channel
+    K[60, 0, 2], K[61, 0, 2] = math.inf, -math.inf
+    K[100, 0, 11] = math.inf
+    K[300, 1, 4], K[301, 1, 6] = math.inf, -math.inf
+    st.q[:, :, 11] = 0
+    bounds = torch.zeros((st.n_pages, st.H, 2, D), dtype=dtype, device=DEV)
+    for p in range(-(-L // P)):
+        kk = K[p * P:(p + 1) * P]
+        bounds[st.table[0, p]] = torch.stack([kk.amin(0), kk.amax(0)], 1)
+    got = st.cache.page_scores(st.batch, st.q, bounds).to(F64)
+    assert st.cache.status() == ibp.IBP_OK
+    b = bounds[st.table[0].long()].to(F64)
+    lo, hi = b[:, None, :, None, 0], b[:, None, :, None, 1]  # [pages, 1, H, 1, D]
+    q = st.q.view(1, n, st.H, G, D).to(F64)
+    term = torch.maximum(q * lo, q * hi)
+    want = term.sum(-1).amax(-1).permute(1, 2, 0)
+    big = q.abs() * torch.maximum(lo.abs(), hi.abs())
+    big = torch.where(torch.isfinite(big), big, torch.where(torch.isfinite(term), term.abs(), 0.0))
+    tol = (4 * D * 2.0 ** -24 * big.sum(-1).amax(-1)).permute(1, 2, 0)
+    for t in range(n):
+        vis = (L - n + t) // P + 1
+        g, w = got[t, :, :vis], want[t, :, :vis]
+        assert torch.equal(torch.isnan(g), torch.isnan(w))
+        assert torch.equal(torch.isinf(g), torch.isinf(w))
+        fin = torch.isfinite(w)
+        assert torch.equal(g[~fin & ~torch.isnan(w)], w[~fin & ~torch.isnan(w)])
+        assert bool(((g - w).abs() <= tol[t, :, :vis])[fin].all())
