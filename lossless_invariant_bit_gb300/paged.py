@@ -112,6 +112,7 @@ class PagedCache:
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.n_pages, self.dtype, self.k, self.v = n_pages, dtype, k, v
         self.device, self._index = k.device, k.device.index
+        self._bounds_shape = (n_pages, kv_heads, 2, head_dim)
         # a dimension of one element has no stride to speak of
         row = head_dim * 2
         st = [s * 2 if n > 1 else max(s * 2, row) for s, n in zip(k.stride(), shape)]
@@ -267,9 +268,9 @@ class PagedCache:
         return (out, total) if lse else out
 
     def _bounds(self, batch: PagedBatch, bounds: torch.Tensor) -> None:
-        if (batch.index != self._index
-                or bounds.shape != (self.n_pages, self.kv_heads, 2, self.head_dim)
-                or bounds.dtype != self.dtype or bounds.get_device() != self._index
+        index = self._index
+        if (batch.index != index or bounds.get_device() != index
+                or bounds.shape != self._bounds_shape or bounds.dtype is not self.dtype
                 or not bounds.is_contiguous()):
             raise ValueError("bounds must be a contiguous [n_pages, kv_heads, 2, head_dim] of the "
                              "cache's type and device (as the batch)")
