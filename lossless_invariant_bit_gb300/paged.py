@@ -29,7 +29,8 @@ import torch
 from . import ibp
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
-_raw_stream = torch._C._cuda_getCurrentRawStream  # the current stream's handle, by device
+# the current stream's handle, by device (a torch without CUDA has none)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 # Attention's workspace of each (device, stream): calls on one stream follow one another

@@ -1,6 +1,9 @@
 """PagedCache's checks of its arguments, without a GPU: tensors that only say what
 they are, and a library that counts its calls."""
 import contextlib
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -157,3 +160,18 @@ def test_a_batch_is_on_one_device(lib, kw):
 def test_pages_are_on_one_device(lib, kw):
     with pytest.raises(ValueError):
         a_cache(**kw)
+
+
+def test_the_module_loads_where_torch_has_no_cuda():
+    """(A torch that was built without CUDA has no such function.)"""
+    code = ("import torch\n"
+            "if hasattr(torch._C, '_cuda_getCurrentRawStream'):\n"
+            "    del torch._C._cuda_getCurrentRawStream\n"
+            "from lossless_invariant_bit_gb300 import paged\n"
+            "try:\n"
+            "    paged.PagedCache(2, 64, 16, 4, torch.float32)\n"
+            "except ValueError:\n"
+            "    print('refused')\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(paged.__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root)
+    assert r.returncode == 0 and r.stdout.strip() == "refused", r.stderr
