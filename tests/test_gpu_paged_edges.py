@@ -228,3 +228,54 @@ def test_scores_of_pages_with_infinite_keys(G, D, dtype):
         fin = torch.isfinite(w)
         assert torch.equal(g[~fin & ~torch.isnan(w)], w[~fin & ~torch.isnan(w)])
         assert bool(((g - w).abs() <= tol[t, :, :vis])[fin].all())
+
+
+def test_the_bindings_functions_make_the_same_calls():
+    """ibp.ibp_paged_*: one function to each C entry point, which PagedCache passes by."""
+    st = Setup([3, 40], [70, 300], G=4, D=64, poison=False)
+    c, b, ws = st.cache, st.batch, torch.empty(ibp.PAGED_WORKSPACE_BYTES, dtype=torch.uint8,
+                                               device=DEV)
+    H, D, T = st.H, st.D, st.T
+    qkv = torch.randn((T, 6 * H, D), generator=st.g, device=DEV).to(st.dtype)
+    q, k, v = qkv[:, :4 * H], qkv[:, 4 * H:5 * H], qkv[:, 5 * H:]
+    w = (1 + 0.1 * torch.randn(D, generator=st.g, device=DEV)).to(st.dtype)
+    cs = rope_table(300, D)
+    row = 6 * H * D * 2
+    want_q = c.append(b, k, v, q=q, q_norm=w, k_norm=w, cos_sin=cs, pairs=True)
+    pages = [st.k.clone(), st.v.clone()]
+    st.k.zero_(), st.v.zero_()
+    for s in range(2):
+        st.put(s)
+    got_q = torch.empty_like(want_q)
+    ibp.ibp_paged_append(c.handle, b.desc, k, v, row, q, row, got_q, 4 * H * D * 2, 4 * H, w, w,
+                         1e-6, cs, 300, D, True)
+    assert torch.equal(got_q, want_q)
+    wrote = torch.zeros((st.n_pages, st.P), dtype=torch.bool, device=DEV)
+    for s, (n, L) in enumerate(zip(st.q_lens, st.kv_lens)):
+        pos = torch.arange(L - n, L, device=DEV)
+        wrote[st.table[s, pos // st.P].long(), pos % st.P] = True
+    assert torch.equal(st.k[wrote], pages[0][wrote]) and torch.equal(st.v[wrote], pages[1][wrote])
+    want, want_lse = c.attention(b, got_q, window=50, lse=True)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    ibp.ibp_paged_attention(c.handle, b.desc, got_q, 4 * H * D * 2, 4 * H, out, lse, D ** -0.5,
+                            True, 50, None, 0, ws, ibp.PAGED_WORKSPACE_BYTES)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    bounds = [torch.zeros((st.n_pages, H, 2, D), dtype=st.dtype, device=DEV) for _ in range(2)]
+    c.update_bounds(b, bounds[0])
+    ibp.ibp_paged_bounds(c.handle, b.desc, bounds[1])
+    assert torch.equal(*bounds)
+    want = c.page_scores(b, got_q, bounds[0])
+    scores = torch.empty_like(want)
+    ibp.ibp_paged_scores(c.handle, b.desc, got_q, 4 * H * D * 2, 4 * H, bounds[0], scores)
+    assert torch.equal(scores, want)
+    picked = c.select_pages(b, scores, 5)
+    got = torch.empty_like(picked)
+    ibp.ibp_paged_select(c.handle, b.desc, scores, 5, got)
+    assert torch.equal(got, picked)
+    want = c.attention(b, got_q, pages=picked)
+    ibp.ibp_paged_attention(c.handle, b.desc, got_q, 4 * H * D * 2, 4 * H, out, None, D ** -0.5,
+                            True, 0, picked, 5, ws, ibp.PAGED_WORKSPACE_BYTES)
+    assert torch.equal(out, want) and c.status() == ibp.IBP_OK
+    with pytest.raises(ibp.IbpError):
+        ibp.ibp_paged_attention(c.handle, b.desc, got_q, 4 * H * D * 2, 4 * H, out, None, 0.125,
+                                True, 0, None, 0, ws, 1024)
