@@ -511,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t first = (int32_t)(w.t.L - w.t.n + w.t.row0 / a.G);
           const int32_t last = (int32_t)(w.t.L - w.t.n + (w.t.row0 + w.t.rows - 1u) / a.G);
           x->all_hi = a.causal ? (uint32_t)max(first + 1, 0) : w.t.L;
-          x->all_lo = a.window ? (uint32_t)max(last + 1 - (int32_t)a.window, 0) : 0u;
+          x->all_lo = a.window && last >= (int32_t)a.window
+                          ? (uint32_t)(last + 1 - (int32_t)a.window)
+                          : 0u;
         }
         mbar_arrive(info_full + tiles % kInfos);
         if (more && w.blk + w.count == w.t.nb && !whole) {
@@ -822,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
       }
     };
-    uint32_t sn = 0, tiles = 0, blocks = 0, e0 = 0;
+    uint32_t sn = 0, tiles = 0, blocks = 0;
     while (true) {
       bool go = true;
       const Info* t = info_of(tiles);
@@ -963,7 +965,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         key0 += (int32_t)(both ? 2u * kKeys : kKeys);
       }
       blocks += count;
-      e0 += 2u * count;
       go = go && wait_or_fail(o_full, tiles & 1u, s_fail);
       ++tiles;
       // The slots count on each other below: all eight warps go on, or all leave.  (Each

@@ -486,7 +486,9 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
             for (int e = 0; e < 2; ++e) {  // those of its keys that the row sees
               const int32_t pos = (int32_t)(L - n + (row0 + r0 + 8u * e) / a.G);
               const int32_t end = kSel || !a.causal ? 32 : pos + 1 - (int32_t)key0;
-              const int32_t from = a.window ? pos + 1 - (int32_t)a.window - (int32_t)key0 : 0;
+              const int32_t from = a.window && pos >= (int32_t)a.window
+                                       ? pos + 1 - (int32_t)a.window - (int32_t)key0
+                                       : 0;
               const uint32_t below = end <= 0 ? 0u : end >= 32 ? ~0u : (1u << end) - 1u;
               const uint32_t above = from <= 0 ? ~0u : from >= 32 ? 0u : ~0u << from;
               bad[e] = bad[e] || (lost & below & above) != 0u;
