@@ -500,7 +500,9 @@ typedef struct {
 
 /* Create a handle on a cache (the descriptor is copied, the pages stay the
  * caller's) on the current device; its status word is one of 4096 that the
- * library holds there from the first handle on.  Errors: IBP_EINVAL (geometry),
+ * library holds there from the first handle on.  Not while a CUDA graph is being captured
+ * (the first handle of a device allocates, and later ones may clear a word).  Calls on the
+ * handle may be captured.  Errors: IBP_EINVAL (geometry),
  * IBP_EALIGN, IBP_ENOMEM, IBP_ECUDA. */
 IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc);
 

@@ -514,8 +514,9 @@ __device__ __forceinline__ uint32_t select_row(const PagedGeom& g, const PagedBa
 // exponentially there (tails do), every third time in the middle: 6 to 8 counts for
 // 1000 normal scores.  Where no such threshold lies between two scores (equal ones,
 // infinities) the n_sel-th largest is found bit by bit, and of those equal to it the
-// first are taken.  Bound by issue: 2 kPer instructions a count, 9 kPer to write the
-// numbers.  4 rows to a CTA when kWarps is 1.
+// first are taken.  Bound by issue: 59 kPer instructions a row of 1001, of them 2 kPer for
+// each count and 9 kPer to write the numbers (7960 such rows in 23 us).  4 rows to a CTA
+// when kWarps is 1.
 template <int kWarps, int kPer>
 __global__ void __launch_bounds__(kWarps == 1 ? 128 : kWarps * 32,
                                   kPer <= 16 ? 4 : kPer <= 32 && kWarps == 1 ? 6 : 1)
@@ -797,9 +798,10 @@ cudaError_t launch_paged_scores(const PagedGeom& g, const PagedBatchView& b, con
   const uint64_t tiles = (uint64_t)b.n_tokens / tpt + b.n_seqs;
   const uint64_t groups = (b.max_pages + kScoreGroup - 1u) / kScoreGroup;
   if (tiles > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  // A row's groups of pages go to as many CTAs as the GPU holds at a time (three to an SM),
-  // so that what a CTA looks up first is paid once: 16 tokens x 8 heads x 2048 pages in
-  // 33.4 us; six to an SM 35.9, two 38.9, one 49.7.  (Tiles that hold rows: the numbers leave gaps.)
+  // A row's groups of pages go to as many CTAs as the GPU holds at a time (at most three to
+  // an SM, the same number to each tile), so that what a CTA looks up first is paid once:
+  // 16 tokens x 8 heads x 2048 pages in 33.6 us (384 CTAs); six to an SM 35.9, two 38.9, one
+  // 49.7.  (Tiles that hold rows: the numbers leave gaps.)
   const uint64_t full = b.n_tokens < (uint64_t)tpt * b.n_seqs
                             ? (b.n_tokens < b.n_seqs ? b.n_tokens : b.n_seqs)
                             : (b.n_tokens + tpt - 1u) / tpt;

@@ -33,7 +33,7 @@
 // list, cut into equal runs, one per CTA; a tile that is cut is joined from its pieces
 // by a second kernel, in order.
 //
-// Measured: 2048 tokens behind 6144, 64 query heads of 128 on 8, causal: 333 us, 1.45
+// Measured: 2048 tokens behind 6144, 64 query heads of 128 on 8, causal: 331 us, 1.45
 // PFLOP/s, bound by the scores' products (both operands from shared memory: 740 to
 // 830 cycles a block against 520 for the values') and the turns between the slots.
 // Without turns (both issuers at will) 438 us; a tile's memory released by the

@@ -89,7 +89,9 @@ class PagedCache:
 
     Calls run on the current stream, or on `stream` (a torch stream or a
     cudaStream_t), on which their outputs and workspaces are then allocated too.
-    The pages' device has to be the current one."""
+    The pages' device has to be the current one.  Several threads may call on one
+    stream.  The operators are for serving: results carry no gradient, also where
+    the arguments require one."""
 
     def __init__(self, kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
                  dtype: torch.dtype = torch.bfloat16, k: Optional[torch.Tensor] = None,
