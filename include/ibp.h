@@ -506,6 +506,28 @@ typedef struct {
  * IBP_EALIGN, IBP_ENOMEM, IBP_ECUDA. */
 IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc);
 
+/* As ibp_paged_create, for pages held in 8 bits: the keys (and the values) of one page and
+ * head are codes, e4m3 numbers of one byte, under one scale, and stand for code * scale.
+ *   desc      k, v and the strides are the codes' (token_stride = kv_heads * head_dim and
+ *             head_stride = head_dim make a token's codes one IBP row); dtype is the 16-bit
+ *             type of the calls' queries, keys, values, results and bounds
+ *   k_scales, v_scales  device, one byte each, [n_pages, kv_heads], contiguous: byte e is the
+ *             scale 2^(e - 127) (E8M0), 77 <= e <= 177
+ * Every call takes the handle as it takes one on 16-bit pages:
+ *   append     computes keys as before, in fp32, and rounds once, to the codes.  A scale is
+ *              the smallest that holds (as 448 * scale) the largest finite magnitude of the
+ *              new tokens that go into the page; where the page holds older tokens of the
+ *              sequence, it never falls, and if it grows their codes are rounded to it again
+ *              (a power of two: exact but for codes that become subnormal).  What the
+ *              largest scale does not hold becomes the largest code; infinities and NaN
+ *              become NaN codes.  A page that new tokens go into belongs to one sequence
+ *   attention  as over code * scale, in fp32 with weights and codes multiplied in fp16; the
+ *              scales are exact
+ *   bounds     of code * scale, rounded to the 16-bit type
+ * A scale outside its range is an error like a page id out of range, where it is needed. */
+IBP_API ibp_status ibp_paged_create_8bit(ibp_paged** out, const ibp_paged_desc* desc,
+                                         void* k_scales, void* v_scales);
+
 /* Free a handle, once the work of its calls is done (the pages are not touched;
  * work still in flight would report into a later handle's status word).  NULL is a no-op. */
 IBP_API ibp_status ibp_paged_destroy(ibp_paged* cache);
@@ -598,6 +620,41 @@ IBP_API ibp_status ibp_paged_scores(const ibp_paged* cache, const ibp_paged_batc
 IBP_API ibp_status ibp_paged_select(const ibp_paged* cache, const ibp_paged_batch* batch,
                                     const float* scores, uint32_t n_selected, int32_t* selected,
                                     ibp_stream_t stream);
+
+/* The pages that sequences hold, on the device: sequence s has kv_lens[s] tokens, in the
+ * pages page_table[s][0 .. ceil(kv_lens[s] / page_tokens) - 1] (further entries are not
+ * looked at); pages that no sequence holds are free_pages[0 .. state[0] - 1]. */
+typedef struct {
+  int32_t* page_table;    /* device [n_seqs, table_stride] */
+  int32_t* kv_lens;       /* device [n_seqs] */
+  int32_t* free_pages;    /* device [n_pages of the cache] */
+  int32_t* state;         /* device [2]: how many are free; a counter, 0 at the start */
+  uint64_t table_stride;  /* entries between rows of the page table */
+  uint32_t n_seqs;
+  uint32_t max_pages;     /* columns of the page table */
+} ibp_paged_tables;
+
+/* Resize sequences: sequence s gets target[s] tokens.  One that grows takes the pages that it
+ * lacks from the end of the list of free ones, one that shrinks (0: it has ended) returns those
+ * that it no longer needs, before any is taken.  Pages return in the reverse order of
+ * sequences and places, and are taken in order, so a growth that is taken back leaves
+ * the list as it was.
+ *   target    device [n_seqs]; kv_lens becomes a copy of it
+ *   n_tokens  rows of the new tokens' arrays, at least the sum of what sequences grow by (a
+ *             call with 0 only shrinks)
+ *   q_starts  device [n_seqs + 1] (not looked at when n_tokens is 0): becomes the first row of
+ *             each sequence's new tokens, with the total behind the last; with page_table and
+ *             kv_lens it is a batch of ibp_paged_append and ibp_paged_attention
+ *   slots     NULL, or device [n_tokens]: becomes page * page_tokens + place of each new token
+ *             (its row of a cache whose tokens are rows); rows behind the last are left alone
+ * A call that cannot be served as a whole (too few free pages, more new tokens than
+ * n_tokens, a length or target outside [0, max_pages * page_tokens], a list longer than the
+ * cache) sets IBP_ERANGE in the handle's status word and changes nothing, but that q_starts
+ * becomes 0: its batch has no rows.  Calls on the same tables follow one another; they may
+ * be captured.  Errors: IBP_EINVAL, IBP_EALIGN, IBP_ECUDA. */
+IBP_API ibp_status ibp_paged_resize(const ibp_paged* cache, const ibp_paged_tables* tables,
+                                    const int32_t* target, int32_t* q_starts, int64_t* slots,
+                                    uint32_t n_tokens, ibp_stream_t stream);
 
 /* Copy the store's Mask and Bitval (R/4 words each) to host arrays.  Synchronous. */
 IBP_API ibp_status ibp_meta_get(const ibp_store* store, uint32_t* mask_host, uint32_t* bitval_host);

@@ -1,8 +1,9 @@
 """Build libibp.so in-tree with nvcc for sm_103a (GB300).
 
 The translation units (kernels, C-ABI, allocation-free builder, transfer
-baselines, projection with the compressor in its epilogue, launch helpers, paged K/V cache) compile in parallel, then link into a
-shared library beside this file.  The CUDA runtime is linked statically, so
+baselines, projection with the compressor in its epilogue, launch helpers, paged
+K/V cache in 16 and in 8 bits) compile in parallel, then link into a shared
+library beside this file.  The CUDA runtime is linked statically, so
 the library loads without any other CUDA library on the path.
 """
 from __future__ import annotations
@@ -21,7 +22,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libibp.so")
 SOURCES = ["ibp_kernels.cu", "ibp_api.cu", "ibp_noalloc.cu", "ibp_transfer.cu", "ibp_project.cu",
            "ibp_launch.cu", "ibp_paged.cu", "ibp_paged_step.cu",
-           "ibp_paged_chunk.cu", "ibp_paged_api.cu"]
+           "ibp_paged_chunk.cu", "ibp_paged_api.cu", "ibp_paged8.cu", "ibp_paged8_step.cu",
+           "ibp_paged_tables.cu", "ibp_paged8_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -16,6 +16,7 @@ struct PagedGeom {
   uint64_t page_stride, head_stride, token_stride;
   uint32_t n_pages, page_lg, H, D, bf16;
   uint32_t* status;
+  uint8_t *k_scales, *v_scales;  // NULL, or of pages held in 8 bits: [n_pages, H]
 };
 
 struct PagedBatchView {
@@ -58,6 +59,18 @@ struct PagedAppendArgs {
   uint32_t n_pos, rot, pairs;
 };
 
+// Sequences that change their lengths.
+struct PagedTablesArgs {
+  int32_t *table, *kv_lens, *free_pages;
+  int32_t* state;           // how many pages are free; a counter that is 0 between calls
+  const int32_t* target;
+  int32_t* q_starts;
+  int64_t* slots;           // NULL or [n_tokens]
+  uint32_t* status;
+  uint64_t table_stride;
+  uint32_t n_seqs, max_pages, n_tokens, n_pages, page_lg;
+};
+
 // workspace of an attention call: the one-token kernel's pieces, then the chunk kernel's
 constexpr uint64_t kStepWsBytes = 32ull << 20;
 
@@ -85,6 +98,17 @@ cudaError_t launch_paged_chunk(const PagedAttnArgs& a, const PagedMaps& m, int s
                                cudaStream_t st);
 // Joins its pieces: after it, and after the step kernel where the call has one.
 cudaError_t launch_paged_chunk_join(const PagedAttnArgs& a, int sm_count, cudaStream_t st);
+
+cudaError_t launch_paged_resize(const PagedTablesArgs& a, int sm_count, cudaStream_t st);
+
+// What a cache's calls launch, by what its pages hold.
+struct PagedLaunches {
+  decltype(&launch_paged_append) append;
+  decltype(&launch_paged_bounds) bounds;
+  decltype(&launch_paged_step) step;
+  decltype(&launch_paged_chunk) chunk;  // NULL: the step kernel takes every sequence
+  decltype(&launch_paged_chunk_join) chunk_join;
+};
 
 #ifdef __CUDACC__
 
@@ -162,5 +186,22 @@ __device__ __forceinline__ uint32_t paged_find_tile(const PagedBatchView& b, uin
 }
 
 #endif
+
+}  // namespace ibp
+
+struct ibp_paged {
+  int status_at;
+  ibp::PagedGeom g;
+  int device, sm_count;
+  ibp::PagedMaps maps;
+  const ibp::PagedLaunches* launches;
+};
+
+namespace ibp {
+
+// A handle on pages of 16-bit values, or of codes of one byte under the scales given;
+// the descriptor is checked.
+ibp_status paged_create(ibp_paged** out, const ibp_paged_desc* desc, uint8_t* k_scales,
+                        uint8_t* v_scales, const PagedLaunches* launches);
 
 }  // namespace ibp

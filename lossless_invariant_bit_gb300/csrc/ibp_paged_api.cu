@@ -81,13 +81,6 @@ std::mutex& call_lock(const void* workspace) {
 
 }  // namespace
 
-struct ibp_paged {
-  int status_at;
-  ibp::PagedGeom g;
-  int device, sm_count;
-  ibp::PagedMaps maps;
-};
-
 namespace {
 
 inline bool misaligned(const void* p, uintptr_t to) {
@@ -96,18 +89,26 @@ inline bool misaligned(const void* p, uintptr_t to) {
 
 inline ibp_status cu(cudaError_t e) { return e == cudaSuccess ? IBP_OK : IBP_ECUDA; }
 
-// The pages as {head_dim, tokens of a page, heads, pages}, in boxes of 64
-// channels x `tokens` tokens: rows of 128 bytes, swizzled; channels past head_dim read as zero.
-bool page_map(CUtensorMap* map, const ibp_paged_desc& d, void* base, uint32_t tokens) {
+const ibp::PagedLaunches k16Bit = {&ibp::launch_paged_append, &ibp::launch_paged_bounds,
+                                   &ibp::launch_paged_step, &ibp::launch_paged_chunk,
+                                   &ibp::launch_paged_chunk_join};
+
+// The pages as {head_dim, tokens of a page, heads, pages}, in boxes of 64 channels x `tokens`
+// tokens: rows of 128 bytes, swizzled; channels past head_dim read as zero.  Codes: boxes of
+// 128 channels, or of 64 (and rows of as many bytes) for heads that need no more.
+bool page_map(CUtensorMap* map, const ibp_paged_desc& d, void* base, uint32_t tokens, bool codes) {
   const ibp::EncodeTiledFn f = ibp::encode_tiled();
   if (!f) return false;
+  const cuuint32_t span = !codes || d.head_dim <= 64u ? 64u : 128u;
   const cuuint64_t dims[4] = {d.head_dim, d.page_tokens, d.kv_heads, d.n_pages};
   const cuuint64_t strides[3] = {d.token_stride, d.head_stride, d.page_stride};
-  const cuuint32_t box[4] = {64, tokens < d.page_tokens ? tokens : d.page_tokens, 1, 1};
+  const cuuint32_t box[4] = {span, tokens < d.page_tokens ? tokens : d.page_tokens, 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  return f(map,
-           d.dtype ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, base,
-           dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUtensorMapDataType type = codes     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : d.dtype ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                             : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  return f(map, type, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           codes && span == 64u ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -151,9 +152,8 @@ ibp_status stride_ok(uint64_t stride, uint64_t heads, uint32_t D) {
 
 }  // namespace
 
-extern "C" {
-
-ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
+ibp_status ibp::paged_create(ibp_paged** out, const ibp_paged_desc* d, uint8_t* k_scales,
+                             uint8_t* v_scales, const PagedLaunches* launches) {
   if (!out) return IBP_EINVAL;
   *out = nullptr;
   if (!d || !d->k || !d->v) return IBP_EINVAL;
@@ -165,7 +165,8 @@ ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
   if (misaligned(d->k, 16) || misaligned(d->v, 16) || d->page_stride % 16u ||
       d->head_stride % 16u || d->token_stride % 16u)
     return IBP_EALIGN;
-  const uint64_t row = d->head_dim * 2ull, most = 1ull << 40;  // strides of a tensor map
+  const bool codes = k_scales != nullptr;
+  const uint64_t row = d->head_dim * (codes ? 1ull : 2ull), most = 1ull << 40;  // strides of a tensor map
   if (d->token_stride < row || d->head_stride < row || d->page_stride < row ||
       d->token_stride >= most || d->head_stride >= most || d->page_stride >= most)
     return IBP_EINVAL;
@@ -175,12 +176,13 @@ ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
   while ((1u << lg) < d->page_tokens) ++lg;
   c->g = ibp::PagedGeom{static_cast<uint8_t*>(d->k), static_cast<uint8_t*>(d->v),
                         d->page_stride, d->head_stride, d->token_stride, d->n_pages, lg,
-                        d->kv_heads, d->head_dim, d->dtype, nullptr};
+                        d->kv_heads, d->head_dim, d->dtype, nullptr, k_scales, v_scales};
+  c->launches = launches;
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device) !=
           cudaSuccess ||
-      !page_map(&c->maps.k, *d, d->k, ibp::kBoxTokens) ||
-      !page_map(&c->maps.v, *d, d->v, ibp::kBoxTokens)) {
+      !page_map(&c->maps.k, *d, d->k, ibp::kBoxTokens, codes) ||
+      !page_map(&c->maps.v, *d, d->v, ibp::kBoxTokens, codes)) {
     delete c;
     return IBP_ECUDA;
   }
@@ -191,6 +193,12 @@ ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
   }
   *out = c;
   return IBP_OK;
+}
+
+extern "C" {
+
+ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* d) {
+  return ibp::paged_create(out, d, nullptr, nullptr, &k16Bit);
 }
 
 ibp_status ibp_paged_destroy(ibp_paged* c) {
@@ -250,7 +258,7 @@ ibp_status ibp_paged_append(const ibp_paged* c, const ibp_paged_batch* b, const 
   a.n_pos = n_pos;
   a.rot = cos_sin ? rot_dim : 0u;
   a.pairs = pairs;
-  return cu(ibp::launch_paged_append(a, c->sm_count, reinterpret_cast<cudaStream_t>(stream)));
+  return cu(c->launches->append(a, c->sm_count, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, const void* q,
@@ -289,14 +297,16 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
   // Lists of pages, and sequences with one tile of 16 rows at most, go to the step
   // kernel, the others to the chunk kernel; a batch may need both, and the step kernel's
   // CTAs then fill the SMs that the chunk kernel's have left.
-  const bool few = selected || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
+  const ibp::PagedLaunches& run = *c->launches;
+  const bool few =
+      selected || !run.chunk || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
   const bool both = !few && b->n_seqs > 1u;
-  a.max_rows = few || both ? ibp::kStepRows : 0u;
+  a.max_rows = !run.chunk ? ~0u : few || both ? ibp::kStepRows : 0u;
   std::lock_guard<std::mutex> lock(call_lock(workspace));
-  cudaError_t ce = few ? cudaSuccess : ibp::launch_paged_chunk(a, c->maps, c->sm_count, st);
+  cudaError_t ce = few ? cudaSuccess : run.chunk(a, c->maps, c->sm_count, st);
   if (ce == cudaSuccess && (few || both))
-    ce = ibp::launch_paged_step(a, c->maps, c->sm_count, both, st);
-  if (ce == cudaSuccess && !few) ce = ibp::launch_paged_chunk_join(a, c->sm_count, st);
+    ce = run.step(a, c->maps, c->sm_count, both, st);
+  if (ce == cudaSuccess && !few) ce = run.chunk_join(a, c->sm_count, st);
   return cu(ce);
 }
 
@@ -307,8 +317,8 @@ ibp_status ibp_paged_bounds(const ibp_paged* c, const ibp_paged_batch* b, void* 
   if (e != IBP_OK || empty) return e;
   if (!bounds) return IBP_EINVAL;
   if (misaligned(bounds, 16)) return IBP_EALIGN;
-  return cu(ibp::launch_paged_bounds(c->g, view(b), static_cast<uint8_t*>(bounds),
-                                     reinterpret_cast<cudaStream_t>(stream)));
+  return cu(c->launches->bounds(c->g, view(b), static_cast<uint8_t*>(bounds),
+                                reinterpret_cast<cudaStream_t>(stream)));
 }
 
 ibp_status ibp_paged_scores(const ibp_paged* c, const ibp_paged_batch* b, const void* q,

@@ -1,0 +1,241 @@
+// Page tables on the GPU: sequences change their lengths, pages come from the list of free
+// ones or go back to it, and the new tokens get their rows and slots.
+//
+// have = ceil(length / page), want = ceil(target / page).  All sequences' pages that go are
+// numbered r = 0 .. R - 1 by sequence and place, those that come j = 0 .. J - 1; with n free
+// pages at the start
+//   free[n + R - 1 - r] = page r             (the last one first, so that a growth that is
+//   page j = free[n + R - 1 - j]              taken back leaves the list as it was)
+// Prefix sums of R, J and the new tokens T over the sequences place everything.
+//
+// Two kernels, the second behind the first: pages that go are on the list before any is
+// taken from it.  Each CTA sums over all sequences for itself (a few kB from L2, where a
+// hand-over would cost another launch), then takes an equal part of the pages, or of the new
+// tokens.  A call that cannot be served as a whole changes nothing: every CTA finds the
+// same sums.  Lengths and the list's length change when the last CTA has ended, since
+// all of them read the old ones.
+#include "ibp_paged.cuh"
+#include "ibp_sm103.cuh"
+
+namespace ibp {
+namespace {
+
+constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+
+struct Sums {
+  uint64_t gone, come, rows;
+};
+
+// A sequence's part of the sums.
+struct Part {
+  uint32_t old, have, want, gone, come, rows;
+  bool ok;
+};
+
+__device__ __forceinline__ Part part_of(const PagedTablesArgs& a, uint32_t s) {
+  const int32_t old = a.kv_lens[s], to = __ldg(a.target + s);
+  const uint64_t most = (uint64_t)a.max_pages << a.page_lg;
+  Part p{};
+  p.ok = old >= 0 && to >= 0 && (uint64_t)old <= most && (uint64_t)to <= most;
+  if (!p.ok) return p;
+  const uint32_t up = (1u << a.page_lg) - 1u;
+  p.old = (uint32_t)old;
+  p.have = ((uint32_t)old + up) >> a.page_lg;
+  p.want = ((uint32_t)to + up) >> a.page_lg;
+  p.gone = p.have > p.want ? p.have - p.want : 0u;
+  p.come = p.want > p.have ? p.want - p.have : 0u;
+  p.rows = to > old ? (uint32_t)(to - old) : 0u;
+  return p;
+}
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
+  return x;
+}
+
+// The sums over all sequences, and whether the call can be served.
+__device__ __forceinline__ bool total(const PagedTablesArgs& a, Sums& t, uint32_t& n_free) {
+  __shared__ uint64_t s_sum[3][kWarps];
+  __shared__ uint32_t s_bad;
+  if (threadIdx.x == 0) s_bad = 0;
+  __syncthreads();
+  Sums m{0, 0, 0};
+  bool ok = true;
+  for (uint32_t s = threadIdx.x; s < a.n_seqs; s += kThreads) {
+    const Part p = part_of(a, s);
+    ok = ok && p.ok;
+    m.gone += p.gone, m.come += p.come, m.rows += p.rows;
+  }
+  m.gone = warp_sum(m.gone), m.come = warp_sum(m.come), m.rows = warp_sum(m.rows);
+  const uint32_t warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31u) == 0u)
+    s_sum[0][warp] = m.gone, s_sum[1][warp] = m.come, s_sum[2][warp] = m.rows;
+  if (!ok) s_bad = 1;
+  const int32_t n = a.state[0];
+  __syncthreads();
+  t = Sums{0, 0, 0};
+  for (uint32_t w = 0; w < kWarps; ++w)
+    t.gone += s_sum[0][w], t.come += s_sum[1][w], t.rows += s_sum[2][w];
+  n_free = (uint32_t)n;
+  return !s_bad && n >= 0 && n_free + t.gone <= a.n_pages && t.come <= n_free + t.gone &&
+         t.rows <= a.n_tokens;
+}
+
+// Sums of x before this thread, and over all threads.
+__device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t (&s_warp)[kWarps], uint32_t& all) {
+  const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
+  uint32_t inc = x;
+#pragma unroll
+  for (uint32_t d = 1; d < 32u; d <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+    if (lane >= d) inc += v;
+  }
+  __syncthreads();
+  if (lane == 31u) s_warp[warp] = inc;
+  __syncthreads();
+  uint32_t before = 0;
+  all = 0;
+  for (uint32_t w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_warp[w];
+    all += s_warp[w];
+  }
+  return before + inc - x;
+}
+
+// The last of kThreads sums, which do not decrease, that is at most x.
+__device__ __forceinline__ uint32_t last_at_most(const uint32_t (&sums)[kThreads], uint32_t x) {
+  uint32_t at = 0;
+#pragma unroll
+  for (uint32_t d = kThreads / 2; d; d >>= 1)
+    if (sums[at + d] <= x) at += d;
+  return at;
+}
+
+// The last CTA to come here sets what the others have read.
+__device__ __forceinline__ void finish(const PagedTablesArgs& a, bool ok, const Sums& t,
+                                       uint32_t n_free) {
+  __shared__ uint32_t s_last;
+  __syncthreads();  // (every thread's reads and writes are before its CTA's ticket)
+  if (threadIdx.x == 0) {
+    __threadfence();
+    s_last = atomicAdd(reinterpret_cast<uint32_t*>(a.state) + 1, 1u) == gridDim.x - 1u;
+    __threadfence();
+  }
+  __syncthreads();
+  if (!s_last) return;
+  if (ok)
+    for (uint32_t s = threadIdx.x; s < a.n_seqs; s += kThreads) a.kv_lens[s] = __ldg(a.target + s);
+  if (threadIdx.x == 0) {
+    if (ok)
+      a.state[0] = (int32_t)(n_free + (uint32_t)t.gone - (uint32_t)t.come);
+    else
+      set_status(a.status, IBP_ERANGE);
+    a.state[1] = 0;
+  }
+}
+
+// Pages that go, onto the list; all there is to do when no sequence may grow.
+__global__ void __launch_bounds__(kThreads) k_paged_give(PagedTablesArgs a) {
+  __shared__ uint32_t s_warp[kWarps], s_sum[kThreads], s_want[kThreads];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Sums t;
+  uint32_t n_free;
+  const bool ok = total(a, t, n_free);
+  if (ok && t.gone) {
+    const uint32_t R = (uint32_t)t.gone;
+    const uint32_t r0 = (uint32_t)((uint64_t)R * blockIdx.x / gridDim.x);
+    const uint32_t r1 = (uint32_t)((uint64_t)R * (blockIdx.x + 1u) / gridDim.x);
+    uint32_t base = 0;
+    for (uint32_t c = 0; c < a.n_seqs && base < r1; c += kThreads) {
+      Part p{};
+      if (c + threadIdx.x < a.n_seqs) p = part_of(a, c + threadIdx.x);
+      uint32_t all;
+      const uint32_t before = scan(p.gone, s_warp, all);
+      s_sum[threadIdx.x] = base + before;
+      s_want[threadIdx.x] = p.want;
+      __syncthreads();
+      for (uint32_t r = max(r0, base) + threadIdx.x; r < min(r1, base + all); r += kThreads) {
+        const uint32_t i = last_at_most(s_sum, r);
+        a.free_pages[n_free + R - 1u - r] =
+            a.table[(uint64_t)(c + i) * a.table_stride + s_want[i] + (r - s_sum[i])];
+      }
+      base += all;
+      __syncthreads();
+    }
+  }
+  if (!a.n_tokens) finish(a, ok, t, n_free);
+}
+
+// Rows, pages and slots of the new tokens, behind k_paged_give.
+__global__ void __launch_bounds__(kThreads) k_paged_take(PagedTablesArgs a) {
+  __shared__ uint32_t s_warp[kWarps], s_row[kThreads], s_page[kThreads], s_old[kThreads];
+  Sums t;
+  uint32_t n_free;
+  const bool ok = total(a, t, n_free);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t T = ok ? (uint32_t)t.rows : 0u;
+  const uint32_t t0 = (uint32_t)((uint64_t)T * blockIdx.x / gridDim.x);
+  const uint32_t t1 = (uint32_t)((uint64_t)T * (blockIdx.x + 1u) / gridDim.x);
+  const uint32_t top = ok ? n_free + (uint32_t)t.gone - 1u : 0u;
+  const uint32_t lg = a.page_lg, P = 1u << lg;
+  uint32_t row = 0, page = 0;  // sums before the sequences from c on
+  const bool starts = blockIdx.x == 0;
+  for (uint32_t c = 0; c < a.n_seqs && (starts || row < t1); c += kThreads) {
+    const uint32_t s = c + threadIdx.x;
+    Part p{};
+    if (ok && s < a.n_seqs) p = part_of(a, s);
+    uint32_t rows, pages;
+    const uint32_t before = scan(p.rows, s_warp, rows);
+    const uint32_t first = scan(p.come, s_warp, pages);
+    s_row[threadIdx.x] = row + before;
+    s_page[threadIdx.x] = page + first - p.have;  // number of its page i that is new: this + i
+    s_old[threadIdx.x] = p.old;
+    if (starts && s < a.n_seqs) {
+      a.q_starts[s] = (int32_t)(row + before);
+      if (s + 1u == a.n_seqs) a.q_starts[s + 1u] = (int32_t)(row + before + p.rows);
+    }
+    __syncthreads();
+    for (uint32_t x = max(t0, row) + threadIdx.x; x < min(t1, row + rows); x += kThreads) {
+      const uint32_t i = last_at_most(s_row, x);
+      const uint32_t old = s_old[i], pos = old + (x - s_row[i]), at = pos >> lg;
+      int32_t* entry = a.table + (uint64_t)(c + i) * a.table_stride + at;
+      int32_t id;
+      if (at >= (old + P - 1u) >> lg) {  // a new page; its first token writes its entry
+        id = a.free_pages[top - (s_page[i] + at)];
+        if ((pos & (P - 1u)) == 0u) *entry = id;
+      } else {
+        id = *entry;
+      }
+      if (a.slots) a.slots[x] = ((int64_t)id << lg) + (pos & (P - 1u));
+    }
+    row += rows;
+    page += pages;
+    __syncthreads();
+  }
+  finish(a, ok, t, n_free);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_resize(const PagedTablesArgs& a, int sm_count, cudaStream_t st) {
+  auto ctas = [&](uint64_t n) {
+    const uint64_t c = (n + 4u * kThreads - 1) / (4u * kThreads);
+    return (unsigned)(c < 1u ? 1u : c > (uint64_t)sm_count ? (uint64_t)sm_count : c);
+  };
+  k_paged_give<<<ctas((uint64_t)a.n_seqs * a.max_pages), kThreads, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !a.n_tokens) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas(a.n_tokens), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_paged_take, a);
+}
+
+}  // namespace ibp

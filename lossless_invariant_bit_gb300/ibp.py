@@ -51,6 +51,13 @@ class ibp_paged_batch(ctypes.Structure):
                 ("n_tokens", ctypes.c_uint32), ("max_q_tokens", ctypes.c_uint32)]
 
 
+class ibp_paged_tables(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("state", ctypes.c_void_p),
+                ("table_stride", ctypes.c_uint64), ("n_seqs", ctypes.c_uint32),
+                ("max_pages", ctypes.c_uint32)]
+
+
 PAGED_WORKSPACE_BYTES = 96 << 20  # IBP_PAGED_WORKSPACE_BYTES of include/ibp.h
 
 _lib = None
@@ -93,6 +100,7 @@ _SIGS = {
     "ibp_gather_copy_staged": [_P, _P, _U64, _U32, _P, _U64, _U64, _P, _P],
     "ibp_project_compress": [_P, _P, _U64, _U64, _P, _P, _U32, _P, _P, _P, _P, _P, _U64, _P],
     "ibp_paged_create": [ctypes.POINTER(ctypes.c_void_p), _P],
+    "ibp_paged_create_8bit": [ctypes.POINTER(ctypes.c_void_p), _P, _P, _P],
     "ibp_paged_destroy": [_P],
     "ibp_paged_status": [_P, _P, ctypes.POINTER(ctypes.c_int), ctypes.c_int],
     "ibp_paged_append": [_P, _P, _P, _P, _U64, _P, _U64, _P, _U64, _U32, _P, _P, _F32, _P, _U32,
@@ -102,6 +110,7 @@ _SIGS = {
     "ibp_paged_bounds": [_P, _P, _P, _P],
     "ibp_paged_scores": [_P, _P, _P, _U64, _U32, _P, _P, _P],
     "ibp_paged_select": [_P, _P, _P, _U32, _P, _P],
+    "ibp_paged_resize": [_P, _P, _P, _P, _P, _U32, _P],
 }
 
 
@@ -395,6 +404,14 @@ def ibp_paged_create(desc: "ibp_paged_desc") -> int:
     return h.value
 
 
+def ibp_paged_create_8bit(desc: "ibp_paged_desc", k_scales, v_scales) -> int:
+    h = ctypes.c_void_p()
+    _check(_lib_handle().ibp_paged_create_8bit(ctypes.byref(h), ctypes.addressof(desc),
+                                               _ptr(k_scales), _ptr(v_scales)),
+           "ibp_paged_create_8bit")
+    return h.value
+
+
 def ibp_paged_destroy(cache: int) -> None:
     _check(_lib_handle().ibp_paged_destroy(cache), "ibp_paged_destroy")
 
@@ -445,6 +462,13 @@ def ibp_paged_select(cache: int, batch: "ibp_paged_batch", scores, n_selected: i
     _check(_lib_handle().ibp_paged_select(cache, ctypes.addressof(batch), _ptr(scores),
                                           n_selected, _ptr(selected), _stream(stream)),
            "ibp_paged_select")
+
+
+def ibp_paged_resize(cache: int, tables: "ibp_paged_tables", target, q_starts, slots,
+                     n_tokens: int, stream=None) -> None:
+    _check(_lib_handle().ibp_paged_resize(cache, ctypes.addressof(tables), _ptr(target),
+                                          _ptr(q_starts), _ptr(slots), n_tokens,
+                                          _stream(stream)), "ibp_paged_resize")
 
 
 def ibp_status_str(status: int) -> str:

@@ -17,6 +17,18 @@ this class checks shapes and types, allocates outputs and passes pointers.
 A token's keys (or values) over all heads are one row of ``kv_heads *
 head_dim`` 16-bit values, so pages go to a compressed host store and come back
 through ``IbpStore``: ``key_rows()`` and ``value_rows()`` are the rows.
+
+With ``page_dtype=torch.float8_e4m3fn`` the pages hold one byte for each value, under a
+scale for each page and head (``k_scales``, ``v_scales``: powers of two,
+float8_e8m0fnu); every call is the same:
+
+    cache = PagedCache(8, 128, 16, 4096, torch.bfloat16, page_dtype=torch.float8_e4m3fn)
+
+The pages that sequences hold can be kept on the device:
+
+    tables = cache.tables(n_seqs, max_pages)              # every page is free
+    batch, slots = tables.resize(target, n_tokens)        # lengths change: pages come and go
+    cache.append(batch, k, v)                             # slots: the new tokens' rows
 """
 from __future__ import annotations
 
@@ -29,6 +41,7 @@ import torch
 from . import ibp
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+_CODES, _SCALES = torch.float8_e4m3fn, torch.float8_e8m0fnu
 # the current stream's handle, by device (a torch without CUDA has none)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -85,7 +98,10 @@ class PagedBatch:
 
 class PagedCache:
     """Key and value pages of one layer, [n_pages, page_tokens, kv_heads, head_dim]
-    (any strides of whole heads; allocated when not given).
+    (any strides of whole heads; allocated when not given).  `dtype` is the type of the
+    calls' queries, keys, values and results, and of the pages unless `page_dtype` is
+    float8_e4m3fn: then a page's keys (values) of one head are codes under the scale in
+    k_scales (v_scales) [n_pages, kv_heads], float8_e8m0fnu, which appends keep.
 
     Calls run on the current stream, or on `stream` (a torch stream or a
     cudaStream_t), on which their outputs and workspaces are then allocated too.
@@ -95,35 +111,58 @@ class PagedCache:
 
     def __init__(self, kv_heads: int, head_dim: int, page_tokens: int, n_pages: int,
                  dtype: torch.dtype = torch.bfloat16, k: Optional[torch.Tensor] = None,
-                 v: Optional[torch.Tensor] = None, device=None):
+                 v: Optional[torch.Tensor] = None, device=None,
+                 page_dtype: Optional[torch.dtype] = None,
+                 k_scales: Optional[torch.Tensor] = None,
+                 v_scales: Optional[torch.Tensor] = None):
         self.handle = None
         if dtype not in _DTYPES:
             raise ValueError("a paged cache holds float16 or bfloat16")
+        held = dtype if page_dtype is None else page_dtype
+        if held is not dtype and held is not _CODES:
+            raise ValueError("page_dtype is the cache's dtype or float8_e4m3fn")
         shape = (n_pages, page_tokens, kv_heads, head_dim)
         if (k is None) != (v is None):
             raise ValueError("give both k and v, or neither")
+        codes = held is _CODES
+        if (k_scales is None) != (v_scales is None) or (k_scales is not None) != (
+                codes and k is not None):
+            raise ValueError("codes that are given come with k_scales and v_scales, and nothing "
+                             "else does")
         if k is None:
             device = device or torch.device("cuda", torch.cuda.current_device())
-            k = torch.empty(shape, dtype=dtype, device=device)
-            v = torch.empty(shape, dtype=dtype, device=device)
+            k = torch.empty(shape, dtype=held, device=device)
+            v = torch.empty(shape, dtype=held, device=device)
+            if codes:
+                k_scales, v_scales = (torch.empty((n_pages, kv_heads), dtype=_SCALES,
+                                                  device=device) for _ in range(2))
         for t in (k, v):
-            if tuple(t.shape) != shape or t.dtype != dtype or not t.is_cuda or t.stride(3) != 1:
+            if tuple(t.shape) != shape or t.dtype != held or not t.is_cuda or t.stride(3) != 1:
                 raise ValueError("k and v must be device tensors [n_pages, page_tokens, kv_heads, "
                                  "head_dim] of the cache's type, each head contiguous")
         if k.stride() != v.stride() or k.device != v.device:
             raise ValueError("k and v must have the same strides and device")
+        for t in (k_scales, v_scales) if codes else ():
+            if (tuple(t.shape) != (n_pages, kv_heads) or t.dtype != _SCALES
+                    or t.device != k.device or not t.is_contiguous()):
+                raise ValueError("k_scales and v_scales must be contiguous float8_e8m0fnu "
+                                 "[n_pages, kv_heads] on the pages' device")
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
-        self.n_pages, self.dtype, self.k, self.v = n_pages, dtype, k, v
+        self.n_pages, self.dtype, self.page_dtype, self.k, self.v = n_pages, dtype, held, k, v
+        self.k_scales, self.v_scales = k_scales, v_scales
         self.device, self._index = k.device, k.device.index
         self._bounds_shape = (n_pages, kv_heads, 2, head_dim)
         # a dimension of one element has no stride to speak of
-        row = head_dim * 2
-        st = [s * 2 if n > 1 else max(s * 2, row) for s, n in zip(k.stride(), shape)]
+        size = 1 if codes else 2
+        row = head_dim * size
+        st = [s * size if n > 1 else max(s * size, row) for s, n in zip(k.stride(), shape)]
+        desc = ibp.ibp_paged_desc(k.data_ptr(), v.data_ptr(), st[0], st[2], st[1], n_pages,
+                                  page_tokens, kv_heads, head_dim, _DTYPES[dtype])
         self._lib = ibp._lib_handle()
         with torch.cuda.device(self._index):  # the handle belongs to the pages' device
-            self.handle = ibp.ibp_paged_create(ibp.ibp_paged_desc(
-                k.data_ptr(), v.data_ptr(), st[0], st[2], st[1], n_pages, page_tokens, kv_heads,
-                head_dim, _DTYPES[dtype]))
+            self.handle = (ibp.ibp_paged_create_8bit(desc, k_scales.data_ptr(),
+                                                     v_scales.data_ptr())
+                           if codes else ibp.ibp_paged_create(desc))
 
     # -- lifetime
     def close(self) -> None:
@@ -169,6 +208,11 @@ class PagedCache:
         new tokens), int32 on the device; n_tokens rows in all, of one sequence at
         most max_q_tokens."""
         return PagedBatch(page_table, kv_lens, q_starts, n_tokens, max_q_tokens)
+
+    def tables(self, n_seqs: int, max_pages: int) -> "PageTables":
+        """Page tables of n_seqs sequences of up to max_pages pages each, on the cache's
+        device: every sequence is empty, every page free."""
+        return PageTables(self, n_seqs, max_pages)
 
     def _heads(self, name: str, t: torch.Tensor, batch: PagedBatch, heads: Optional[int]) -> int:
         """Checks a [n_tokens, heads, head_dim] tensor; its token stride in bytes."""
@@ -332,3 +376,66 @@ class PagedCache:
                                               out.data_ptr(), _raw_stream(self._index)),
                    "ibp_paged_select")
         return out
+
+
+class PageTables:
+    """The pages that sequences of a cache hold, kept on the device: page_table [n_seqs,
+    max_pages], kv_lens [n_seqs], and the free pages free_pages[:n_free], int32.
+
+    Every sequence is empty at first and every page free; the tensors may be filled in
+    otherwise before a call."""
+
+    def __init__(self, cache: PagedCache, n_seqs: int, max_pages: int):
+        if n_seqs < 1 or max_pages < 1:
+            raise ValueError("page tables have sequences and columns")
+        self.cache, self.n_seqs, self.max_pages = cache, n_seqs, max_pages
+        dev = cache.device
+        self.page_table = torch.full((n_seqs, max_pages), -1, dtype=torch.int32, device=dev)
+        self.kv_lens = torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+        self.free_pages = torch.arange(cache.n_pages, dtype=torch.int32, device=dev).flip(0)
+        self._state = torch.tensor([cache.n_pages, 0], dtype=torch.int32, device=dev)
+        self.n_free = self._state[:1]
+        self._desc = ibp.ibp_paged_tables(
+            self.page_table.data_ptr(), self.kv_lens.data_ptr(), self.free_pages.data_ptr(),
+            self._state.data_ptr(), max_pages, n_seqs, max_pages)
+
+    def resize(self, target: torch.Tensor, n_tokens: int = 0,
+               max_q_tokens: Optional[int] = None, slots: Optional[torch.Tensor] = None,
+               stream=None) -> Optional[Tuple[PagedBatch, torch.Tensor]]:
+        """Sequence s gets target[s] tokens (int32 [n_seqs] on the device): pages come from the
+        free ones or go back to them.  n_tokens: rows of the new tokens' arrays, at least
+        what sequences grow by together; of one at most max_q_tokens (n_tokens).  Returns the
+        batch of the new tokens, whose lengths and table are these, and their slots (int64
+        [n_tokens]: page * page_tokens + place, rows of key_rows() and value_rows()); nothing
+        when n_tokens is 0: such a call only shrinks.
+
+        Where that cannot be done as a whole nothing changes, the batch is empty, and
+        the cache's status says IBP_ERANGE."""
+        if stream is not None:
+            with torch.cuda.stream(_as_stream(stream)):
+                return self.resize(target, n_tokens, max_q_tokens, slots)
+        cache, index = self.cache, self.cache._index
+        if (target.shape != self.kv_lens.shape or target.dtype != torch.int32
+                or target.get_device() != index or not target.is_contiguous()):
+            raise ValueError("target must be a contiguous int32 [n_seqs] on the cache's device")
+        if n_tokens < 0:
+            raise ValueError("n_tokens is not negative")
+        q_starts = None
+        if n_tokens:
+            if slots is None:
+                slots = torch.empty(n_tokens, dtype=torch.int64, device=cache.device)
+            elif (slots.shape != (n_tokens,) or slots.dtype != torch.int64
+                  or slots.get_device() != index or not slots.is_contiguous()):
+                raise ValueError("slots must be a contiguous int64 [n_tokens] on the cache's "
+                                 "device")
+            q_starts = torch.empty(self.n_seqs + 1, dtype=torch.int32, device=cache.device)
+        elif slots is not None:
+            raise ValueError("a call without new tokens has no slots")
+        ibp._check(cache._lib.ibp_paged_resize(
+            cache.handle, ctypes.addressof(self._desc), target.data_ptr(),
+            q_starts.data_ptr() if n_tokens else None, slots.data_ptr() if n_tokens else None,
+            n_tokens, _raw_stream(index)), "ibp_paged_resize")
+        if not n_tokens:
+            return None
+        return (PagedBatch(self.page_table, self.kv_lens, q_starts, n_tokens,
+                           n_tokens if max_q_tokens is None else max_q_tokens), slots)
