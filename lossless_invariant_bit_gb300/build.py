@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libibp.so")
 SOURCES = ["ibp_kernels.cu", "ibp_api.cu", "ibp_noalloc.cu", "ibp_transfer.cu", "ibp_project.cu",
            "ibp_launch.cu", "ibp_paged.cu", "ibp_paged_step.cu",
            "ibp_paged_chunk.cu", "ibp_paged_api.cu", "ibp_paged8.cu", "ibp_paged8_step.cu",
-           "ibp_paged_tables.cu", "ibp_paged8_api.cu"]
+           "ibp_paged8_chunk.cu", "ibp_paged_tables.cu", "ibp_paged8_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

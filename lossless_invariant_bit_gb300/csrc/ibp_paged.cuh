@@ -106,7 +106,7 @@ struct PagedLaunches {
   decltype(&launch_paged_append) append;
   decltype(&launch_paged_bounds) bounds;
   decltype(&launch_paged_step) step;
-  decltype(&launch_paged_chunk) chunk;  // NULL: the step kernel takes every sequence
+  decltype(&launch_paged_chunk) chunk;
   decltype(&launch_paged_chunk_join) chunk_join;
 };
 

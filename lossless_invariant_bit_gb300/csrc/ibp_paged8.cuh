@@ -12,6 +12,9 @@ cudaError_t launch_paged8_bounds(const PagedGeom& g, const PagedBatchView& b, ui
                                  cudaStream_t st);
 cudaError_t launch_paged8_step(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
                                bool behind, cudaStream_t st);
+cudaError_t launch_paged8_chunk(const PagedAttnArgs& a, const PagedMaps& m, int sm_count,
+                                cudaStream_t st);
+cudaError_t launch_paged8_chunk_join(const PagedAttnArgs& a, int sm_count, cudaStream_t st);
 
 // Bytes of scales: 2^-50 to 2^50.  The range is bounded so that no power of a page's scale,
 // nor the product of two pages', leaves fp32 where a result still depends on it.
@@ -58,6 +61,7 @@ __device__ __forceinline__ uint32_t code_chunk(uint32_t row, uint32_t chunk) {
 // magnitude into [2^14, 2^15).
 struct Lift {
   float up, down;
+  uint8_t byte;  // down's exponent, as a scale's
 };
 // The larger magnitude of two bf16 values as bits, infinities and NaN apart.
 __device__ __forceinline__ uint32_t bf16_top(uint32_t x) {
@@ -67,7 +71,7 @@ __device__ __forceinline__ uint32_t bf16_top(uint32_t x) {
 __device__ __forceinline__ Lift row_lift(uint32_t top) {
   const int32_t up = min(126, 14 + 127 - (int32_t)(top >> 7));  // (top: 254 at most, so >= -113)
   return Lift{__uint_as_float((uint32_t)(127 + up) << 23),
-              __uint_as_float((uint32_t)(127 - up) << 23)};
+              __uint_as_float((uint32_t)(127 - up) << 23), (uint8_t)(127 - up)};
 }
 __device__ __forceinline__ uint32_t bf16_to_fp16(uint32_t x, float up) {
   return pack2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xFFFF0000u) * up, 0u);

@@ -298,10 +298,9 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
   // kernel, the others to the chunk kernel; a batch may need both, and the step kernel's
   // CTAs then fill the SMs that the chunk kernel's have left.
   const ibp::PagedLaunches& run = *c->launches;
-  const bool few =
-      selected || !run.chunk || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
+  const bool few = selected || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
   const bool both = !few && b->n_seqs > 1u;
-  a.max_rows = !run.chunk ? ~0u : few || both ? ibp::kStepRows : 0u;
+  a.max_rows = few || both ? ibp::kStepRows : 0u;
   std::lock_guard<std::mutex> lock(call_lock(workspace));
   cudaError_t ce = few ? cudaSuccess : run.chunk(a, c->maps, c->sm_count, st);
   if (ce == cudaSuccess && (few || both))
