@@ -33,6 +33,8 @@
 namespace ibp {
 namespace {
 
+constexpr uint32_t kWarps = 4, kThreads = 32 * (kWarps + 1);
+
 // Weights are rounded to 16 bits for the product with the values.  In fp16 they are 2^14
 // times the formula's, the sum with them (the result does not change): the largest is
 // 2^14, and what is 2^-28 of it still a normal number.  Unlifted, many keys of weights below
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  Run run = step_run<kSel>(a, s_scan, s_found);
+  Run run = step_run<kSel, kThreads>(a, s_scan, s_found);
   Cursor& ld = run.ld;
   const uint64_t u0 = run.u0, u1 = run.u1;
   if (warp == kWarps) {
@@ -398,9 +400,9 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
               make_float2(o[i][2 * e], o[i][2 * e + 1]);
       }
       asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
-      merge_rows<kDP, kBf16, step_lift<kBf16>()>(a, t, rows, merge, pieces);
+      merge_rows<kDP, kBf16, step_lift<kBf16>(), kWarps>(a, t, rows, merge, pieces);
       // the sums have been read: the next tile may write its own
-      if (any_of_four(!go || count == 0)) break;
+      if (any_of<kWarps>(!go || count == 0)) break;
     }
   }
   __syncthreads();

@@ -11,7 +11,7 @@
 namespace ibp {
 namespace {
 
-constexpr uint32_t kWarps = 4, kBlock = 128, kWarpKeys = 32, kThreads = 32 * (kWarps + 1);
+constexpr uint32_t kBlock = 128, kWarpKeys = 32;
 constexpr uint32_t kMaxCtas = 512;
 // in the place of a box's first position: nothing to read, a page id out of range
 constexpr uint32_t kNoPage = 0xFFFFFFFFu, kBadPage = 0xFFFFFFFEu;
@@ -32,7 +32,8 @@ struct Join {
 };
 
 // What the producer tells the others of a run of blocks of one tile; count 0: no
-// more.  A ring of 8: the producer is at most 3 blocks ahead.
+// more.  A ring of 8: the producer has at most kStages blocks (each of a tile of its own,
+// at worst) before it and tells of one more, while the others still write a tile's rows.
 struct Info {
   uint32_t count;         // blocks
   uint32_t q0, head;      // first row of the sequence (or the token), K/V head
@@ -137,8 +138,9 @@ struct Run {
   uint32_t ctas;    // CTAs with a run: never more than blocks
 };
 
-template <bool kSel>
-__device__ __forceinline__ Run step_run(const PagedAttnArgs& a, uint64_t (&s_scan)[kWarps + 1],
+template <bool kSel, uint32_t kThreads>
+__device__ __forceinline__ Run step_run(const PagedAttnArgs& a,
+                                        uint64_t (&s_scan)[kThreads / 32],
                                         uint64_t (&s_found)[2]) {
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u, tid = threadIdx.x;
   Run r;
@@ -175,7 +177,7 @@ __device__ __forceinline__ Run step_run(const PagedAttnArgs& a, uint64_t (&s_sca
     for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
     if (lane == 0) s_scan[warp] = mine;
     __syncthreads();
-    for (uint32_t w = 0; w <= kWarps; ++w) total += s_scan[w];
+    for (uint32_t w = 0; w < kThreads / 32; ++w) total += s_scan[w];
     total *= a.g.H;
     if (total < ctas) ctas = (uint32_t)total;
     if (blockIdx.x < ctas) {
@@ -200,7 +202,7 @@ __device__ __forceinline__ Run step_run(const PagedAttnArgs& a, uint64_t (&s_sca
       if (lane == 31u) s_scan[warp] = inc;
       __syncthreads();
       uint64_t before = 0, all = 0;
-      for (uint32_t w = 0; w <= kWarps; ++w) {
+      for (uint32_t w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before += s_scan[w];
         all += s_scan[w];
       }
@@ -268,14 +270,15 @@ __device__ __forceinline__ uint32_t tell_tile(const PagedAttnArgs& a, const Run&
   return count;
 }
 
-// A barrier of the four warps that compute, and whether any of their threads says so.
-__device__ __forceinline__ bool any_of_four(bool mine) {
+// A barrier of the kCount warps that compute, and whether any of their threads says so.
+template <uint32_t kCount>
+__device__ __forceinline__ bool any_of(bool mine) {
   uint32_t any;
   asm volatile(
       "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n"
-      " barrier.cta.red.or.pred q, 1, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      " barrier.cta.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(any)
-      : "r"((uint32_t)mine)
+      : "r"((uint32_t)mine), "n"(32u * kCount)
       : "memory");
   return any != 0u;
 }
@@ -297,19 +300,19 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& a, uint64_t at, u
     a.lse[at] = some ? (m - (float)kLift + log2f(l)) * 0.69314718056f : -INFINITY;
 }
 
-// The four warps' rows of a tile (or of this CTA's run of it), joined: the result, or a
+// The kCount warps' rows of a tile (or of this CTA's run of it), joined: the result, or a
 // piece of it.  A warp's rows lie in `merge`: outputs, then maximum, sum and whether it
 // could not be read.
-template <int kDP, bool kBf16, int kLift>
+template <int kDP, bool kBf16, int kLift, uint32_t kCount>
 __device__ __forceinline__ void merge_rows(const PagedAttnArgs& a, const Info* t, uint32_t rows,
                                            const float* merge, Piece<kDP>* pieces) {
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31u;
   Piece<kDP>* piece = pieces + 2u * blockIdx.x + t->place;
-  for (uint32_t r = warp; r < rows; r += kWarps) {
-    float mm[kWarps], mx = -INFINITY, ll = 0.f, ov[kDP / 32];
+  for (uint32_t r = warp; r < rows; r += kCount) {
+    float mm[kCount], mx = -INFINITY, ll = 0.f, ov[kDP / 32];
     bool isbad = false;
 #pragma unroll
-    for (uint32_t w = 0; w < kWarps; ++w) {
+    for (uint32_t w = 0; w < kCount; ++w) {
       mm[w] = merge[(w * 16u + r) * (kDP + 4u) + kDP];
       mx = fmaxf(mx, mm[w]);
       isbad = isbad || merge[(w * 16u + r) * (kDP + 4u) + kDP + 2u] != 0.f;
@@ -318,7 +321,7 @@ __device__ __forceinline__ void merge_rows(const PagedAttnArgs& a, const Info* t
 #pragma unroll
     for (int i = 0; i < kDP / 32; ++i) ov[i] = 0.f;
 #pragma unroll
-    for (uint32_t w = 0; w < kWarps; ++w) {
+    for (uint32_t w = 0; w < kCount; ++w) {
       const float* src = merge + (w * 16u + r) * (kDP + 4u);
       const float f = ex2(mm[w] - base);
       ll += f * src[kDP + 1];
