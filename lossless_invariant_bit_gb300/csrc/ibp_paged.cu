@@ -22,6 +22,8 @@ namespace {
 // four 53, 12 CTAs and two 51, 16 CTAs (32 registers, spilled) 52 to 55.
 template <int kLanes, int kAhead, bool kBf16, bool kPairs>
 __global__ void __launch_bounds__(128, 10) k_paged_append(PagedAppendArgs a, uint32_t per) {
+  // (for the kernel of 8-bit keys and values behind the queries', which waits for this one)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr uint32_t kSubs = 128u / kLanes;  // heads side by side
   const uint32_t lane = threadIdx.x & (kLanes - 1u), sub = threadIdx.x / kLanes;
   const uint32_t t = blockIdx.x;

@@ -13,22 +13,26 @@ __device__ __forceinline__ uint32_t scale_for(float m) {
   return (uint32_t)min(max(e, (int32_t)kScaleLow), (int32_t)kScaleHigh);
 }
 
-// Two values over a scale as two codes: to the nearest, ties to even; what is not finite
-// becomes NaN (x * 0 is), what the largest scale does not hold the largest code.
-__device__ __forceinline__ uint32_t codes2(float lo, float hi, float inv) {
+// Two values over a scale as two codes: to the nearest, ties to even, what the largest scale
+// does not hold the largest code; NaN stays NaN.
+__device__ __forceinline__ uint32_t codes2(uint64_t x, uint64_t inv) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-      : "=h"(r)
-      : "f"(fmaf(hi, 0.f, hi * inv)), "f"(fmaf(lo, 0.f, lo * inv)));
+  float lo, hi;
+  halves2(mul2(x, inv), lo, hi);
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// Infinities become NaN (x * 0 is).
+__device__ __forceinline__ uint64_t without_inf(uint64_t x) { return fma2(x, 0ull, x); }
 
 // Four codes under a larger scale.
 __device__ __forceinline__ uint32_t rescale4(uint32_t x, float f) {
   uint32_t p[2];
   codes_to_fp16(x, p[0], p[1]);
   const float2 u = unpack2(p[0], 0u), v = unpack2(p[1], 0u);
-  return codes2(u.x, u.y, f) | codes2(v.x, v.y, f) << 16;
+  const uint64_t f2 = pair2(f, f);
+  return codes2(pair2(u.x, u.y), f2) | codes2(pair2(v.x, v.y), f2) << 16;
 }
 
 // ---------------------------------------------------------------- append
@@ -39,7 +43,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t x, float f) {
 // caches the second time.  A lane's channels are the 16-bit append's: 4 and their
 // rotation partners.
 template <int kLanes, bool kBf16, bool kPairs>
-__global__ void __launch_bounds__(128) k_paged8_append(PagedAppendArgs a, uint32_t unit_lg) {
+__device__ __forceinline__ void append_units(const PagedAppendArgs& a, uint32_t unit_lg,
+                                             uint32_t per) {
   constexpr int kTokens = 4;
   __shared__ float s_top[4];
   const uint32_t unit = 1u << unit_lg, tid = threadIdx.x;
@@ -73,163 +78,184 @@ __global__ void __launch_bounds__(128) k_paged8_append(PagedAppendArgs a, uint32
     t1 = a.n_pos > p0 ? a.n_pos - p0 : 0u;
   }
   if (t1 <= t0) return;
-  // this unit's head: keys', then values'
-  const uint32_t u = blockIdx.y * (128u >> unit_lg) + (tid >> unit_lg);
-  const bool live = u < 2u * a.g.H, keys = u < a.g.H;
-  const uint32_t h = !live ? 0u : keys ? u : u - a.g.H;
-  uint8_t* scale = (keys ? a.g.k_scales : a.g.v_scales) + (uint64_t)(uint32_t)page * a.g.H + h;
-  uint32_t was = t0 && live ? *scale : 0u;
-  const bool mine = live && lane * 8u < a.g.D;
-  const uint32_t half = a.rot / 2u;
-  const bool turned = keys && lane * 8u < a.rot, split = !kPairs && lane * 8u < a.rot;
-  const uint32_t c0 = split ? lane * 4u : lane * 8u, c1 = split ? half + lane * 4u : c0 + 4u;
-  // row of slot t in the call's arrays: q0 + (p0 + t) - (L - n)
-  const uint8_t* src = (keys ? a.kx : a.vx) + (uint64_t)h * a.g.D * 2u;
-  const int64_t row0 = (int64_t)q.q0 + p0 - ((int64_t)q.L - q.n);
-  uint8_t* dst = (keys ? a.g.k : a.g.v) + (uint64_t)(uint32_t)page * a.g.page_stride +
-                 h * a.g.head_stride;
-  uint64_t w[4] = {};  // the norm's weights
-  if (a.k_norm && mine) {
-    const uint2 x = __ldg(reinterpret_cast<const uint2*>(a.k_norm + c0 * 2u));
-    const uint2 y = __ldg(reinterpret_cast<const uint2*>(a.k_norm + c1 * 2u));
-    const uint32_t z[4] = {x.x, x.y, y.x, y.y};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 f = unpack2(z[k], kBf16);
-      w[k] = pair2(f.x, f.y);
-    }
-  }
-  const float inv_d = 1.f / (float)a.g.D;
-  uint64_t f[kTokens][4];
-  // the values of the unit's tokens from slot `at` on
-  auto compute = [&](uint32_t at) {
-    uint2 x[kTokens][2];
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      const uint32_t t = at + i * rows + row;
-      x[i][0] = x[i][1] = make_uint2(0u, 0u);
-      if (mine && t >= t0 && t < t1) {
-        const uint8_t* p = src + (uint64_t)(row0 + t) * a.kv_stride;
-        x[i][0] = __ldg(reinterpret_cast<const uint2*>(p + c0 * 2u));
-        x[i][1] = __ldg(reinterpret_cast<const uint2*>(p + c1 * 2u));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      const uint32_t t = at + i * rows + row;
-      const uint32_t z[4] = {x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y};
+  // the CTA's units, a round of 128 / unit of them at a time: keys' heads, then values'
+  for (uint32_t round = 0; round < per; ++round) {
+    const uint32_t u = (blockIdx.y * per + round) * (128u >> unit_lg) + (tid >> unit_lg);
+    const bool live = u < 2u * a.g.H, keys = u < a.g.H;
+    const uint32_t h = !live ? 0u : keys ? u : u - a.g.H;
+    uint8_t* scale = (keys ? a.g.k_scales : a.g.v_scales) + (uint64_t)(uint32_t)page * a.g.H + h;
+    uint32_t was = t0 && live ? *scale : 0u;
+    const bool mine = live && lane * 8u < a.g.D;
+    const uint32_t half = a.rot / 2u;
+    const bool turned = keys && lane * 8u < a.rot, split = !kPairs && lane * 8u < a.rot;
+    const uint32_t c0 = split ? lane * 4u : lane * 8u, c1 = split ? half + lane * 4u : c0 + 4u;
+    // row of slot t in the call's arrays: q0 + (p0 + t) - (L - n)
+    const uint8_t* src = (keys ? a.kx : a.vx) + (uint64_t)h * a.g.D * 2u;
+    const int64_t row0 = (int64_t)q.q0 + p0 - ((int64_t)q.L - q.n);
+    uint8_t* dst = (keys ? a.g.k : a.g.v) + (uint64_t)(uint32_t)page * a.g.page_stride +
+                   h * a.g.head_stride;
+    uint64_t w[4] = {};  // the norm's weights
+    if (a.k_norm && mine) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(a.k_norm + c0 * 2u));
+      const uint2 y = __ldg(reinterpret_cast<const uint2*>(a.k_norm + c1 * 2u));
+      const uint32_t z[4] = {x.x, x.y, y.x, y.y};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 v = unpack2(z[k], kBf16);
-        f[i][k] = pair2(v.x, v.y);
+        const float2 f = unpack2(z[k], kBf16);
+        w[k] = pair2(f.x, f.y);
       }
-      if (a.k_norm) {  // (every lane of the warp comes to the shuffles)
-        uint64_t s2 = mul2(f[i][0], f[i][0]);
+    }
+    const float inv_d = 1.f / (float)a.g.D;
+    uint64_t f[kTokens][4];
+    // the values of the unit's tokens from slot `at` on
+    auto compute = [&](uint32_t at) {
+      uint2 x[kTokens][2];
 #pragma unroll
-        for (int k = 1; k < 4; ++k) s2 = fma2(f[i][k], f[i][k], s2);
-        float sum, odd;
-        halves2(s2, sum, odd);
-        sum += odd;
-#pragma unroll
-        for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-        const float n = rsqrtf(fmaf(sum, inv_d, a.eps));
-        if (keys)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) f[i][k] = mul2(f[i][k], mul2(pair2(n, n), w[k]));
+      for (int i = 0; i < kTokens; ++i) {
+        const uint32_t t = at + i * rows + row;
+        x[i][0] = x[i][1] = make_uint2(0u, 0u);
+        if (mine && t >= t0 && t < t1) {
+          const uint8_t* p = src + (uint64_t)(row0 + t) * a.kv_stride;
+          x[i][0] = __ldg(reinterpret_cast<const uint2*>(p + c0 * 2u));
+          x[i][1] = __ldg(reinterpret_cast<const uint2*>(p + c1 * 2u));
+        }
       }
-      if (a.cos_sin && turned && t >= t0 && t < t1) {
-        const float* cs = a.cos_sin + (uint64_t)(p0 + t) * a.rot + lane * 4u;
-        const float4 cc = __ldg(reinterpret_cast<const float4*>(cs));
-        const float4 ss = __ldg(reinterpret_cast<const float4*>(cs + half));
-        if (kPairs) {
-          const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+      for (int i = 0; i < kTokens; ++i) {
+        const uint32_t t = at + i * rows + row;
+        const uint32_t z[4] = {x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = unpack2(z[k], kBf16);
+          f[i][k] = pair2(v.x, v.y);
+        }
+        if (a.k_norm && (keys || unit < 32u)) {  // (all lanes of a warp, or none)
+          uint64_t s2 = mul2(f[i][0], f[i][0]);
+#pragma unroll
+          for (int k = 1; k < 4; ++k) s2 = fma2(f[i][k], f[i][k], s2);
+          float sum, odd;
+          halves2(s2, sum, odd);
+          sum += odd;
+#pragma unroll
+          for (int d = kLanes / 2; d; d >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+          const float n = rsqrtf(fmaf(sum, inv_d, a.eps));
+          if (keys)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[i][k] = mul2(f[i][k], mul2(pair2(n, n), w[k]));
+        }
+        if (a.cos_sin && turned && t >= t0 && t < t1) {
+          const float* cs = a.cos_sin + (uint64_t)(p0 + t) * a.rot + lane * 4u;
+          const float4 cc = __ldg(reinterpret_cast<const float4*>(cs));
+          const float4 ss = __ldg(reinterpret_cast<const float4*>(cs + half));
+          if (kPairs) {
+            const float c4[4] = {cc.x, cc.y, cc.z, cc.w}, s4[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float x0, x1;
+              halves2(f[i][k], x0, x1);
+              f[i][k] = fma2(f[i][k], pair2(c4[k], c4[k]), mul2(pair2(-x1, x0), pair2(s4[k], s4[k])));
+            }
+          } else {
+            const uint64_t c2[2] = {pair2(cc.x, cc.y), pair2(cc.z, cc.w)};
+            const uint64_t s2[2] = {pair2(ss.x, ss.y), pair2(ss.z, ss.w)};
+            const uint64_t m2[2] = {pair2(-ss.x, -ss.y), pair2(-ss.z, -ss.w)};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint64_t x0 = f[i][k], x1 = f[i][k + 2];
+              f[i][k] = fma2(x0, c2[k], mul2(x1, m2[k]));
+              f[i][k + 2] = fma2(x1, c2[k], mul2(x0, s2[k]));
+            }
+          }
+        }
+      }
+    };
+    const uint32_t step = rows * kTokens;
+    const uint32_t begin = t0 & ~(step - 1u);
+    uint32_t at;
+    float top;
+    // The largest magnitude (NaN have no part in it); where it is infinite, once more without
+    // infinities, which become NaN codes.
+    bool odd = false;
+    while (true) {
+      top = 0.f;
+      for (at = begin;; at += step) {
+        compute(at);
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float x0, x1;
-            halves2(f[i][k], x0, x1);
-            f[i][k] = fma2(f[i][k], pair2(c4[k], c4[k]), mul2(pair2(-x1, x0), pair2(s4[k], s4[k])));
+            if (odd) f[i][k] = without_inf(f[i][k]);
+            float x, y;
+            halves2(f[i][k], x, y);
+            top = fmaxf(top, fmaxf(fabsf(x), fabsf(y)));
           }
-        } else {
-          const uint64_t c2[2] = {pair2(cc.x, cc.y), pair2(cc.z, cc.w)};
-          const uint64_t s2[2] = {pair2(ss.x, ss.y), pair2(ss.z, ss.w)};
-          const uint64_t m2[2] = {pair2(-ss.x, -ss.y), pair2(-ss.z, -ss.w)};
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint64_t x0 = f[i][k], x1 = f[i][k + 2];
-            f[i][k] = fma2(x0, c2[k], mul2(x1, m2[k]));
-            f[i][k + 2] = fma2(x1, c2[k], mul2(x0, s2[k]));
+        if (at + step >= t1) break;
+      }
+      for (uint32_t d = 1; d < (unit < 32u ? unit : 32u); d <<= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+      if (unit > 32u) {
+        __syncthreads();  // (what the last round wrote there has been read)
+        if ((tid & 31u) == 0u) s_top[tid >> 5] = top;
+        __syncthreads();
+        const uint32_t w0 = tid >> unit_lg << (unit_lg - 5u);
+        for (uint32_t i = 0; i < unit / 32u; ++i) top = fmaxf(top, s_top[w0 + i]);
+      }
+      if (odd || !__syncthreads_or(top == INFINITY)) break;
+      odd = true;
+    }
+    uint32_t byte = scale_for(top);
+    if (t0 && live) {
+      if (scale_ok(was)) {
+        byte = max(byte, was);
+      } else {
+        if (ut == 0) set_status(a.g.status, IBP_ERANGE);
+        was = byte;  // what the page holds has no value: it is left
+      }
+      if (byte > was) {  // the codes that it holds, under the new scale
+        const float down = scale_of(127u + was - byte);
+        for (uint32_t t = row; t < t0; t += rows)
+          if (mine) {
+            uint32_t* p0 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c0);
+            uint32_t* p1 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c1);
+            *p0 = rescale4(*p0, down);
+            *p1 = rescale4(*p1, down);
           }
-        }
       }
     }
-  };
-  const uint32_t step = rows * kTokens;
-  float top = 0.f;
-  uint32_t at = t0 & ~(step - 1u);
-  const uint32_t begin = at;
-  for (;; at += step) {
-    compute(at);
+    if (ut == 0 && live) *scale = (uint8_t)byte;
+    const float down = scale_of(254u - byte);
+    const uint64_t inv = pair2(down, down);
+    // backwards, beginning with what is still in registers
+    for (;; at -= step) {
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i)
+      for (int i = 0; i < kTokens; ++i) {
+        const uint32_t t = at + i * rows + row;
+        if (!mine || t < t0 || t >= t1) continue;
+        uint32_t z[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float x, y;
-        halves2(f[i][k], x, y);
-        x = fabsf(x), y = fabsf(y);
-        top = fmaxf(top, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
+        for (int k = 0; k < 2; ++k)
+          z[k] = codes2(f[i][2 * k], inv) | codes2(f[i][2 * k + 1], inv) << 16;
+        *reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c0) = z[0];
+        *reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c1) = z[1];
       }
-    if (at + step >= t1) break;
-  }
-  for (uint32_t d = 1; d < (unit < 32u ? unit : 32u); d <<= 1)
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-  if (unit > 32u) {
-    if ((tid & 31u) == 0u) s_top[tid >> 5] = top;
-    __syncthreads();
-    const uint32_t w0 = tid >> unit_lg << (unit_lg - 5u);
-    for (uint32_t i = 0; i < unit / 32u; ++i) top = fmaxf(top, s_top[w0 + i]);
-  }
-  uint32_t byte = scale_for(top);
-  if (!live) return;  // (no shuffle or barrier follows, but for those of compute below)
-  if (t0) {
-    if (scale_ok(was)) {
-      byte = max(byte, was);
-    } else {
-      if (ut == 0) set_status(a.g.status, IBP_ERANGE);
-      was = byte;  // what the page holds has no value: it is left
-    }
-    if (byte > was) {  // the codes that it holds, under the new scale
-      const float down = scale_of(127u + was - byte);
-      for (uint32_t t = row; t < t0; t += rows)
-        if (mine) {
-          uint32_t* p0 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c0);
-          uint32_t* p1 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c1);
-          *p0 = rescale4(*p0, down);
-          *p1 = rescale4(*p1, down);
-        }
-    }
-  }
-  if (ut == 0) *scale = (uint8_t)byte;
-  const float inv = scale_of(254u - byte);
-  // backwards, beginning with what is still in registers
-  for (;; at -= step) {
+      if (at == begin) break;
+      compute(at - step);
+      if (odd)
 #pragma unroll
-    for (int i = 0; i < kTokens; ++i) {
-      const uint32_t t = at + i * rows + row;
-      if (!mine || t < t0 || t >= t1) continue;
-      uint32_t z[2];
+        for (int i = 0; i < kTokens; ++i)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float x0, x1, x2, x3;
-        halves2(f[i][2 * k], x0, x1);
-        halves2(f[i][2 * k + 1], x2, x3);
-        z[k] = codes2(x0, x1, inv) | codes2(x2, x3, inv) << 16;
-      }
-      *reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c0) = z[0];
-      *reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c1) = z[1];
+          for (int k = 0; k < 4; ++k) f[i][k] = without_inf(f[i][k]);
     }
-    if (at == begin) break;
-    compute(at - step);
   }
+}
+
+// Behind the kernel of the queries, beside which it may run; it ends after it, so that what
+// follows may count on both.
+template <int kLanes, bool kBf16, bool kPairs>
+__global__ void __launch_bounds__(128) k_paged8_append(PagedAppendArgs a, uint32_t unit_lg,
+                                                       uint32_t per) {
+  append_units<kLanes, kBf16, kPairs>(a, unit_lg, per);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------- bounds
@@ -241,6 +267,7 @@ __global__ void __launch_bounds__(128)
     k_paged8_bounds(PagedGeom g, PagedBatchView b, uint8_t* bounds) {
   // the scores' CTAs may come up beside this kernel (they wait for its end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  constexpr uint32_t kAhead = 8;
   const uint32_t lane = threadIdx.x & 31u, sub = lane & (kLanes - 1u), row = lane / kLanes;
   const uint64_t id = (uint64_t)blockIdx.x * 4u + (threadIdx.x >> 5);
   const uint32_t tile = (uint32_t)(id / g.H), h = (uint32_t)(id % g.H);
@@ -257,13 +284,11 @@ __global__ void __launch_bounds__(128)
   const uint32_t p = (from >> g.page_lg) + (tile - first);
   if (p > (q.L - 1u) >> g.page_lg) return;
   const int32_t page = __ldg(b.table + s * b.table_stride + p);
-  uint32_t byte = 0;
-  if (page >= 0 && (uint32_t)page < g.n_pages)
-    byte = __ldg(g.k_scales + (uint64_t)(uint32_t)page * g.H + h);
-  if (!scale_ok(byte)) {
+  if (page < 0 || (uint32_t)page >= g.n_pages) {
     if (lane == 0) set_status(g.status, IBP_ERANGE);
     return;
   }
+  const uint32_t byte = __ldg(g.k_scales + (uint64_t)(uint32_t)page * g.H + h);
   const uint32_t held = min(P, q.L - p * P);
   const uint8_t* src = g.k + (uint64_t)(uint32_t)page * g.page_stride + h * g.head_stride +
                        sub * 16u;
@@ -274,23 +299,33 @@ __global__ void __launch_bounds__(128)
     lo[i] = __half2half2(__ushort_as_half(0x7C00u));
     hi[i] = __half2half2(__ushort_as_half(0xFC00u));
   }
-  if (mine) {
-#pragma unroll 4
-    for (uint32_t t = row; t < held; t += 32u / kLanes) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(src + t * g.token_stride));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if (mine)
+    for (uint32_t t0 = row; t0 < held; t0 += kAhead * (32u / kLanes)) {
+      uint4 x[kAhead];  // on their way together; behind the last, the first once more
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t y[2];
-        codes_to_fp16(w[i], y[0], y[1]);
+      for (uint32_t i = 0; i < kAhead; ++i) {
+        const uint32_t t = t0 + i * (32u / kLanes);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(src + (t < held ? t : t0) * g.token_stride));
+      }
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const __half2 v = *reinterpret_cast<const __half2*>(&y[k]);
-          lo[2 * i + k] = __hmin2_nan(lo[2 * i + k], v);
-          hi[2 * i + k] = __hmax2_nan(hi[2 * i + k], v);
+      for (uint32_t k = 0; k < kAhead; ++k) {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t y[2];
+          codes_to_fp16(w[i], y[0], y[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const __half2 v = *reinterpret_cast<const __half2*>(&y[k]);
+            lo[2 * i + k] = __hmin2_nan(lo[2 * i + k], v);
+            hi[2 * i + k] = __hmax2_nan(hi[2 * i + k], v);
+          }
         }
       }
     }
+  if (!scale_ok(byte)) {
+    if (lane == 0) set_status(g.status, IBP_ERANGE);
+    return;
   }
 #pragma unroll
   for (int d = kLanes; d < 32; d <<= 1)
@@ -329,23 +364,34 @@ cudaError_t launch_paged8_append(const PagedAppendArgs& a, int sm_count, cudaStr
   uint32_t unit_lg = 7;
   while (unit_lg > 4u && (1u << unit_lg) > (lanes << a.g.page_lg) / 4u) --unit_lg;
   const uint64_t tiles = ((uint64_t)a.b.n_tokens >> a.g.page_lg) + 2ull * a.b.n_seqs;
-  const uint64_t y = (2ull * a.g.H + (128u >> unit_lg) - 1u) / (128u >> unit_lg);
+  const uint64_t rounds = (2ull * a.g.H + (128u >> unit_lg) - 1u) / (128u >> unit_lg);
+  // Rounds of a CTA: as many as leave 6 CTAs to each SM (what a CTA looks up before its first
+  // is 3 us of waiting).
+  const uint64_t full = ((uint64_t)a.b.n_tokens >> a.g.page_lg) + 1u;
+  uint64_t per = rounds * full / (6ull * sm_count);
+  per = per < 1u ? 1u : per > rounds ? rounds : per;
+  const uint64_t y = (rounds + per - 1u) / per;
   if (tiles > 0x7FFFFFFFull || y > 65535u) return cudaErrorInvalidValue;
-  const dim3 grid((unsigned)tiles, (unsigned)y);
-#define IBP_CALL(L, B)                                                                       \
-  do {                                                                                       \
-    if (a.pairs) k_paged8_append<L, B, true><<<grid, 128, 0, st>>>(a, unit_lg);              \
-    else k_paged8_append<L, B, false><<<grid, 128, 0, st>>>(a, unit_lg);                     \
-  } while (0)
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)tiles, (unsigned)y, 1);
+  cfg.blockDim = dim3(128, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.Hq ? 1 : 0;
+#define IBP_CALL(L, B)                                                                        \
+  return a.pairs                                                                              \
+             ? cudaLaunchKernelEx(&cfg, k_paged8_append<L, B, true>, a, unit_lg, (uint32_t)per) \
+             : cudaLaunchKernelEx(&cfg, k_paged8_append<L, B, false>, a, unit_lg, (uint32_t)per)
   if (lanes == 8u) {
     if (a.g.bf16) IBP_CALL(8, true);
-    else IBP_CALL(8, false);
-  } else {
-    if (a.g.bf16) IBP_CALL(16, true);
-    else IBP_CALL(16, false);
+    IBP_CALL(8, false);
   }
+  if (a.g.bf16) IBP_CALL(16, true);
+  IBP_CALL(16, false);
 #undef IBP_CALL
-  return cudaGetLastError();
 }
 
 cudaError_t launch_paged8_bounds(const PagedGeom& g, const PagedBatchView& b, uint8_t* bounds,

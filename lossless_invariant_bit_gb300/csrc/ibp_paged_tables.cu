@@ -13,14 +13,15 @@
 // hand-over would cost another launch), then takes an equal part of the pages, or of the new
 // tokens.  A call that cannot be served as a whole changes nothing: every CTA finds the
 // same sums.  Lengths and the list's length change when the last CTA has ended, since
-// all of them read the old ones.
+// all of them read the old ones.  Few sequences and tokens go to one CTA, which does one after
+// the other and needs one launch.
 #include "ibp_paged.cuh"
 #include "ibp_sm103.cuh"
 
 namespace ibp {
 namespace {
 
-constexpr uint32_t kThreads = 256, kWarps = kThreads / 32;
+constexpr uint32_t kThreads = 256;
 
 struct Sums {
   uint64_t gone, come, rows;
@@ -54,16 +55,20 @@ __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
   return x;
 }
 
-// The sums over all sequences, and whether the call can be served.
-__device__ __forceinline__ bool total(const PagedTablesArgs& a, Sums& t, uint32_t& n_free) {
-  __shared__ uint64_t s_sum[3][kWarps];
+// The sums over all sequences, and whether the call can be served; `own`: of sequence
+// threadIdx.x.
+template <uint32_t kT>
+__device__ __forceinline__ bool total(const PagedTablesArgs& a, Sums& t, uint32_t& n_free,
+                                      Part& own) {
+  __shared__ uint64_t s_sum[3][kT / 32];
   __shared__ uint32_t s_bad;
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
   Sums m{0, 0, 0};
   bool ok = true;
-  for (uint32_t s = threadIdx.x; s < a.n_seqs; s += kThreads) {
+  for (uint32_t s = threadIdx.x; s < a.n_seqs; s += kT) {
     const Part p = part_of(a, s);
+    if (s == threadIdx.x) own = p;
     ok = ok && p.ok;
     m.gone += p.gone, m.come += p.come, m.rows += p.rows;
   }
@@ -75,7 +80,7 @@ __device__ __forceinline__ bool total(const PagedTablesArgs& a, Sums& t, uint32_
   const int32_t n = a.state[0];
   __syncthreads();
   t = Sums{0, 0, 0};
-  for (uint32_t w = 0; w < kWarps; ++w)
+  for (uint32_t w = 0; w < kT / 32; ++w)
     t.gone += s_sum[0][w], t.come += s_sum[1][w], t.rows += s_sum[2][w];
   n_free = (uint32_t)n;
   return !s_bad && n >= 0 && n_free + t.gone <= a.n_pages && t.come <= n_free + t.gone &&
@@ -83,7 +88,8 @@ __device__ __forceinline__ bool total(const PagedTablesArgs& a, Sums& t, uint32_
 }
 
 // Sums of x before this thread, and over all threads.
-__device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t (&s_warp)[kWarps], uint32_t& all) {
+template <uint32_t kT>
+__device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t (&s_warp)[kT / 32], uint32_t& all) {
   const uint32_t lane = threadIdx.x & 31u, warp = threadIdx.x >> 5;
   uint32_t inc = x;
 #pragma unroll
@@ -96,28 +102,32 @@ __device__ __forceinline__ uint32_t scan(uint32_t x, uint32_t (&s_warp)[kWarps],
   __syncthreads();
   uint32_t before = 0;
   all = 0;
-  for (uint32_t w = 0; w < kWarps; ++w) {
+  for (uint32_t w = 0; w < kT / 32; ++w) {
     if (w < warp) before += s_warp[w];
     all += s_warp[w];
   }
   return before + inc - x;
 }
 
-// The last of kThreads sums, which do not decrease, that is at most x.
-__device__ __forceinline__ uint32_t last_at_most(const uint32_t (&sums)[kThreads], uint32_t x) {
+// The last of kT sums, which do not decrease, that is at most x.
+template <uint32_t kT>
+__device__ __forceinline__ uint32_t last_at_most(const uint32_t (&sums)[kT], uint32_t x) {
   uint32_t at = 0;
 #pragma unroll
-  for (uint32_t d = kThreads / 2; d; d >>= 1)
+  for (uint32_t d = kT / 2; d; d >>= 1)
     if (sums[at + d] <= x) at += d;
   return at;
 }
 
 // The last CTA to come here sets what the others have read.
+template <uint32_t kT>
 __device__ __forceinline__ void finish(const PagedTablesArgs& a, bool ok, const Sums& t,
                                        uint32_t n_free) {
   __shared__ uint32_t s_last;
   __syncthreads();  // (every thread's reads and writes are before its CTA's ticket)
-  if (threadIdx.x == 0) {
+  if (gridDim.x == 1u) {
+    s_last = 1u;
+  } else if (threadIdx.x == 0) {
     __threadfence();
     s_last = atomicAdd(reinterpret_cast<uint32_t*>(a.state) + 1, 1u) == gridDim.x - 1u;
     __threadfence();
@@ -125,7 +135,7 @@ __device__ __forceinline__ void finish(const PagedTablesArgs& a, bool ok, const 
   __syncthreads();
   if (!s_last) return;
   if (ok)
-    for (uint32_t s = threadIdx.x; s < a.n_seqs; s += kThreads) a.kv_lens[s] = __ldg(a.target + s);
+    for (uint32_t s = threadIdx.x; s < a.n_seqs; s += kT) a.kv_lens[s] = __ldg(a.target + s);
   if (threadIdx.x == 0) {
     if (ok)
       a.state[0] = (int32_t)(n_free + (uint32_t)t.gone - (uint32_t)t.come);
@@ -135,45 +145,41 @@ __device__ __forceinline__ void finish(const PagedTablesArgs& a, bool ok, const 
   }
 }
 
-// Pages that go, onto the list; all there is to do when no sequence may grow.
-__global__ void __launch_bounds__(kThreads) k_paged_give(PagedTablesArgs a) {
-  __shared__ uint32_t s_warp[kWarps], s_sum[kThreads], s_want[kThreads];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Sums t;
-  uint32_t n_free;
-  const bool ok = total(a, t, n_free);
-  if (ok && t.gone) {
-    const uint32_t R = (uint32_t)t.gone;
-    const uint32_t r0 = (uint32_t)((uint64_t)R * blockIdx.x / gridDim.x);
-    const uint32_t r1 = (uint32_t)((uint64_t)R * (blockIdx.x + 1u) / gridDim.x);
-    uint32_t base = 0;
-    for (uint32_t c = 0; c < a.n_seqs && base < r1; c += kThreads) {
-      Part p{};
-      if (c + threadIdx.x < a.n_seqs) p = part_of(a, c + threadIdx.x);
-      uint32_t all;
-      const uint32_t before = scan(p.gone, s_warp, all);
-      s_sum[threadIdx.x] = base + before;
-      s_want[threadIdx.x] = p.want;
-      __syncthreads();
-      for (uint32_t r = max(r0, base) + threadIdx.x; r < min(r1, base + all); r += kThreads) {
-        const uint32_t i = last_at_most(s_sum, r);
-        a.free_pages[n_free + R - 1u - r] =
-            a.table[(uint64_t)(c + i) * a.table_stride + s_want[i] + (r - s_sum[i])];
-      }
-      base += all;
-      __syncthreads();
+// Pages that go, onto the list.
+template <uint32_t kT>
+__device__ __forceinline__ void give(const PagedTablesArgs& a, const Sums& t, uint32_t n_free,
+                                     const Part& own) {
+  __shared__ uint32_t s_warp[kT / 32], s_sum[kT], s_want[kT];
+  const uint32_t R = (uint32_t)t.gone;
+  const uint32_t r0 = (uint32_t)((uint64_t)R * blockIdx.x / gridDim.x);
+  const uint32_t r1 = (uint32_t)((uint64_t)R * (blockIdx.x + 1u) / gridDim.x);
+  uint32_t base = 0;
+  for (uint32_t c = 0; c < a.n_seqs && base < r1; c += kT) {
+    Part p = own;
+    if (c) p = c + threadIdx.x < a.n_seqs ? part_of(a, c + threadIdx.x) : Part{};
+    uint32_t all;
+    const uint32_t before = scan<kT>(p.gone, s_warp, all);
+    s_sum[threadIdx.x] = base + before;
+    s_want[threadIdx.x] = p.want;
+    __syncthreads();
+    const uint32_t from = max(r0, base) + threadIdx.x;
+    uint32_t i = last_at_most<kT>(s_sum, from);
+#pragma unroll 4
+    for (uint32_t r = from; r < min(r1, base + all); r += kT) {
+      while (i + 1u < kT && s_sum[i + 1u] <= r) ++i;
+      a.free_pages[n_free + R - 1u - r] =
+          a.table[(uint64_t)(c + i) * a.table_stride + s_want[i] + (r - s_sum[i])];
     }
+    base += all;
+    __syncthreads();
   }
-  if (!a.n_tokens) finish(a, ok, t, n_free);
 }
 
-// Rows, pages and slots of the new tokens, behind k_paged_give.
-__global__ void __launch_bounds__(kThreads) k_paged_take(PagedTablesArgs a) {
-  __shared__ uint32_t s_warp[kWarps], s_row[kThreads], s_page[kThreads], s_old[kThreads];
-  Sums t;
-  uint32_t n_free;
-  const bool ok = total(a, t, n_free);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// Rows, pages and slots of the new tokens, from the list with the pages that went.
+template <uint32_t kT>
+__device__ __forceinline__ void take(const PagedTablesArgs& a, bool ok, const Sums& t,
+                                     uint32_t n_free, const Part& own) {
+  __shared__ uint32_t s_warp[kT / 32], s_row[kT], s_page[kT], s_old[kT];
   const uint32_t T = ok ? (uint32_t)t.rows : 0u;
   const uint32_t t0 = (uint32_t)((uint64_t)T * blockIdx.x / gridDim.x);
   const uint32_t t1 = (uint32_t)((uint64_t)T * (blockIdx.x + 1u) / gridDim.x);
@@ -181,13 +187,14 @@ __global__ void __launch_bounds__(kThreads) k_paged_take(PagedTablesArgs a) {
   const uint32_t lg = a.page_lg, P = 1u << lg;
   uint32_t row = 0, page = 0;  // sums before the sequences from c on
   const bool starts = blockIdx.x == 0;
-  for (uint32_t c = 0; c < a.n_seqs && (starts || row < t1); c += kThreads) {
+  for (uint32_t c = 0; c < a.n_seqs && (starts || row < t1); c += kT) {
     const uint32_t s = c + threadIdx.x;
-    Part p{};
-    if (ok && s < a.n_seqs) p = part_of(a, s);
+    Part p = own;
+    if (c) p = s < a.n_seqs ? part_of(a, s) : Part{};
+    if (!ok) p = Part{};
     uint32_t rows, pages;
-    const uint32_t before = scan(p.rows, s_warp, rows);
-    const uint32_t first = scan(p.come, s_warp, pages);
+    const uint32_t before = scan<kT>(p.rows, s_warp, rows);
+    const uint32_t first = scan<kT>(p.come, s_warp, pages);
     s_row[threadIdx.x] = row + before;
     s_page[threadIdx.x] = page + first - p.have;  // number of its page i that is new: this + i
     s_old[threadIdx.x] = p.old;
@@ -196,34 +203,72 @@ __global__ void __launch_bounds__(kThreads) k_paged_take(PagedTablesArgs a) {
       if (s + 1u == a.n_seqs) a.q_starts[s + 1u] = (int32_t)(row + before + p.rows);
     }
     __syncthreads();
-    for (uint32_t x = max(t0, row) + threadIdx.x; x < min(t1, row + rows); x += kThreads) {
-      const uint32_t i = last_at_most(s_row, x);
+    const uint32_t from = max(t0, row) + threadIdx.x;
+    uint32_t i = last_at_most<kT>(s_row, from);
+#pragma unroll 4
+    for (uint32_t x = from; x < min(t1, row + rows); x += kT) {
+      while (i + 1u < kT && s_row[i + 1u] <= x) ++i;
       const uint32_t old = s_old[i], pos = old + (x - s_row[i]), at = pos >> lg;
       int32_t* entry = a.table + (uint64_t)(c + i) * a.table_stride + at;
-      int32_t id;
-      if (at >= (old + P - 1u) >> lg) {  // a new page; its first token writes its entry
-        id = a.free_pages[top - (s_page[i] + at)];
-        if ((pos & (P - 1u)) == 0u) *entry = id;
-      } else {
-        id = *entry;
-      }
+      const bool fresh = at >= (old + P - 1u) >> lg;  // its first token writes its entry
+      const int32_t id = fresh ? a.free_pages[top - (s_page[i] + at)] : *entry;
+      if (fresh && (pos & (P - 1u)) == 0u) *entry = id;
       if (a.slots) a.slots[x] = ((int64_t)id << lg) + (pos & (P - 1u));
     }
     row += rows;
     page += pages;
     __syncthreads();
   }
-  finish(a, ok, t, n_free);
+}
+
+// All there is to do when no sequence may grow; else the rest is k_paged_take's.
+__global__ void __launch_bounds__(kThreads) k_paged_give(PagedTablesArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Sums t;
+  Part own{};
+  uint32_t n_free;
+  const bool ok = total<kThreads>(a, t, n_free, own);
+  if (ok && t.gone) give<kThreads>(a, t, n_free, own);
+  if (!a.n_tokens) finish<kThreads>(a, ok, t, n_free);
+}
+
+__global__ void __launch_bounds__(kThreads) k_paged_take(PagedTablesArgs a) {
+  Sums t;
+  Part own{};
+  uint32_t n_free;
+  const bool ok = total<kThreads>(a, t, n_free, own);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  take<kThreads>(a, ok, t, n_free, own);
+  finish<kThreads>(a, ok, t, n_free);
+}
+
+// One CTA: the list is written before it is read.
+__global__ void __launch_bounds__(kThreads) k_paged_resize(PagedTablesArgs a) {
+  Sums t;
+  Part own{};
+  uint32_t n_free;
+  const bool ok = total<kThreads>(a, t, n_free, own);
+  if (ok && t.gone) give<kThreads>(a, t, n_free, own);
+  __syncthreads();
+  if (a.n_tokens) take<kThreads>(a, ok, t, n_free, own);
+  finish<kThreads>(a, ok, t, n_free);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_resize(const PagedTablesArgs& a, int sm_count, cudaStream_t st) {
+  const uint64_t entries = (uint64_t)a.n_seqs * a.max_pages;
+  if (entries <= 16u * kThreads && a.n_tokens <= 4u * kThreads) {
+    k_paged_resize<<<1, kThreads, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  // Two loads to a thread, four CTAs to an SM at most: a look-up waits for the last, and each CTA
+  // takes the sums again.
   auto ctas = [&](uint64_t n) {
-    const uint64_t c = (n + 4u * kThreads - 1) / (4u * kThreads);
-    return (unsigned)(c < 1u ? 1u : c > (uint64_t)sm_count ? (uint64_t)sm_count : c);
+    const uint64_t c = (n + 2u * kThreads - 1) / (2u * kThreads), most = 4ull * sm_count;
+    return (unsigned)(c < 1u ? 1u : c > most ? most : c);
   };
-  k_paged_give<<<ctas((uint64_t)a.n_seqs * a.max_pages), kThreads, 0, st>>>(a);
+  k_paged_give<<<ctas(entries), kThreads, 0, st>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !a.n_tokens) return e;
   cudaLaunchConfig_t cfg = {};

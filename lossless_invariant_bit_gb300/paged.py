@@ -395,9 +395,12 @@ class PageTables:
         self.free_pages = torch.arange(cache.n_pages, dtype=torch.int32, device=dev).flip(0)
         self._state = torch.tensor([cache.n_pages, 0], dtype=torch.int32, device=dev)
         self.n_free = self._state[:1]
+        self.q_starts = torch.zeros(n_seqs + 1, dtype=torch.int32, device=dev)
+        self._batches = {}  # of calls with as many tokens: the tensors are always these
         self._desc = ibp.ibp_paged_tables(
             self.page_table.data_ptr(), self.kv_lens.data_ptr(), self.free_pages.data_ptr(),
             self._state.data_ptr(), max_pages, n_seqs, max_pages)
+        self._address = ctypes.addressof(self._desc)
 
     def resize(self, target: torch.Tensor, n_tokens: int = 0,
                max_q_tokens: Optional[int] = None, slots: Optional[torch.Tensor] = None,
@@ -405,9 +408,9 @@ class PageTables:
         """Sequence s gets target[s] tokens (int32 [n_seqs] on the device): pages come from the
         free ones or go back to them.  n_tokens: rows of the new tokens' arrays, at least
         what sequences grow by together; of one at most max_q_tokens (n_tokens).  Returns the
-        batch of the new tokens, whose lengths and table are these, and their slots (int64
-        [n_tokens]: page * page_tokens + place, rows of key_rows() and value_rows()); nothing
-        when n_tokens is 0: such a call only shrinks.
+        batch of the new tokens, whose tensors are these tables' (another call changes them), and
+        their slots (int64 [n_tokens]: page * page_tokens + place, rows of key_rows() and
+        value_rows()); nothing when n_tokens is 0: such a call only shrinks.
 
         Where that cannot be done as a whole nothing changes, the batch is empty, and
         the cache's status says IBP_ERANGE."""
@@ -418,24 +421,27 @@ class PageTables:
         if (target.shape != self.kv_lens.shape or target.dtype != torch.int32
                 or target.get_device() != index or not target.is_contiguous()):
             raise ValueError("target must be a contiguous int32 [n_seqs] on the cache's device")
-        if n_tokens < 0:
-            raise ValueError("n_tokens is not negative")
-        q_starts = None
-        if n_tokens:
-            if slots is None:
-                slots = torch.empty(n_tokens, dtype=torch.int64, device=cache.device)
-            elif (slots.shape != (n_tokens,) or slots.dtype != torch.int64
-                  or slots.get_device() != index or not slots.is_contiguous()):
-                raise ValueError("slots must be a contiguous int64 [n_tokens] on the cache's "
-                                 "device")
-            q_starts = torch.empty(self.n_seqs + 1, dtype=torch.int32, device=cache.device)
-        elif slots is not None:
-            raise ValueError("a call without new tokens has no slots")
-        ibp._check(cache._lib.ibp_paged_resize(
-            cache.handle, ctypes.addressof(self._desc), target.data_ptr(),
-            q_starts.data_ptr() if n_tokens else None, slots.data_ptr() if n_tokens else None,
-            n_tokens, _raw_stream(index)), "ibp_paged_resize")
-        if not n_tokens:
+        if n_tokens <= 0:
+            if n_tokens or slots is not None:
+                raise ValueError("n_tokens is not negative, and a call without new tokens has no "
+                                 "slots")
+            ibp._check(cache._lib.ibp_paged_resize(
+                cache.handle, self._address, target.data_ptr(), None, None, 0,
+                _raw_stream(index)), "ibp_paged_resize")
             return None
-        return (PagedBatch(self.page_table, self.kv_lens, q_starts, n_tokens,
-                           n_tokens if max_q_tokens is None else max_q_tokens), slots)
+        if slots is None:
+            slots = torch.empty(n_tokens, dtype=torch.int64, device=cache.device)
+        elif (slots.shape != (n_tokens,) or slots.dtype != torch.int64
+              or slots.get_device() != index or not slots.is_contiguous()):
+            raise ValueError("slots must be a contiguous int64 [n_tokens] on the cache's device")
+        ibp._check(cache._lib.ibp_paged_resize(
+            cache.handle, self._address, target.data_ptr(), self.q_starts.data_ptr(),
+            slots.data_ptr(), n_tokens, _raw_stream(index)), "ibp_paged_resize")
+        most = n_tokens if max_q_tokens is None else max_q_tokens
+        batch = self._batches.get((n_tokens, most))
+        if batch is None:
+            if len(self._batches) >= 64:  # (prompts of ever other lengths)
+                self._batches.clear()
+            batch = self._batches[n_tokens, most] = PagedBatch(
+                self.page_table, self.kv_lens, self.q_starts, n_tokens, most)
+        return batch, slots

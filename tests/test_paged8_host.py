@@ -116,7 +116,8 @@ class Tables:
         t = object.__new__(paged.PageTables)
         t.cache, t.n_seqs, t.max_pages = cache, 2, 4
         t.page_table, t.kv_lens = Said((2, 4), I32), Said((2,), I32)
-        t._desc = ibp.ibp_paged_tables()
+        t.q_starts = Said((3,), I32)
+        t._address, t._batches = 0, {}
         return t
 
 
