@@ -78,6 +78,7 @@ __device__ __forceinline__ void append_units(const PagedAppendArgs& a, uint32_t 
     t1 = a.n_pos > p0 ? a.n_pos - p0 : 0u;
   }
   if (t1 <= t0) return;
+  const uint64_t next_row = rows * a.kv_stride, next_slot = rows * a.g.token_stride;
   // the CTA's units, a round of 128 / unit of them at a time: keys' heads, then values'
   for (uint32_t round = 0; round < per; ++round) {
     const uint32_t u = (blockIdx.y * per + round) * (128u >> unit_lg) + (tid >> unit_lg);
@@ -90,10 +91,11 @@ __device__ __forceinline__ void append_units(const PagedAppendArgs& a, uint32_t 
     const bool turned = keys && lane * 8u < a.rot, split = !kPairs && lane * 8u < a.rot;
     const uint32_t c0 = split ? lane * 4u : lane * 8u, c1 = split ? half + lane * 4u : c0 + 4u;
     // row of slot t in the call's arrays: q0 + (p0 + t) - (L - n)
-    const uint8_t* src = (keys ? a.kx : a.vx) + (uint64_t)h * a.g.D * 2u;
+    const uint8_t* src = (keys ? a.kx : a.vx) + (uint64_t)h * a.g.D * 2u + c0 * 2u;
+    const uint32_t apart = c1 - c0;
     const int64_t row0 = (int64_t)q.q0 + p0 - ((int64_t)q.L - q.n);
     uint8_t* dst = (keys ? a.g.k : a.g.v) + (uint64_t)(uint32_t)page * a.g.page_stride +
-                   h * a.g.head_stride;
+                   h * a.g.head_stride + c0;
     uint64_t w[4] = {};  // the norm's weights
     if (a.k_norm && mine) {
       const uint2 x = __ldg(reinterpret_cast<const uint2*>(a.k_norm + c0 * 2u));
@@ -110,18 +112,19 @@ __device__ __forceinline__ void append_units(const PagedAppendArgs& a, uint32_t 
     // the values of the unit's tokens from slot `at` on
     auto compute = [&](uint32_t at) {
       uint2 x[kTokens][2];
+      const uint8_t* p = src + (uint64_t)(row0 + at + row) * a.kv_stride;
 #pragma unroll
-      for (int i = 0; i < kTokens; ++i) {
+      for (int i = 0; i < kTokens; ++i, p += next_row) {
         const uint32_t t = at + i * rows + row;
         x[i][0] = x[i][1] = make_uint2(0u, 0u);
         if (mine && t >= t0 && t < t1) {
-          const uint8_t* p = src + (uint64_t)(row0 + t) * a.kv_stride;
-          x[i][0] = __ldg(reinterpret_cast<const uint2*>(p + c0 * 2u));
-          x[i][1] = __ldg(reinterpret_cast<const uint2*>(p + c1 * 2u));
+          x[i][0] = __ldg(reinterpret_cast<const uint2*>(p));
+          x[i][1] = __ldg(reinterpret_cast<const uint2*>(p + 2u * apart));
         }
       }
+      const float* cs = a.cos_sin + (uint64_t)(p0 + at + row) * a.rot + lane * 4u;
 #pragma unroll
-      for (int i = 0; i < kTokens; ++i) {
+      for (int i = 0; i < kTokens; ++i, cs += rows * a.rot) {
         const uint32_t t = at + i * rows + row;
         const uint32_t z[4] = {x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y};
 #pragma unroll
@@ -144,7 +147,6 @@ __device__ __forceinline__ void append_units(const PagedAppendArgs& a, uint32_t 
             for (int k = 0; k < 4; ++k) f[i][k] = mul2(f[i][k], mul2(pair2(n, n), w[k]));
         }
         if (a.cos_sin && turned && t >= t0 && t < t1) {
-          const float* cs = a.cos_sin + (uint64_t)(p0 + t) * a.rot + lane * 4u;
           const float4 cc = __ldg(reinterpret_cast<const float4*>(cs));
           const float4 ss = __ldg(reinterpret_cast<const float4*>(cs + half));
           if (kPairs) {
@@ -215,8 +217,8 @@ __device__ __forceinline__ void append_units(const PagedAppendArgs& a, uint32_t 
         const float down = scale_of(127u + was - byte);
         for (uint32_t t = row; t < t0; t += rows)
           if (mine) {
-            uint32_t* p0 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c0);
-            uint32_t* p1 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c1);
+            uint32_t* p0 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride);
+            uint32_t* p1 = reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + apart);
             *p0 = rescale4(*p0, down);
             *p1 = rescale4(*p1, down);
           }
@@ -227,16 +229,17 @@ __device__ __forceinline__ void append_units(const PagedAppendArgs& a, uint32_t 
     const uint64_t inv = pair2(down, down);
     // backwards, beginning with what is still in registers
     for (;; at -= step) {
+      uint8_t* d = dst + (at + row) * a.g.token_stride;
 #pragma unroll
-      for (int i = 0; i < kTokens; ++i) {
+      for (int i = 0; i < kTokens; ++i, d += next_slot) {
         const uint32_t t = at + i * rows + row;
         if (!mine || t < t0 || t >= t1) continue;
         uint32_t z[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k)
           z[k] = codes2(f[i][2 * k], inv) | codes2(f[i][2 * k + 1], inv) << 16;
-        *reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c0) = z[0];
-        *reinterpret_cast<uint32_t*>(dst + t * a.g.token_stride + c1) = z[1];
+        *reinterpret_cast<uint32_t*>(d) = z[0];
+        *reinterpret_cast<uint32_t*>(d + apart) = z[1];
       }
       if (at == begin) break;
       compute(at - step);
