@@ -1,8 +1,10 @@
 """A decode loop over a paged K/V cache: prompts in chunks, then tokens one by one,
 over every cached token or over the pages that score best; a sequence that pauses
-leaves its pages for a compressed host store and comes back.
+leaves its pages for a compressed host store and comes back.  The page tables are
+kept on the GPU: pages come and go as lengths change.
 
     python examples/paged_decode.py            # prints tokens per second of each form
+    python examples/paged_decode.py --bits 8   # the pages held as e4m3 codes
 
 The model here is one attention layer with random projections: what matters is
 the order of the calls.
@@ -57,7 +59,7 @@ class Layer:
 
 
 def run(seqs=4, prompt=2000, chunk=512, steps=32, hidden=1024, q_heads=32, kv_heads=8, dim=128,
-        page=16, pick=48, dtype=torch.bfloat16, seed=0):
+        page=16, pick=48, dtype=torch.bfloat16, seed=0, bits=16):
     """Returns (outputs of the steps over every token, over the selected pages, the
     store's ratio of compressed to raw bytes, whether the paused sequence came back bit for
     bit, tokens per second of both forms)."""
@@ -66,56 +68,61 @@ def run(seqs=4, prompt=2000, chunk=512, steps=32, hidden=1024, q_heads=32, kv_he
     total = prompt + 2 * steps
     per = -(-total // page)
     layer = Layer(hidden, q_heads, kv_heads, dim, total, dtype, seed)
-    cache = PagedCache(kv_heads, dim, page, (seqs + 1) * per, dtype)
-    perm = torch.randperm((seqs + 1) * per, generator=g, device="cuda").to(torch.int32)
-    table, spare = perm[:seqs * per].view(seqs, per).clone(), perm[seqs * per:]
+    cache = PagedCache(kv_heads, dim, page, (seqs + 1) * per, dtype,
+                       page_dtype=torch.float8_e4m3fn if bits == 8 else None)
+    tables = cache.tables(seqs, per)
+    tables.free_pages.copy_(torch.randperm(cache.n_pages, generator=g, device="cuda"))
+    target = torch.zeros(seqs, dtype=torch.int32, device="cuda")  # the lengths to come
     bounds = torch.zeros((cache.n_pages, kv_heads, 2, dim), dtype=dtype, device="cuda")
-
-    def batch_of(lens, new):
-        starts = torch.arange(seqs + 1, dtype=torch.int32, device="cuda") * new
-        return cache.batch(table, torch.full((seqs,), lens, dtype=torch.int32, device="cuda"),
-                           starts, seqs * new, new)
 
     x = torch.randn((seqs, total, hidden), generator=g, device="cuda").to(dtype)
     for at in range(0, prompt, chunk):  # prompts, a chunk of every sequence at a time
         n = min(chunk, prompt - at)
-        layer.step(cache, batch_of(at + n, n), x[:, at:at + n].reshape(-1, hidden), bounds)
+        batch, _ = tables.resize(target.add_(n), seqs * n, n)
+        layer.step(cache, batch, x[:, at:at + n].reshape(-1, hidden), bounds)
 
     def decode(first, pick):
-        batch = batch_of(first, 1)  # its lengths grow in place
         outs = []
         torch.cuda.synchronize()
         t = time.perf_counter()
         for i in range(steps):
-            batch.kv_lens.add_(1)
+            batch, _ = tables.resize(target.add_(1), seqs, 1)
             outs.append(layer.step(cache, batch, x[:, first + i], bounds, pick))
         torch.cuda.synchronize()
         return torch.stack(outs), seqs * steps / (time.perf_counter() - t)
 
     full, full_rate = decode(prompt, 0)
 
-    # sequence 0 pauses: a token's keys (values) are one row of the store
-    rows = kv_heads * dim * 2
+    # sequence 0 pauses: a token's keys (values) are one row of the store; its pages go back,
+    # and others come when it goes on
+    rows = kv_heads * dim * cache.k.element_size()
     held = prompt + steps
     at = torch.arange(held, device="cuda")
-    old = table[0, at // page].long() * page + at % page
-    table[0] = spare
-    new = table[0, at // page].long() * page + at % page
-    stored, same = 0, True
+    old = tables.page_table[0, at // page].long() * page + at % page
+    first = torch.arange(0, held, page, device="cuda")  # a token of each of its pages
+    beside = [t for t in (bounds, cache.k_scales, cache.v_scales) if t is not None]
+    beside = [t.view(torch.uint8).view(cache.n_pages, -1) for t in beside]
+    kept = [t[old[first] // page].clone() for t in beside]  # what else a page has
+    stored, same, stores = 0, True, []
     for data in (cache.key_rows(), cache.value_rows()):
         seq = data[old].contiguous()
-        store = IbpStore(rows, dim * 2, held)  # a chunk is one head
-        try:
-            store.build(seq)
-            slots, sizes = store.compress(seq)  # pinned host memory
-            stored += int(sizes.sum())
-            data[old] = 0
-            data[new] = store.gather(slots, at)  # and back, into other pages
-            same = same and torch.equal(data[new], seq) and store.status() == 0
-        finally:
-            store.close()
-    moved = torch.arange(-(-held // page), device="cuda")
-    bounds[spare[moved].long()] = bounds[old[moved * page] // page]
+        store = IbpStore(rows, rows // kv_heads, held)  # a chunk is one head
+        stores.append((data, seq, store))
+        store.build(seq)
+        slots, sizes = store.compress(seq)  # pinned host memory
+        stored += int(sizes.sum())
+        data[old] = 0
+        stores[-1] += (slots,)
+    target[0] = 0
+    tables.resize(target)
+    target[0] = held
+    _, new = tables.resize(target, held)
+    for data, seq, store, slots in stores:
+        data[new] = store.gather(slots, at)
+        same = same and torch.equal(data[new], seq) and store.status() == 0
+        store.close()
+    for t, what in zip(beside, kept):
+        t[new[first] // page] = what
 
     few, few_rate = decode(prompt + steps, pick)
     assert cache.status() == 0
@@ -129,9 +136,10 @@ def main():
     ap.add_argument("--prompt", type=int, default=16000)
     ap.add_argument("--steps", type=int, default=64)
     ap.add_argument("--pick", type=int, default=64)
+    ap.add_argument("--bits", type=int, choices=(16, 8), default=16)
     a = ap.parse_args()
-    run(seqs=2, prompt=600, steps=4)  # warm-up
-    _, _, ratio, same, rates = run(a.seqs, a.prompt, steps=a.steps, pick=a.pick)
+    run(seqs=2, prompt=600, steps=4, bits=a.bits)  # warm-up
+    _, _, ratio, same, rates = run(a.seqs, a.prompt, steps=a.steps, pick=a.pick, bits=a.bits)
     print("%d sequences of %d tokens: %.0f tokens/s over every token, %.0f over %d pages of 16; "
           "a paused sequence stored at %.3f of its size, back bit for bit: %s"
           % (a.seqs, a.prompt, rates[0], rates[1], a.pick, ratio, same))

@@ -210,6 +210,24 @@ def test_chunk(q_lens, kv_lens, G, D, P, layout, dtype):
     s.check(*attend(s))
 
 
+def test_many_short_tiles():
+    """More tiles to a CTA than any of its rings is long, both kernels' at once."""
+    q_lens = [17 + i % 30 if i % 3 else 1 + i % 4 for i in range(400)]
+    kv_lens = [n + i * 7 % 50 for i, n in enumerate(q_lens)]
+    for D in (64, 128):
+        s = Setup(q_lens, kv_lens, 2, 6, D, 8, torch.bfloat16)
+        out, lse = attend(s)
+        s.check(out, lse)
+
+
+def test_many_rows_of_one_token():
+    """Few keys for each of many sequences: a tile of one block after the other."""
+    for G, H, D in ((1, 8, 64), (8, 4, 128), (12, 4, 64)):
+        s = Setup([1] * 300, [1 + i * 11 % 90 for i in range(300)], G, H, D, 16, torch.float16)
+        out, lse = attend(s)
+        s.check(out, lse)
+
+
 @pytest.mark.parametrize("window", [1, 5, 128, 300])
 @pytest.mark.parametrize("q_lens,kv_lens,G", [([1, 3], [700, 100], 2), ([90, 400], [700, 800], 4)])
 def test_window(q_lens, kv_lens, G, window):
@@ -702,3 +720,50 @@ def test_the_same_call_gives_the_same_bits():
     for _ in range(3):
         b, lb = s.cache.attention(s.batch, s.q, lse=True)
         assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_the_example():
+    """The decode loop of examples/paged_decode.py over pages held in 8 bits."""
+    import importlib.util
+    import os
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location(
+        "paged_decode", os.path.join(root, "examples", "paged_decode.py"))
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    kw = dict(seqs=3, prompt=300, chunk=128, steps=5, hidden=256, q_heads=8, kv_heads=2, dim=64,
+              bits=8)
+    full, few, ratio, same, _ = m.run(pick=1000, **kw)
+    assert same and 0 < ratio <= 1.0
+    for x in (full, few):
+        assert x.shape == (5, 3, 256) and bool(torch.isfinite(x.float()).all())
+    b = m.run(pick=0, **kw)
+    assert torch.equal(full, b[0])
+    # every page selected: the same sums in another order, two roundings to bf16 on either
+    # side of a projection
+    d = (few.double() - b[1].double()).norm() / b[1].double().norm()
+    assert d < 2.0 ** -7
+
+
+def test_threads_on_one_stream():
+    """Calls of two threads on one stream, each with its own cache and tables."""
+    import threading
+
+    def work(seed, out):
+        s = Setup([1, 1], [300, 70], 4, 2, 64, 16, torch.float16, seed=seed)
+        out.extend(s.cache.attention(s.batch, s.q) for _ in range(20))
+        torch.cuda.synchronize()
+        assert s.cache.status() == 0
+        out.append(s)
+
+    outs = [[], []]
+    ts = [threading.Thread(target=work, args=(i, o)) for i, o in enumerate(outs)]
+    for x in ts:
+        x.start()
+    for x in ts:
+        x.join()
+    for o in outs:
+        s = o.pop()
+        assert len(o) == 20 and all(torch.equal(x, o[0]) for x in o)
+        s.check(o[0], None)
