@@ -521,7 +521,8 @@ IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc)
  *              (a power of two: exact but for codes that become subnormal).  What the
  *              largest scale does not hold becomes the largest code; infinities and NaN
  *              become NaN codes.  A page that new tokens go into belongs to one sequence
- *   attention  as over code * scale, in fp32 with weights and codes multiplied in fp16; the
+ *   attention  as over code * scale, in fp32 with weights and codes multiplied in fp16 (in
+ *        bf16 where ibp_paged_workspace asks for more: then as over 16-bit pages); the
  *              scales are exact
  *   bounds     of code * scale, rounded to the 16-bit type
  * A scale outside its range is an error like a page id out of range, where it is needed. */
@@ -575,8 +576,8 @@ IBP_API ibp_status ibp_paged_append(const ibp_paged* cache, const ibp_paged_batc
  *        K/V head h sees only the keys of the pages selected[i][h][...] (numbers
  *        of the sequence's pages, no page twice; negative entries and those
  *        beyond the row's position are passed over).  Causal, without window.
- *   workspace  device, IBP_PAGED_WORKSPACE_BYTES, 16-byte aligned: the call's until its
- *        work is done.  Calls on one stream may share one, from several threads too
+ *   workspace  device, at least IBP_PAGED_WORKSPACE_BYTES (ibp_paged_workspace: what is made use
+ *        of), 16-byte aligned: the call's until its work is done.  Calls on one stream may share one, from several threads too
  *        (they are enqueued one after the other); calls on different streams may not
  * Scores, softmax and sums in fp32, the weights rounded to the 16-bit type
  * before they multiply the values (weights down to 2^-25 of a row's largest with the
@@ -588,6 +589,14 @@ IBP_API ibp_status ibp_paged_attention(const ibp_paged* cache, const ibp_paged_b
                                        uint32_t window, const int32_t* selected,
                                        uint32_t n_selected, void* workspace,
                                        uint64_t workspace_bytes, ibp_stream_t stream);
+
+/* The bytes of workspace that ibp_paged_attention makes use of for such a batch (without lists):
+ * IBP_PAGED_WORKSPACE_BYTES, and for a handle on pages held in 8 bits, of type bf16, whose
+ * chunks of new tokens are long, room for its pages as 16-bit ones, which are then made once
+ * (n_seqs * max_pages pages: a table with columns that no sequence needs costs room).  With less
+ * the result is computed from the codes, in more time.  Errors: IBP_EINVAL. */
+IBP_API ibp_status ibp_paged_workspace(const ibp_paged* cache, const ibp_paged_batch* batch,
+                                       uint32_t q_heads, uint64_t* bytes);
 
 /* Bounds of the pages that the batch's new tokens went into, over all tokens
  * they hold now: bounds [n_pages, kv_heads, 2, head_dim], contiguous, of the

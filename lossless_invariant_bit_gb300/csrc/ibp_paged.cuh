@@ -23,6 +23,7 @@ struct PagedBatchView {
   const int32_t *table, *kv_lens, *q_starts;
   uint64_t table_stride;
   uint32_t n_seqs, max_pages, n_tokens, max_q;
+  uint64_t table_heads;  // entries between heads' tables; 0: all heads have one
 };
 
 // Tensor maps of the key and value pages: {D, page tokens, heads, pages} with
@@ -108,6 +109,8 @@ struct PagedLaunches {
   decltype(&launch_paged_step) step;
   decltype(&launch_paged_chunk) chunk;
   decltype(&launch_paged_chunk_join) chunk_join;
+  // NULL, or makes 16-bit pages of what a call's chunk kernel reads, and their table.
+  cudaError_t (*stage)(const PagedAttnArgs& a, const PagedAttnArgs& staged, cudaStream_t st);
 };
 
 #ifdef __CUDACC__

@@ -354,6 +354,55 @@ __global__ void __launch_bounds__(128)
   }
 }
 
+// ---------------------------------------------------------------- 16-bit pages
+// One CTA for each (sequence, page, keys or values): codes times scales as bf16 (exact), one
+// head after the other, for the pages that the chunk kernel reads.  Every tile of 256 rows
+// converts its keys again in the kernel on codes, at 4400 cycles a block of 128 keys; of
+// converted pages a block takes 2800, and the conversion of 8192 tokens x 8 heads of 128 here
+// 12 us in all.  A head's table has no page where one cannot be read.
+__global__ void __launch_bounds__(256) k_paged8_stage(PagedAttnArgs a, PagedAttnArgs to) {
+  const uint32_t s = blockIdx.x / a.b.max_pages, i = blockIdx.x - s * a.b.max_pages;
+  const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
+  if (q.n == 0 || q.n * a.G <= a.max_rows) return;
+  const uint32_t P = 1u << a.g.page_lg, H = a.g.H, D = a.g.D;
+  const int64_t first = (int64_t)q.L - q.n;
+  const int64_t lo = a.window ? first + 1 - (int64_t)a.window : 0;
+  if ((uint64_t)i * P >= q.L || (int64_t)(i + 1u) * P <= lo) return;
+  const bool values = blockIdx.y != 0u;
+  const int32_t page = __ldg(a.b.table + s * a.b.table_stride + i);
+  const bool there = page >= 0 && (uint32_t)page < a.g.n_pages;
+  if (!values)
+    for (uint32_t h = threadIdx.x; h < H; h += blockDim.x)
+      const_cast<int32_t*>(to.b.table)[s * to.b.table_stride + h * to.b.table_heads + i] =
+          there && scales_ok(page_scales(a.g, (uint32_t)page, h)) ? (int32_t)blockIdx.x : -1;
+  if (!there) return;
+  const uint8_t* src = (values ? a.g.v : a.g.k) + (uint64_t)(uint32_t)page * a.g.page_stride;
+  const uint8_t* scales = (values ? a.g.v_scales : a.g.k_scales) + (uint64_t)(uint32_t)page * H;
+  uint8_t* dst = (values ? to.g.v : to.g.k) + (uint64_t)blockIdx.x * to.g.page_stride;
+  const uint32_t chunks = D / 16u, rows = P * chunks;
+  for (uint32_t x = threadIdx.x; x < rows * H; x += blockDim.x) {  // 16 channels
+    const uint32_t h = x / rows, r = x - h * rows, t = r / chunks, c = r - t * chunks;
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + t * a.g.token_stride +
+                                                         h * a.g.head_stride + c * 16u));
+    const float f = scale_of(__ldg(scales + h));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t p[2];
+      codes_to_fp16(w[k], p[0], p[1]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float2 z = unpack2(p[j], 0u);
+        y[2 * k + j] = pack2(z.x * f, z.y * f, 1u);
+      }
+    }
+    uint4* d = reinterpret_cast<uint4*>(dst + (uint64_t)x * 32u);
+    d[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    d[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_paged8_append(const PagedAppendArgs& a, int sm_count, cudaStream_t st) {
@@ -411,6 +460,13 @@ cudaError_t launch_paged8_bounds(const PagedGeom& g, const PagedBatchView& b, ui
     else IBP_CALL(8, false);
   }
 #undef IBP_CALL
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged8_stage(const PagedAttnArgs& a, const PagedAttnArgs& staged,
+                                cudaStream_t st) {
+  const dim3 grid((unsigned)((uint64_t)a.b.n_seqs * a.b.max_pages), 2);
+  k_paged8_stage<<<grid, 256, 0, st>>>(a, staged);
   return cudaGetLastError();
 }
 

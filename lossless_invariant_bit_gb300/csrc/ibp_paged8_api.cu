@@ -7,7 +7,7 @@ namespace {
 
 const ibp::PagedLaunches k8Bit = {&ibp::launch_paged8_append, &ibp::launch_paged8_bounds,
                                   &ibp::launch_paged8_step, &ibp::launch_paged8_chunk,
-                                  &ibp::launch_paged8_chunk_join};
+                                  &ibp::launch_paged8_chunk_join, &ibp::launch_paged8_stage};
 
 inline bool misaligned(const void* p, uintptr_t to) {
   return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) != 0;

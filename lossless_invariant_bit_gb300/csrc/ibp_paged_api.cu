@@ -91,7 +91,7 @@ inline ibp_status cu(cudaError_t e) { return e == cudaSuccess ? IBP_OK : IBP_ECU
 
 const ibp::PagedLaunches k16Bit = {&ibp::launch_paged_append, &ibp::launch_paged_bounds,
                                    &ibp::launch_paged_step, &ibp::launch_paged_chunk,
-                                   &ibp::launch_paged_chunk_join};
+                                   &ibp::launch_paged_chunk_join, nullptr};
 
 // The pages as {head_dim, tokens of a page, heads, pages}, in boxes of 64 channels x `tokens`
 // tokens: rows of 128 bytes, swizzled; channels past head_dim read as zero.  Codes: boxes of
@@ -143,6 +143,35 @@ ibp::PagedBatchView view(const ibp_paged_batch* b) {
 bool heads_ok(const ibp_paged* c, const ibp_paged_batch* b, uint32_t q_heads) {
   return q_heads != 0 && q_heads % c->g.H == 0 && q_heads <= 65536u &&
          (uint64_t)b->n_tokens * q_heads <= 0x7FFFFFFFull;
+}
+
+// Pages in 8 bits that many tiles of a chunk read are converted once, into 16-bit pages in the
+// workspace, instead of by each of them (ibp_paged_create_8bit): a table for each (sequence,
+// head), the keys, the values.
+struct Staging {
+  uint64_t pages, bytes;  // of the keys, of the values
+  uint64_t table, total;  // bytes
+};
+
+// For bf16 alone, which holds every code times every scale, heads of more than 64 channels, and
+// 6 tiles of 256 rows or more for each sequence and head on the average.  With the codes and
+// with 16-bit pages, us (one chunk behind 8192 tokens, 8 heads of 128, 64 queries): 4 tiles 62.6
+// and 58.3, 6 tiles 78.6 and 67.2, 16 tiles 166.5 and 120.5, 64 tiles 553.7 and 346.5; many
+// short chunks beside single tokens (2 tiles) 82 and 93; 16 tiles of heads of 64 111.7 and
+// 114.7.  Where it gains little, the workspace is not worth it.
+constexpr uint64_t kStageTiles = 6;
+
+bool stage_pays(const ibp_paged* c, const ibp_paged_batch* b, uint32_t q_heads, Staging* s) {
+  const uint64_t G = q_heads / c->g.H;
+  if (!c->launches->stage || !c->g.bf16 || c->g.D <= 64u ||
+      (uint64_t)b->max_q_tokens * G <= ibp::kStepRows ||
+      b->n_tokens * G < kStageTiles * 256u * b->n_seqs)
+    return false;
+  s->pages = (uint64_t)b->n_seqs * b->max_pages;
+  s->bytes = (s->pages << c->g.page_lg) * c->g.H * c->g.D * 2u;
+  s->table = (s->pages * c->g.H * 4u + 1023u) & ~1023ull;
+  s->total = s->table + 2u * s->bytes;
+  return s->pages <= 0x7FFFFFFFull && s->bytes <= 1ull << 38;
 }
 
 // A token stride of `heads` heads: long enough, a multiple of 16.
@@ -302,12 +331,51 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
   const bool few = selected || (uint64_t)b->max_q_tokens * a.G <= ibp::kStepRows;
   const bool both = !few && b->n_seqs > 1u;
   a.max_rows = few || both ? ibp::kStepRows : 0u;
+  // 16-bit pages for the chunk kernel, where they pay and the workspace holds them
+  Staging s;
+  ibp::PagedAttnArgs wide = a;
+  ibp::PagedMaps wide_maps;
+  const bool staged = !few && stage_pays(c, b, q_heads, &s) &&
+                      workspace_bytes >= IBP_PAGED_WORKSPACE_BYTES + s.total;
+  if (staged) {
+    uint8_t* at = a.ws + IBP_PAGED_WORKSPACE_BYTES;
+    wide.b.table = reinterpret_cast<const int32_t*>(at);
+    wide.b.table_heads = b->max_pages;
+    wide.b.table_stride = (uint64_t)b->max_pages * c->g.H;
+    wide.g.k = at + s.table;
+    wide.g.v = wide.g.k + s.bytes;
+    wide.g.token_stride = c->g.D * 2u;
+    wide.g.head_stride = wide.g.token_stride << c->g.page_lg;
+    wide.g.page_stride = wide.g.head_stride * c->g.H;
+    wide.g.n_pages = (uint32_t)s.pages;
+    wide.g.k_scales = wide.g.v_scales = nullptr;
+    const ibp_paged_desc d = {wide.g.k,        wide.g.v,       wide.g.page_stride,
+                              wide.g.head_stride, wide.g.token_stride, wide.g.n_pages,
+                              1u << c->g.page_lg, c->g.H,       c->g.D,
+                              c->g.bf16};
+    if (!page_map(&wide_maps.k, d, wide.g.k, ibp::kBoxTokens, false) ||
+        !page_map(&wide_maps.v, d, wide.g.v, ibp::kBoxTokens, false))
+      return IBP_ECUDA;
+  }
   std::lock_guard<std::mutex> lock(call_lock(workspace));
-  cudaError_t ce = few ? cudaSuccess : run.chunk(a, c->maps, c->sm_count, st);
+  cudaError_t ce = staged ? run.stage(a, wide, st) : cudaSuccess;
+  if (ce == cudaSuccess && !few)
+    ce = staged ? ibp::launch_paged_chunk(wide, wide_maps, c->sm_count, st)
+                : run.chunk(a, c->maps, c->sm_count, st);
   if (ce == cudaSuccess && (few || both))
     ce = run.step(a, c->maps, c->sm_count, both, st);
-  if (ce == cudaSuccess && !few) ce = run.chunk_join(a, c->sm_count, st);
+  if (ce == cudaSuccess && !few)
+    ce = staged ? ibp::launch_paged_chunk_join(wide, c->sm_count, st)
+                : run.chunk_join(a, c->sm_count, st);
   return cu(ce);
+}
+
+ibp_status ibp_paged_workspace(const ibp_paged* c, const ibp_paged_batch* b, uint32_t q_heads,
+                               uint64_t* bytes) {
+  if (!c || !b || !bytes || q_heads == 0 || q_heads % c->g.H) return IBP_EINVAL;
+  Staging s;
+  *bytes = IBP_PAGED_WORKSPACE_BYTES + (stage_pays(c, b, q_heads, &s) ? s.total : 0u);
+  return IBP_OK;
 }
 
 ibp_status ibp_paged_bounds(const ibp_paged* c, const ibp_paged_batch* b, void* bounds,

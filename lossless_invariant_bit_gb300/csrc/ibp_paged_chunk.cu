@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++tiles;
       __syncwarp();
       if (!more) break;
-      const int32_t* table = a.b.table + w.t.s * a.b.table_stride;
+      const int32_t* table =
+          a.b.table + w.t.s * a.b.table_stride + w.t.head * a.b.table_heads;
       auto page_at = [&](uint32_t b) {
         const uint32_t key = (w.t.b0 + b) * kKeys + (lane << box_lg);
         if (lane >= npg || key >= w.t.hi || key + (1u << box_lg) <= w.t.lo) return -1;
@@ -354,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t key = (int32_t)(key0 + j);
         if (!(keys[j >> 5] >> (j & 31u) & 1u) || key < from || key >= to) continue;
         const int32_t page =
-            __ldg(a.b.table + t->s * a.b.table_stride + ((uint32_t)key >> a.g.page_lg));
+            __ldg(a.b.table + t->s * a.b.table_stride + t->head * a.b.table_heads +
+                  ((uint32_t)key >> a.g.page_lg));
         const uint16_t* v = reinterpret_cast<const uint16_t*>(
             a.g.v + (uint64_t)(uint32_t)page * a.g.page_stride + t->head * a.g.head_stride +
             ((uint32_t)key & ((1u << a.g.page_lg) - 1u)) * a.g.token_stride);

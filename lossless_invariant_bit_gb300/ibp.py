@@ -107,6 +107,7 @@ _SIGS = {
                          _U32, _U32, _P],
     "ibp_paged_attention": [_P, _P, _P, _U64, _U32, _P, _P, _F32, _U32, _U32, _P, _U32, _P, _U64,
                             _P],
+    "ibp_paged_workspace": [_P, _P, _U32, _P],
     "ibp_paged_bounds": [_P, _P, _P, _P],
     "ibp_paged_scores": [_P, _P, _P, _U64, _U32, _P, _P, _P],
     "ibp_paged_select": [_P, _P, _P, _U32, _P, _P],
@@ -443,6 +444,13 @@ def ibp_paged_attention(cache: int, batch: "ibp_paged_batch", q, q_token_stride:
                                              int(bool(causal)), window, _ptr(selected),
                                              n_selected, _ptr(workspace), workspace_bytes,
                                              _stream(stream)), "ibp_paged_attention")
+
+
+def ibp_paged_workspace(cache: int, batch: "ibp_paged_batch", q_heads: int) -> int:
+    out = ctypes.c_uint64(0)
+    _check(_lib_handle().ibp_paged_workspace(cache, ctypes.addressof(batch), q_heads,
+                                             ctypes.addressof(out)), "ibp_paged_workspace")
+    return out.value
 
 
 def ibp_paged_bounds(cache: int, batch: "ibp_paged_batch", bounds, stream=None) -> None:

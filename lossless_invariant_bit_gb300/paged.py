@@ -61,6 +61,21 @@ def _workspace(device: torch.device, raw: int) -> torch.Tensor:
     return ws
 
 
+# Above this a call does without the larger workspace that chunks over 8-bit pages make use of.
+_MOST_WORKSPACE = 2 << 30
+
+
+def _large_workspace(device: torch.device, raw: int, bytes_: int) -> torch.Tensor:
+    """As _workspace, of at least as many bytes; the stream keeps the largest."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(bytes_, dtype=torch.uint8, device=device)
+    ws = _workspaces.get((device.index, raw))
+    if ws is None or ws.numel() < bytes_:
+        ws = _workspaces[device.index, raw] = torch.empty(bytes_, dtype=torch.uint8,
+                                                          device=device)
+    return ws
+
+
 def _as_stream(stream) -> torch.cuda.Stream:
     if not isinstance(stream, int):
         return stream
@@ -149,7 +164,7 @@ class PagedCache:
                                  "[n_pages, kv_heads] on the pages' device")
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.n_pages, self.dtype, self.page_dtype, self.k, self.v = n_pages, dtype, held, k, v
-        self.k_scales, self.v_scales = k_scales, v_scales
+        self.k_scales, self.v_scales, self._codes = k_scales, v_scales, codes
         self.device, self._index = k.device, k.device.index
         self._bounds_shape = (n_pages, kv_heads, 2, head_dim)
         # a dimension of one element has no stride to speak of
@@ -305,13 +320,20 @@ class PagedCache:
             if n == 0:  # its null pointer would say that there are no lists
                 raise ValueError("pages lists no pages")
         raw = _raw_stream(self._index)
-        ws = _workspace(self.device, raw)
+        size = ibp.PAGED_WORKSPACE_BYTES
+        if self._codes and pages is None and batch.n_tokens > 64:
+            want = ctypes.c_uint64(0)
+            self._lib.ibp_paged_workspace(self.handle, batch.address, heads, ctypes.byref(want))
+            if size < want.value <= _MOST_WORKSPACE:
+                size = want.value
+        ws = (_workspace(self.device, raw) if size == ibp.PAGED_WORKSPACE_BYTES
+              else _large_workspace(self.device, raw, size))
         ibp._check(self._lib.ibp_paged_attention(
             self.handle, batch.address, q.data_ptr(), qs, heads, out.data_ptr(),
             total.data_ptr() if lse else None,
             1.0 / math.sqrt(self.head_dim) if scale is None else scale, 1 if causal else 0, window,
-            None if pages is None else pages.data_ptr(), n, ws.data_ptr(),
-            ibp.PAGED_WORKSPACE_BYTES, raw), "ibp_paged_attention")
+            None if pages is None else pages.data_ptr(), n, ws.data_ptr(), size, raw),
+            "ibp_paged_attention")
         return (out, total) if lse else out
 
     def _bounds(self, batch: PagedBatch, bounds: torch.Tensor) -> None:

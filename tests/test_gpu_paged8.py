@@ -105,8 +105,10 @@ class Setup:
         scale = two(self.scales[which][page].long() - 127)
         return numbers()[self.codes[which][page, pos % self.P].long()] * scale[..., None], scale
 
-    def check(self, out, lse, causal=True, window=0, scale=None, pages=None, zero=(), status=0):
-        """zero: rows (sequence, token) that could not be read."""
+    def check(self, out, lse, causal=True, window=0, scale=None, pages=None, zero=(), status=0,
+              weight=2.0 ** -11):
+        """zero: rows (sequence, token) that could not be read; weight: the rounding of a weight
+        (fp16's half step, where pages are made 16-bit ones first bf16's)."""
         scale = 1 / math.sqrt(self.D) if scale is None else scale
         u, G, e = U[self.dtype], self.G, 2.0 ** -24
         assert self.cache.status() == status
@@ -157,7 +159,7 @@ class Setup:
                 d = 2 * (err + (smax + 130) * 2.0 ** -23 + 2.0 ** -20)
                 quantum = (torch.where(see, p * VS[:, h][None], 0.0).amax(1, keepdim=True) * 448
                            if L else 0 * top)
-                bound = (u * ref.abs() + (2.0 ** -11 + 2 * d + 2.0 ** -20) * absv
+                bound = (u * ref.abs() + (weight + 2 * d + 2.0 ** -20) * absv
                          + L * 2.0 ** -25 * quantum)
                 if self.dtype == torch.float16:
                     bound = bound + 2.0 ** -25
@@ -207,6 +209,62 @@ def test_step(q_lens, kv_lens, G, D, P, dtype):
 ])
 def test_chunk(q_lens, kv_lens, G, D, P, layout, dtype):
     s = Setup(q_lens, kv_lens, G, 2, D, P, dtype, layout)
+    s.check(*attend(s))
+
+
+BF16_WEIGHT = 2.0 ** -8  # half a step relative to the weight, as finfo(bf16).eps / 2
+
+
+@pytest.mark.parametrize("q_lens,kv_lens,G,D,P,layout,window,causal", [
+    ([1600], [1600], 1, 128, 16, "rows", 0, True), ([400, 801], [2001, 900], 4, 80, 8, "heads", 0, True),
+    ([7, 1, 500], [300, 45, 513], 12, 112, 256, "rows", 0, True),
+    ([900], [3000], 2, 128, 32, "heads", 77, True), ([333], [1111], 5, 96, 64, "rows", 0, False),
+])
+def test_long_chunks_of_bf16(q_lens, kv_lens, G, D, P, layout, window, causal):
+    """Six tiles and more to a sequence and head: 16-bit pages in the workspace."""
+    s = Setup(q_lens, kv_lens, G, 2, D, P, torch.bfloat16, layout)
+    assert ibp.ibp_paged_workspace(s.cache.handle, s.batch.desc, 2 * G) > ibp.PAGED_WORKSPACE_BYTES
+    out, lse = attend(s, window=window, causal=causal)
+    s.check(out, lse, window=window, causal=causal, weight=BF16_WEIGHT)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        again = s.cache.attention(s.batch, s.q, window=window, causal=causal)
+    g.replay()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, out)
+
+
+def test_long_chunks_of_bf16_bad_pages():
+    """Pages that cannot be read and NaN in the others, through 16-bit pages."""
+    for kv in (0, 1):
+        s = Setup([500], [900], 4, 2, 128, 16, torch.bfloat16)
+        s.codes[1][s.table[0, 40].long(), 3, 0, 5] = NAN  # a value: its head's channel alone
+        good = attend(s)
+        s.check(*good, weight=BF16_WEIGHT)
+        at = s.table[0, 50].long()
+        own = s.scales[kv][at, 1].clone()
+        s.scales[kv][at, 1] = 255  # one head's page, from token 400 on
+        out, lse = attend(s)
+        assert s.cache.status() == ibp.IBP_ERANGE
+        a, b = out.view(500, 2, 512).view(torch.int16), good[0].view(500, 2, 512).view(torch.int16)
+        assert not out.view(500, 2, 512)[400:, 1].any()
+        assert torch.equal(a[:, 0], b[:, 0]) and torch.equal(a[:400], b[:400])
+        assert (lse[400:, 4:] == -math.inf).all() and torch.equal(lse[:, :4], good[1][:, :4])
+        s.scales[kv][at, 1] = own
+        s.table[0, 50] = s.n_pages
+        out, _ = attend(s)
+        assert s.cache.status() == ibp.IBP_ERANGE
+        assert not out[400:].any() and torch.equal(out[:400].view(torch.int16),
+                                                   good[0][:400].view(torch.int16))
+
+
+def test_small_workspace_of_long_chunks(monkeypatch):
+    """Without the room the codes are multiplied: another rounding of the weights, no more."""
+    from lossless_invariant_bit_gb300 import paged
+    s = Setup([900], [3000], 2, 2, 128, 32, torch.bfloat16)
+    s.check(*attend(s), weight=BF16_WEIGHT)
+    monkeypatch.setattr(paged, "_MOST_WORKSPACE", 0)
     s.check(*attend(s))
 
 

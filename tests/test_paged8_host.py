@@ -45,6 +45,10 @@ def test_null_arguments(real):
         assert real.ibp_paged_create_8bit(ctypes.byref(out), ctypes.addressof(d), ks,
                                           vs) == ibp.IBP_EINVAL
         assert out.value is None
+    n = ctypes.c_uint64(7)
+    b = ibp.ibp_paged_batch()
+    assert real.ibp_paged_workspace(None, ctypes.addressof(b), 8,
+                                    ctypes.byref(n)) == ibp.IBP_EINVAL and n.value == 7
     assert real.ibp_paged_resize(None, ctypes.addressof(t), 16, 16, 16, 1, None) == ibp.IBP_EINVAL
 
 
