@@ -355,11 +355,15 @@ __global__ void __launch_bounds__(128)
 }
 
 // ---------------------------------------------------------------- 16-bit pages
-// One CTA for each (sequence, page, keys or values): codes times scales as bf16 (exact), one
-// head after the other, for the pages that the chunk kernel reads.  Every tile of 256 rows
-// converts its keys again in the kernel on codes, at 4400 cycles a block of 128 keys; of
-// converted pages a block takes 2800, and the conversion of 8192 tokens x 8 heads of 128 here
-// 12 us in all.  A head's table has no page where one cannot be read.
+// CTAs of 1024 units of 16 channels, several to each (sequence, page, keys or values): codes
+// times scales as bf16 (exact), one head after the other, for the pages that the chunk kernel
+// reads.  The kernel on codes converts a tile's keys once for every 256 rows, 4400 cycles a
+// block of 128 keys; of converted pages a block takes 2800, and the conversion, bound by the
+// bytes, of 8192 tokens x 8 heads of 128 (16.8 MB to 33.5 MB) 13.6 us from a cold cache (16.2
+// with one CTA to a page and one load in flight).  A head's table has no page where one
+// cannot be read.
+constexpr uint32_t kStageUnits = 4;  // units of 16 channels of a thread, their loads in flight
+
 __global__ void __launch_bounds__(256) k_paged8_stage(PagedAttnArgs a, PagedAttnArgs to) {
   const uint32_t s = blockIdx.x / a.b.max_pages, i = blockIdx.x - s * a.b.max_pages;
   const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
@@ -371,7 +375,7 @@ __global__ void __launch_bounds__(256) k_paged8_stage(PagedAttnArgs a, PagedAttn
   const bool values = blockIdx.y != 0u;
   const int32_t page = __ldg(a.b.table + s * a.b.table_stride + i);
   const bool there = page >= 0 && (uint32_t)page < a.g.n_pages;
-  if (!values)
+  if (!values && blockIdx.z == 0u)
     for (uint32_t h = threadIdx.x; h < H; h += blockDim.x)
       const_cast<int32_t*>(to.b.table)[s * to.b.table_stride + h * to.b.table_heads + i] =
           there && scales_ok(page_scales(a.g, (uint32_t)page, h)) ? (int32_t)blockIdx.x : -1;
@@ -380,12 +384,22 @@ __global__ void __launch_bounds__(256) k_paged8_stage(PagedAttnArgs a, PagedAttn
   const uint8_t* scales = (values ? a.g.v_scales : a.g.k_scales) + (uint64_t)(uint32_t)page * H;
   uint8_t* dst = (values ? to.g.v : to.g.k) + (uint64_t)blockIdx.x * to.g.page_stride;
   const uint32_t chunks = D / 16u, rows = P * chunks;
-  for (uint32_t x = threadIdx.x; x < rows * H; x += blockDim.x) {  // 16 channels
-    const uint32_t h = x / rows, r = x - h * rows, t = r / chunks, c = r - t * chunks;
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + t * a.g.token_stride +
-                                                         h * a.g.head_stride + c * 16u));
-    const float f = scale_of(__ldg(scales + h));
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t x = blockIdx.z * (256u * kStageUnits) + threadIdx.x;
+  uint4 v[kStageUnits];
+  float f[kStageUnits];
+#pragma unroll
+  for (uint32_t u = 0; u < kStageUnits; ++u) {
+    const uint32_t xu = x + 256u * u;
+    if (xu >= rows * H) break;
+    const uint32_t h = xu / rows, r = xu - h * rows, t = r / chunks, c = r - t * chunks;
+    v[u] = __ldg(reinterpret_cast<const uint4*>(src + t * a.g.token_stride +
+                                                h * a.g.head_stride + c * 16u));
+    f[u] = scale_of(__ldg(scales + h));
+  }
+#pragma unroll
+  for (uint32_t u = 0; u < kStageUnits; ++u, x += 256u) {
+    if (x >= rows * H) break;
+    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
     uint32_t y[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(256) k_paged8_stage(PagedAttnArgs a, PagedAttn
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 z = unpack2(p[j], 0u);
-        y[2 * k + j] = pack2(z.x * f, z.y * f, 1u);
+        y[2 * k + j] = pack2(z.x * f[u], z.y * f[u], 1u);
       }
     }
     uint4* d = reinterpret_cast<uint4*>(dst + (uint64_t)x * 32u);
@@ -465,7 +479,8 @@ cudaError_t launch_paged8_bounds(const PagedGeom& g, const PagedBatchView& b, ui
 
 cudaError_t launch_paged8_stage(const PagedAttnArgs& a, const PagedAttnArgs& staged,
                                 cudaStream_t st) {
-  const dim3 grid((unsigned)((uint64_t)a.b.n_seqs * a.b.max_pages), 2);
+  const uint32_t units = (a.g.H * (a.g.D / 16u)) << a.g.page_lg, per = 256u * kStageUnits;
+  const dim3 grid((unsigned)((uint64_t)a.b.n_seqs * a.b.max_pages), 2, (units + per - 1u) / per);
   k_paged8_stage<<<grid, 256, 0, st>>>(a, staged);
   return cudaGetLastError();
 }
