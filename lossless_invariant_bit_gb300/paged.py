@@ -432,10 +432,11 @@ class PageTables:
         what sequences grow by together; of one at most max_q_tokens (n_tokens).  Returns the
         batch of the new tokens, whose tensors are these tables' (another call changes them), and
         their slots (int64 [n_tokens]: page * page_tokens + place, rows of key_rows() and
-        value_rows()); nothing when n_tokens is 0: such a call only shrinks.
+        value_rows(); behind the last new token's they stay as they were); nothing when n_tokens
+        is 0: such a call only shrinks.
 
-        Where that cannot be done as a whole nothing changes, the batch is empty, and
-        the cache's status says IBP_ERANGE."""
+        Where that cannot be done as a whole nothing changes, the batch is empty (no slot is
+        written either), and the cache's status says IBP_ERANGE."""
         if stream is not None:
             with torch.cuda.stream(_as_stream(stream)):
                 return self.resize(target, n_tokens, max_q_tokens, slots)
