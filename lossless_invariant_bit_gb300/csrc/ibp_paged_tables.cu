@@ -22,6 +22,7 @@ namespace ibp {
 namespace {
 
 constexpr uint32_t kThreads = 256;
+constexpr uint32_t kLooks = 4;  // tokens of a thread whose pages are looked up together
 
 struct Sums {
   uint64_t gone, come, rows;
@@ -203,17 +204,46 @@ __device__ __forceinline__ void take(const PagedTablesArgs& a, bool ok, const Su
       if (s + 1u == a.n_seqs) a.q_starts[s + 1u] = (int32_t)(row + before + p.rows);
     }
     __syncthreads();
-    const uint32_t from = max(t0, row) + threadIdx.x;
-    uint32_t i = last_at_most<kT>(s_row, from);
-#pragma unroll 4
-    for (uint32_t x = from; x < min(t1, row + rows); x += kT) {
+    const uint32_t end = min(t1, row + rows);
+    uint32_t x = max(t0, row) + threadIdx.x;
+    uint32_t i = last_at_most<kT>(s_row, x);
+    // the sequence in registers, until its last token
+    uint32_t next = 0, shift = 0, have = 0, taken = 0;
+    int32_t* entries = nullptr;
+    auto enter = [&] {
       while (i + 1u < kT && s_row[i + 1u] <= x) ++i;
-      const uint32_t old = s_old[i], pos = old + (x - s_row[i]), at = pos >> lg;
-      int32_t* entry = a.table + (uint64_t)(c + i) * a.table_stride + at;
-      const bool fresh = at >= (old + P - 1u) >> lg;  // its first token writes its entry
-      const int32_t id = fresh ? a.free_pages[top - (s_page[i] + at)] : *entry;
-      if (fresh && (pos & (P - 1u)) == 0u) *entry = id;
-      if (a.slots) a.slots[x] = ((int64_t)id << lg) + (pos & (P - 1u));
+      next = i + 1u < kT ? s_row[i + 1u] : ~0u;
+      shift = s_old[i] - s_row[i];
+      have = (s_old[i] + P - 1u) >> lg;
+      taken = top - s_page[i];
+      entries = a.table + (uint64_t)(c + i) * a.table_stride;
+    };
+    for (; x < end; x += kLooks * kT) {
+      // looked up together; a new page's first token writes its entry
+      uint32_t in[kLooks];
+      int32_t id[kLooks];
+      int32_t* entry[kLooks];
+      const uint32_t x0 = x;
+#pragma unroll
+      for (uint32_t u = 0; u < kLooks; ++u, x += kT) {
+        entry[u] = nullptr;
+        id[u] = 0;
+        if (x >= end) break;
+        if (x >= next) enter();
+        const uint32_t pos = x + shift, at = pos >> lg;
+        const bool fresh = at >= have;
+        in[u] = pos & (P - 1u);
+        id[u] = *(fresh ? a.free_pages + (taken - at) : entries + at);
+        if (fresh && in[u] == 0u) entry[u] = entries + at;
+      }
+      x = x0;
+#pragma unroll
+      for (uint32_t u = 0; u < kLooks; ++u) {
+        const uint32_t y = x0 + u * kT;
+        if (y >= end) break;
+        if (entry[u]) *entry[u] = id[u];
+        if (a.slots) a.slots[y] = ((int64_t)id[u] << lg) + in[u];
+      }
     }
     row += rows;
     page += pages;
@@ -259,16 +289,16 @@ __global__ void __launch_bounds__(kThreads) k_paged_resize(PagedTablesArgs a) {
 cudaError_t launch_paged_resize(const PagedTablesArgs& a, int sm_count, cudaStream_t st) {
   // One CTA and one launch, or two: 20 sequences of 124 pages, up to 5 tokens each, 6.5 us against
   // 7.5;
-  // 250 sequences of 2048 pages, 32768 new tokens, need the two (18.4 us).
+  // 250 sequences of 2048 pages, 32768 new tokens, need the two (14.3 us).
   const uint64_t entries = (uint64_t)a.n_seqs * a.max_pages;
   if (entries <= 16u * kThreads && a.n_tokens <= 4u * kThreads) {
     k_paged_resize<<<1, kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
-  // Two loads to a thread, four CTAs to an SM at most: a look-up waits for the last, and each CTA
-  // takes the sums again.
+  // Two loads to a thread, two CTAs to an SM at most: a look-up waits for the last, and each CTA
+  // takes the sums again (250 sequences: 14.3 us; one 16.2, three 15.3, four 16.5, six 20.8).
   auto ctas = [&](uint64_t n) {
-    const uint64_t c = (n + 2u * kThreads - 1) / (2u * kThreads), most = 4ull * sm_count;
+    const uint64_t c = (n + 2u * kThreads - 1) / (2u * kThreads), most = 2ull * sm_count;
     return (unsigned)(c < 1u ? 1u : c > most ? most : c);
   };
   k_paged_give<<<ctas(entries), kThreads, 0, st>>>(a);

@@ -326,8 +326,14 @@ class PagedCache:
             self._lib.ibp_paged_workspace(self.handle, batch.address, heads, ctypes.byref(want))
             if size < want.value <= _MOST_WORKSPACE:
                 size = want.value
-        ws = (_workspace(self.device, raw) if size == ibp.PAGED_WORKSPACE_BYTES
-              else _large_workspace(self.device, raw, size))
+        ws = None
+        if size != ibp.PAGED_WORKSPACE_BYTES:
+            try:
+                ws = _large_workspace(self.device, raw, size)
+            except torch.OutOfMemoryError:  # (the call does without)
+                size = ibp.PAGED_WORKSPACE_BYTES
+        if ws is None:
+            ws = _workspace(self.device, raw)
         ibp._check(self._lib.ibp_paged_attention(
             self.handle, batch.address, q.data_ptr(), qs, heads, out.data_ptr(),
             total.data_ptr() if lse else None,

@@ -264,7 +264,13 @@ def test_small_workspace_of_long_chunks(monkeypatch):
     from lossless_invariant_bit_gb300 import paged
     s = Setup([900], [3000], 2, 2, 128, 32, torch.bfloat16)
     s.check(*attend(s), weight=BF16_WEIGHT)
-    monkeypatch.setattr(paged, "_MOST_WORKSPACE", 0)
+    with monkeypatch.context() as m:
+        m.setattr(paged, "_MOST_WORKSPACE", 0)
+        s.check(*attend(s))
+
+    def none_left(*a):
+        raise torch.OutOfMemoryError("none left")
+    monkeypatch.setattr(paged, "_large_workspace", none_left)
     s.check(*attend(s))
 
 
