@@ -274,6 +274,63 @@ def test_small_workspace_of_long_chunks(monkeypatch):
     s.check(*attend(s))
 
 
+def test_long_chunks_of_bf16_in_padded_batches():
+    """Rows behind the last sequence stay; tokens without a position see nothing."""
+    s = Setup([700, 900], [1000, 900], 4, 2, 128, 16, torch.bfloat16)
+    want = s.cache.attention(s.batch, s.q)
+    q = torch.cat([s.q, torch.full_like(s.q[:77], float("nan"))])
+    out = torch.full_like(q, 3.0)
+    b = s.cache.batch(s.table, s.batch.kv_lens, s.batch.q_starts, s.T + 77, 2000)
+    s.cache.attention(b, q, out=out)
+    assert torch.equal(out[:s.T], want) and bool((out[s.T:] == 3.0).all())
+    assert s.cache.status() == 0
+    s = Setup([700, 900], [1000, 600], 4, 2, 128, 16, torch.bfloat16)  # 300 of 900 have none
+    got, lse = attend(s)
+    s.check(got, lse, weight=BF16_WEIGHT)
+    assert not got[700:1000].any() and bool((lse[700:1000] == -math.inf).all())
+
+
+def test_long_chunks_of_bf16_streams_threads_graphs():
+    """The larger workspace: one for each stream, grown while calls are in flight, a graph's own."""
+    import threading
+
+    small = Setup([900], [1000], 2, 2, 128, 16, torch.bfloat16, seed=1)
+    large = Setup([500, 900], [9000, 4000], 4, 2, 128, 16, torch.bfloat16, seed=2)
+    want = [s.cache.attention(s.batch, s.q) for s in (small, large)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    outs = [[], []]
+
+    def work(i, s):
+        with torch.cuda.stream(side):
+            outs[i].extend(s.cache.attention(s.batch, s.q) for _ in range(10))
+        side.synchronize()
+
+    ts = [threading.Thread(target=work, args=a) for a in enumerate((small, large))]
+    for x in ts:
+        x.start()
+    for x in ts:
+        x.join()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert len(o) == 10 and all(torch.equal(x, w) for x in o)
+    graphs = []
+    for s in (small, large):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = s.cache.attention(s.batch, s.q)
+        graphs.append((g, out))
+    for _ in range(3):
+        for (g, out), w in zip(graphs, want):
+            out.zero_()
+            g.replay()
+            s = small if w is want[0] else large
+            beside = s.cache.attention(s.batch, s.q, stream=side)
+            torch.cuda.synchronize()
+            assert torch.equal(out, w) and torch.equal(beside, w)
+    assert small.cache.status() == 0 and large.cache.status() == 0
+
+
 def test_many_short_tiles():
     """More tiles to a CTA than any of its rings is long, both kernels' at once."""
     q_lens = [17 + i % 30 if i % 3 else 1 + i % 4 for i in range(400)]
