@@ -110,7 +110,8 @@ struct PagedLaunches {
   decltype(&launch_paged_chunk) chunk;
   decltype(&launch_paged_chunk_join) chunk_join;
   // NULL, or makes 16-bit pages of what a call's chunk kernel reads, and their table.
-  cudaError_t (*stage)(const PagedAttnArgs& a, const PagedAttnArgs& staged, cudaStream_t st);
+  cudaError_t (*stage)(const PagedAttnArgs& a, const PagedAttnArgs& staged, int sm_count,
+                       cudaStream_t st);
 };
 
 #ifdef __CUDACC__

@@ -362,65 +362,77 @@ __global__ void __launch_bounds__(128)
 }
 
 // ---------------------------------------------------------------- 16-bit pages
-// CTAs of 1024 units of 16 channels, several to each (sequence, page, keys or values): codes
-// times scales as bf16 (exact), one head after the other, for the pages that the chunk kernel
-// reads.  The kernel on codes converts a tile's keys once for every 256 rows, 4400 cycles a
-// block of 128 keys; of converted pages a block takes 2800, and the conversion, bound by the
-// bytes, of 8192 tokens x 8 heads of 128 (16.8 MB to 33.5 MB) 13.6 us from a cold cache (16.2
-// with one CTA to a page and one load in flight).  A head's table has no page where one
-// cannot be read.
-constexpr uint32_t kStageUnits = 4;  // units of 16 channels of a thread, their loads in flight
+// Codes times scales as bf16 (exact), one head after the other, for the pages that the chunk
+// kernel reads, in parts of 1024 units of 16 channels.  A sequence's keys (or values) are
+// shared out over gridDim.z CTAs: what its table has room for beyond them costs nothing.
+// The kernel on codes converts a tile's keys once for every 256 rows, 4400 cycles a block of
+// 128 keys; of converted pages a block takes 2800, and the conversion, bound by the bytes, of
+// 8192 tokens x 8 heads of 128 (16.8 MB to 33.5 MB) 13.6 us from a cold cache (16.2 with one
+// load in flight).  A head's table has no page where one cannot be read.
+constexpr uint32_t kStageUnits = 4;  // units of a thread, their loads in flight
+constexpr uint32_t kStagePart = 256u * kStageUnits;
 
 __global__ void __launch_bounds__(256) k_paged8_stage(PagedAttnArgs a, PagedAttnArgs to) {
-  const uint32_t s = blockIdx.x / a.b.max_pages, i = blockIdx.x - s * a.b.max_pages;
+  const uint32_t s = blockIdx.x;
   const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
   if (q.n == 0 || q.n * a.G <= a.max_rows) return;
-  const uint32_t P = 1u << a.g.page_lg, H = a.g.H, D = a.g.D;
+  const uint32_t lg = a.g.page_lg, H = a.g.H;
+  const uint32_t chunks = a.g.D / 16u, rows = chunks << lg, units = rows * H;
+  const uint32_t parts = (units + kStagePart - 1u) / kStagePart;
   const int64_t first = (int64_t)q.L - q.n;
   const int64_t lo = a.window ? first + 1 - (int64_t)a.window : 0;
-  if ((uint64_t)i * P >= q.L || (int64_t)(i + 1u) * P <= lo) return;
+  const uint32_t i0 = lo > 0 ? (uint32_t)lo >> lg : 0u, i1 = (q.L + (1u << lg) - 1u) >> lg;
   const bool values = blockIdx.y != 0u;
-  const int32_t page = __ldg(a.b.table + s * a.b.table_stride + i);
-  const bool there = page >= 0 && (uint32_t)page < a.g.n_pages;
-  if (!values && blockIdx.z == 0u)
-    for (uint32_t h = threadIdx.x; h < H; h += blockDim.x)
-      const_cast<int32_t*>(to.b.table)[s * to.b.table_stride + h * to.b.table_heads + i] =
-          there && scales_ok(page_scales(a.g, (uint32_t)page, h)) ? (int32_t)blockIdx.x : -1;
-  if (!there) return;
-  const uint8_t* src = (values ? a.g.v : a.g.k) + (uint64_t)(uint32_t)page * a.g.page_stride;
-  const uint8_t* scales = (values ? a.g.v_scales : a.g.k_scales) + (uint64_t)(uint32_t)page * H;
-  uint8_t* dst = (values ? to.g.v : to.g.k) + (uint64_t)blockIdx.x * to.g.page_stride;
-  const uint32_t chunks = D / 16u, rows = P * chunks;
-  uint32_t x = blockIdx.z * (256u * kStageUnits) + threadIdx.x;
-  uint4 v[kStageUnits];
-  float f[kStageUnits];
+  const uint8_t* codes = values ? a.g.v : a.g.k;
+  const uint8_t* bytes = values ? a.g.v_scales : a.g.k_scales;
+  for (uint32_t i = i0 + blockIdx.z / parts, part = blockIdx.z % parts; i < i1;) {
+    const uint32_t at = s * a.b.max_pages + i;  // the page of what is made
+    const int32_t page = __ldg(a.b.table + s * a.b.table_stride + i);
+    const bool there = page >= 0 && (uint32_t)page < a.g.n_pages;
+    if (!values && part == 0u)
+      for (uint32_t h = threadIdx.x; h < H; h += blockDim.x)
+        const_cast<int32_t*>(to.b.table)[s * to.b.table_stride + h * to.b.table_heads + i] =
+            there && scales_ok(page_scales(a.g, (uint32_t)page, h)) ? (int32_t)at : -1;
+    if (there) {
+      const uint8_t* src = codes + (uint64_t)(uint32_t)page * a.g.page_stride;
+      const uint8_t* scales = bytes + (uint64_t)(uint32_t)page * H;
+      uint8_t* dst = (values ? to.g.v : to.g.k) + (uint64_t)at * to.g.page_stride;
+      const uint32_t x0 = part * kStagePart + threadIdx.x;
+      uint4 v[kStageUnits];
+      float f[kStageUnits];
 #pragma unroll
-  for (uint32_t u = 0; u < kStageUnits; ++u) {
-    const uint32_t xu = x + 256u * u;
-    if (xu >= rows * H) break;
-    const uint32_t h = xu / rows, r = xu - h * rows, t = r / chunks, c = r - t * chunks;
-    v[u] = __ldg(reinterpret_cast<const uint4*>(src + t * a.g.token_stride +
-                                                h * a.g.head_stride + c * 16u));
-    f[u] = scale_of(__ldg(scales + h));
-  }
+      for (uint32_t u = 0; u < kStageUnits; ++u) {
+        const uint32_t x = x0 + 256u * u;
+        if (x >= units) break;
+        const uint32_t h = x / rows, r = x - h * rows, t = r / chunks, c = r - t * chunks;
+        v[u] = __ldg(reinterpret_cast<const uint4*>(src + t * a.g.token_stride +
+                                                    h * a.g.head_stride + c * 16u));
+        f[u] = scale_of(__ldg(scales + h));
+      }
 #pragma unroll
-  for (uint32_t u = 0; u < kStageUnits; ++u, x += 256u) {
-    if (x >= rows * H) break;
-    const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-    uint32_t y[8];
+      for (uint32_t u = 0; u < kStageUnits; ++u) {
+        const uint32_t x = x0 + 256u * u;
+        if (x >= units) break;
+        const uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+        uint32_t y[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t p[2];
-      codes_to_fp16(w[k], p[0], p[1]);
+        for (int k = 0; k < 4; ++k) {
+          uint32_t p[2];
+          codes_to_fp16(w[k], p[0], p[1]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float2 z = unpack2(p[j], 0u);
-        y[2 * k + j] = pack2(z.x * f[u], z.y * f[u], 1u);
+          for (int j = 0; j < 2; ++j) {
+            const float2 z = unpack2(p[j], 0u);
+            y[2 * k + j] = pack2(z.x * f[u], z.y * f[u], 1u);
+          }
+        }
+        uint4* d = reinterpret_cast<uint4*>(dst + (uint64_t)x * 32u);
+        d[0] = make_uint4(y[0], y[1], y[2], y[3]);
+        d[1] = make_uint4(y[4], y[5], y[6], y[7]);
       }
     }
-    uint4* d = reinterpret_cast<uint4*>(dst + (uint64_t)x * 32u);
-    d[0] = make_uint4(y[0], y[1], y[2], y[3]);
-    d[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    part += gridDim.z % parts;
+    i += gridDim.z / parts;
+    if (part >= parts) part -= parts, ++i;
   }
 }
 
@@ -485,10 +497,12 @@ cudaError_t launch_paged8_bounds(const PagedGeom& g, const PagedBatchView& b, ui
 }
 
 cudaError_t launch_paged8_stage(const PagedAttnArgs& a, const PagedAttnArgs& staged,
-                                cudaStream_t st) {
-  const uint32_t units = (a.g.H * (a.g.D / 16u)) << a.g.page_lg, per = 256u * kStageUnits;
-  const dim3 grid((unsigned)((uint64_t)a.b.n_seqs * a.b.max_pages), 2, (units + per - 1u) / per);
-  k_paged8_stage<<<grid, 256, 0, st>>>(a, staged);
+                                int sm_count, cudaStream_t st) {
+  const uint32_t units = (a.g.H * (a.g.D / 16u)) << a.g.page_lg;
+  const uint64_t most = (uint64_t)a.b.max_pages * ((units + kStagePart - 1u) / kStagePart);
+  uint64_t z = 4ull * sm_count / a.b.n_seqs;  // (keys and values: 8 CTAs to an SM)
+  z = z < 1u ? 1u : z > most ? most : z;
+  k_paged8_stage<<<dim3(a.b.n_seqs, 2, (unsigned)z), 256, 0, st>>>(a, staged);
   return cudaGetLastError();
 }
 

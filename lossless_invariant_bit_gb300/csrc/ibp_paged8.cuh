@@ -17,7 +17,7 @@ cudaError_t launch_paged8_chunk(const PagedAttnArgs& a, const PagedMaps& m, int 
 cudaError_t launch_paged8_chunk_join(const PagedAttnArgs& a, int sm_count, cudaStream_t st);
 
 cudaError_t launch_paged8_stage(const PagedAttnArgs& a, const PagedAttnArgs& staged,
-                                cudaStream_t st);
+                                int sm_count, cudaStream_t st);
 
 // Bytes of scales: 2^-50 to 2^50.  The range is bounded so that no power of a page's scale,
 // nor the product of two pages', leaves fp32 where a result still depends on it.

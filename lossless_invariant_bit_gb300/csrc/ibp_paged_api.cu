@@ -358,7 +358,7 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
       return IBP_ECUDA;
   }
   std::lock_guard<std::mutex> lock(call_lock(workspace));
-  cudaError_t ce = staged ? run.stage(a, wide, st) : cudaSuccess;
+  cudaError_t ce = staged ? run.stage(a, wide, c->sm_count, st) : cudaSuccess;
   if (ce == cudaSuccess && !few)
     ce = staged ? ibp::launch_paged_chunk(wide, wide_maps, c->sm_count, st)
                 : run.chunk(a, c->maps, c->sm_count, st);

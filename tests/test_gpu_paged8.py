@@ -290,6 +290,19 @@ def test_long_chunks_of_bf16_in_padded_batches():
     assert not got[700:1000].any() and bool((lse[700:1000] == -math.inf).all())
 
 
+def test_long_chunks_of_bf16_in_wide_tables():
+    """Columns that no sequence needs, more parts of pages than CTAs for a sequence."""
+    s = Setup([300, 1, 400, 256, 300] * 8, [2500, 40, 400, 700, 3000] * 8, 8, 2, 128, 16,
+              torch.bfloat16)
+    wide = torch.full((40, 2000), -7, dtype=torch.int32, device=DEV)
+    wide[:, :s.table.shape[1]] = s.table
+    s.table = wide
+    s.batch = s.cache.batch(wide, s.batch.kv_lens, s.batch.q_starts, s.T, 400)
+    assert ibp.ibp_paged_workspace(s.cache.handle, s.batch.desc, 16) > ibp.PAGED_WORKSPACE_BYTES
+    out, lse = attend(s, window=2000)
+    s.check(out, lse, window=2000, weight=BF16_WEIGHT)
+
+
 def test_long_chunks_of_bf16_streams_threads_graphs():
     """The larger workspace: one for each stream, grown while calls are in flight, a graph's own."""
     import threading
