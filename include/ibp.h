@@ -522,8 +522,9 @@ IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc)
  *              largest scale does not hold becomes the largest code; infinities and NaN
  *              become NaN codes.  A page that new tokens go into belongs to one sequence
  *   attention  as over code * scale, in fp32 with weights and codes multiplied in fp16 (in
- *        bf16 where ibp_paged_workspace asks for more: then as over 16-bit pages); the
- *              scales are exact
+ *              bf16 where ibp_paged_workspace asks for more: then as over 16-bit pages);
+ *              the scales are exact.  Weights times their values' scale that lie below 2^-25
+ *              of a row's largest are lost
  *   bounds     of code * scale, rounded to the 16-bit type
  * A scale outside its range is an error like a page id out of range, where it is needed. */
 IBP_API ibp_status ibp_paged_create_8bit(ibp_paged** out, const ibp_paged_desc* desc,
