@@ -28,8 +28,8 @@
 //
 // Bound by HBM where there is enough to read: 325.5 MB of 325.1 MB in 63 us (20 x 1984 tokens),
 // of which about 10 are the start, the last blocks and the join; 5.9 TB/s between them.  Page
-// lists: 16 tokens x 128 pages of 16 in 24 us, 120 tokens x 24 pages of 32 (each token's pages
-// are its own copies, 93 MB from L2) in 27.  One sequence of 517 tokens: 11 us, look-ups.
+// lists: 16 tokens x 128 pages of 16 in 23 us, 120 tokens x 24 pages of 32 (each token's pages
+// are its own copies, 93 MB from L2) in 26.  One sequence of 517 tokens: 9.5 us, look-ups.
 #include "ibp_paged_step.cuh"
 #include "ibp_paged8.cuh"
 #include "ibp_tma.cuh"
@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(StepShape8<kDP, kNT>::kThreads, 1)
       }
       u += count;
     }
+    end_join(run, join);
     if (keys && lane == 0) joins[blockIdx.x] = join;
     // whosever wait gave up: the copies in flight land before the CTA leaves (or these
     // waits give up too)

@@ -24,7 +24,7 @@
 //     7/8 padding (the chunk kernel takes what has more rows).
 //
 // Measured: 20 sequences x 32 heads of 128 x 1984 keys in 104 us, 650 MB at 6.25 TB/s;
-// one sequence of 517 keys 12 us, its look-ups, the first block and the join one
+// one sequence of 517 keys 11 us, its look-ups, the first block and the join one
 // after the other; lists of 128 pages of 16 for 16 tokens x 8 heads 32 us (134 MB at
 // 4.2 TB/s: runs of 14 blocks are short beside the ring's start and the join).
 #include "ibp_paged_step.cuh"
@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kThreads, kDP == 64 ? 2 : 1)
       }
       u += count;
     }
+    end_join(run, join);
     if (lane == 0) joins[blockIdx.x] = join;
     // whosever wait gave up: the copies in flight land before the CTA leaves (or these
     // waits give up too)

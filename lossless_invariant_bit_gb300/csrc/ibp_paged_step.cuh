@@ -28,7 +28,7 @@ struct Join {
   uint32_t first, count;  // CTAs that hold its pieces: first .. first + count - 1; 0: none
   uint32_t q0, head;      // first row of the sequence (or token), K/V head
   uint32_t row0, rows;    // the tile's rows
-  uint32_t pad[2];
+  uint64_t tile_u;        // (the first kernel's: where its blocks begin in the list)
 };
 
 // What the producer tells the others of a run of blocks of one tile; count 0: no
@@ -138,6 +138,17 @@ struct Run {
   uint32_t ctas;    // CTAs with a run: never more than blocks
 };
 
+// Where CTA b's run begins: total * b / ctas (b <= ctas <= kMaxCtas), by a division of 32 bits
+// where the list is that short, as the quotients below are: one of 64 takes 0.2 us.
+__device__ __forceinline__ uint64_t run_start(uint64_t total, uint32_t b, uint32_t ctas) {
+  if (total >> 32) return total * b / ctas;
+  const uint32_t n = (uint32_t)total, q = n / ctas;
+  return (uint64_t)q * b + (n - q * ctas) * b / ctas;
+}
+__device__ __forceinline__ uint64_t quotient(uint64_t x, uint32_t d) {
+  return x >> 32 ? x / d : (uint32_t)x / d;
+}
+
 template <bool kSel, uint32_t kThreads>
 __device__ __forceinline__ Run step_run(const PagedAttnArgs& a,
                                         uint64_t (&s_scan)[kThreads / 32],
@@ -154,12 +165,12 @@ __device__ __forceinline__ Run step_run(const PagedAttnArgs& a,
     total = (uint64_t)a.b.n_tokens * a.g.H * nrb * nb;
     if (total < ctas) ctas = (uint32_t)total;
     if (blockIdx.x < ctas) {
-      u0 = total * blockIdx.x / ctas;
-      u1 = total * (blockIdx.x + 1u) / ctas;
-      const uint64_t ti = u0 / nb;
-      ld.t.rb = (uint32_t)(ti % nrb);
-      ld.t.head = (uint32_t)(ti / nrb % a.g.H);
-      ld.t.s = (uint32_t)(ti / nrb / a.g.H);
+      u0 = run_start(total, blockIdx.x, ctas);
+      u1 = run_start(total, blockIdx.x + 1u, ctas);
+      const uint64_t ti = quotient(u0, nb), th = quotient(ti, nrb), ts = quotient(th, a.g.H);
+      ld.t.rb = (uint32_t)(ti - th * nrb);
+      ld.t.head = (uint32_t)(th - ts * a.g.H);
+      ld.t.s = (uint32_t)ts;
       ld.blk = (uint32_t)(u0 - ti * nb);
       tile_u = ti * nb;
       tile_of<kSel>(a, ld.t);
@@ -167,11 +178,13 @@ __device__ __forceinline__ Run step_run(const PagedAttnArgs& a,
     __syncthreads();
   } else {
     uint32_t b0, lo, nrb;
-    uint64_t mine = 0;
+    uint64_t mine = 0, own = 0;  // own: of sequence tid
     for (uint32_t s = tid; s < a.b.n_seqs; s += kThreads) {
       const PagedSeq q = paged_seq(a.b, a.g.page_lg, s);
       if (!q.ok) set_status(a.g.status, IBP_ERANGE);
-      mine += (uint64_t)seq_blocks(a, q, b0, lo, nrb) * nrb;
+      const uint32_t n = seq_blocks(a, q, b0, lo, nrb);
+      mine += (uint64_t)n * nrb;
+      if (s == tid) own = mine;
     }
 #pragma unroll
     for (int d = 16; d; d >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, d);
@@ -181,16 +194,18 @@ __device__ __forceinline__ Run step_run(const PagedAttnArgs& a,
     total *= a.g.H;
     if (total < ctas) ctas = (uint32_t)total;
     if (blockIdx.x < ctas) {
-      u0 = total * blockIdx.x / ctas;
-      u1 = total * (blockIdx.x + 1u) / ctas;
+      u0 = run_start(total, blockIdx.x, ctas);
+      u1 = run_start(total, blockIdx.x + 1u, ctas);
     }
     // the sequence that holds block u0: sums over as many sequences as threads at a time
     uint64_t base = 0;
     for (uint32_t c = 0; c < a.b.n_seqs && u0 < u1; c += kThreads) {
-      uint64_t nb = 0;
-      if (c + tid < a.b.n_seqs) {
+      uint64_t nb = own;
+      if (c && c + tid < a.b.n_seqs) {
         nb = seq_blocks(a, paged_seq(a.b, a.g.page_lg, c + tid), b0, lo, nrb);
         nb *= nrb;
+      } else if (c) {
+        nb = 0;
       }
       uint64_t inc = nb;
 #pragma unroll
@@ -219,9 +234,10 @@ __device__ __forceinline__ Run step_run(const PagedAttnArgs& a,
       ld.t.s = (uint32_t)s_found[0];
       ld.t.head = 0;
       tile_of<kSel>(a, ld.t);
-      const uint64_t in = u0 - s_found[1], ti = in / ld.t.nb;
-      ld.t.rb = (uint32_t)(ti % ld.t.nrb);
-      ld.t.head = (uint32_t)(ti / ld.t.nrb);
+      const uint64_t in = u0 - s_found[1], ti = quotient(in, ld.t.nb);
+      const uint64_t th = quotient(ti, ld.t.nrb);
+      ld.t.rb = (uint32_t)(ti - th * ld.t.nrb);
+      ld.t.head = (uint32_t)th;
       ld.blk = (uint32_t)(in - ti * ld.t.nb);
       tile_u = u0 - ld.blk;
     }
@@ -254,13 +270,9 @@ __device__ __forceinline__ uint32_t tell_tile(const PagedAttnArgs& a, const Run&
     x->whole = whole;
     x->place = r.tile_u >= r.u0 ? 1u : 0u;
     mbar_arrive(bar);
-    if (more && ends && !whole) {  // this CTA has the tile's last piece
-      // the CTA that holds the tile's first block
-      uint64_t f = r.tile_u * r.ctas / r.total;
-      while (f + 1 < r.ctas && r.total * (f + 1) / r.ctas <= r.tile_u) ++f;
-      while (f > 0 && r.total * f / r.ctas > r.tile_u) --f;
-      join.first = (uint32_t)f;
-      join.count = blockIdx.x - (uint32_t)f + 1u;
+    if (more && ends && !whole) {  // this CTA has the tile's last piece (end_join: its first)
+      join.count = 1;
+      join.tile_u = r.tile_u;
       join.q0 = r.ld.t.q0;
       join.rows = x->rows;
       join.row0 = x->row0;
@@ -268,6 +280,18 @@ __device__ __forceinline__ uint32_t tell_tile(const PagedAttnArgs& a, const Run&
     }
   }
   return count;
+}
+
+// The CTA that holds the first block of the tile to be joined: found when the loads are on
+// their way, not before the first.
+__device__ __forceinline__ void end_join(const Run& r, Join& join) {
+  if (join.count == 0) return;
+  const uint64_t u = join.tile_u;
+  uint32_t f = (uint32_t)(u * r.ctas / r.total);
+  while (f + 1u < r.ctas && run_start(r.total, f + 1u, r.ctas) <= u) ++f;
+  while (f > 0 && run_start(r.total, f, r.ctas) > u) --f;
+  join.first = f;
+  join.count = blockIdx.x - f + 1u;
 }
 
 // A barrier of the kCount warps that compute, and whether any of their threads says so.
@@ -359,17 +383,43 @@ __global__ void __launch_bounds__(128) k_paged_step_join(PagedAttnArgs a) {
   if (count == 0 || r >= rows) return;
   // the first piece lies in its CTA's second place (the tile began there)
   auto at_piece = [&](uint32_t i) { return pieces + 2u * (first + i) + (i == 0u ? 1u : 0u); };
-  float mx = -INFINITY;
-  for (uint32_t i = lane; i < count; i += 32u) mx = fmaxf(mx, __ldcg(&at_piece(i)->m[r]));
+  // the first pieces' numbers, all on their way at once (a tile seldom has more)
+  constexpr uint32_t kFirst = 4;
+  float pm[kFirst], pl[kFirst], po[kFirst][kDP / 32], mx = -INFINITY;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+  for (uint32_t i = 0; i < kFirst; ++i) {
+    pm[i] = -INFINITY;
+    if (i < count) {
+      const Piece<kDP>* p = at_piece(i);
+      pm[i] = __ldcg(&p->m[r]);
+      pl[i] = __ldcg(&p->l[r]);
+#pragma unroll
+      for (int x = 0; x < kDP / 32; ++x) po[i][x] = __ldcg(&p->o[r][lane + 32u * x]);
+    }
+  }
+  for (uint32_t i = kFirst + lane; i < count; i += 32u)
+    mx = fmaxf(mx, __ldcg(&at_piece(i)->m[r]));
+  if (count > kFirst)
+#pragma unroll
+    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+#pragma unroll
+  for (uint32_t i = 0; i < kFirst; ++i) mx = fmaxf(mx, pm[i]);
   const float base = mx == -INFINITY ? 0.f : mx;
   float ll = 0.f, ov[kDP / 32];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kDP / 32; ++i) ov[i] = 0.f;
+#pragma unroll
+  for (uint32_t i = 0; i < kFirst; ++i)
+    if (i < count) {
+      const float f = ex2(pm[i] - base);
+      bad = bad || pl[i] == INFINITY;
+      ll += f * pl[i];
+#pragma unroll
+      for (int x = 0; x < kDP / 32; ++x) ov[x] = fmaf(f, po[i][x], ov[x]);
+    }
 #pragma unroll 4
-  for (uint32_t i = 0; i < count; ++i) {
+  for (uint32_t i = kFirst; i < count; ++i) {
     const Piece<kDP>* p = at_piece(i);
     const float li = __ldcg(&p->l[r]);
     const float f = ex2(__ldcg(&p->m[r]) - base);
