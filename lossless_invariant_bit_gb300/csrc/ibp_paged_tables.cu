@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) k_paged_resize(PagedTablesArgs a) {
 cudaError_t launch_paged_resize(const PagedTablesArgs& a, int sm_count, cudaStream_t st) {
   // One CTA and one launch, or two: 20 sequences of 124 pages, up to 5 tokens each, 6.5 us against
   // 7.5;
-  // 250 sequences of 2048 pages, 32768 new tokens, need the two (14.3 us).
+  // 250 sequences of 2048 pages, 1.33 million new tokens, need the two (14.3 us).
   const uint64_t entries = (uint64_t)a.n_seqs * a.max_pages;
   if (entries <= 16u * kThreads && a.n_tokens <= 4u * kThreads) {
     k_paged_resize<<<1, kThreads, 0, st>>>(a);
