@@ -270,8 +270,8 @@ __global__ void __launch_bounds__(128) k_paged8_append(PagedAppendArgs a, uint32
 // One warp per (page that got new tokens, head), 16 channels per lane: minima and maxima of
 // the codes as fp16 (exact), then the scale, then one rounding to the 16-bit type (none for
 // what an append has written, but beyond that type's range).  8 loads of 16 bytes in flight to
-// a lane: 22.7 thousand tokens 11.3 us, 3.5 TB/s (4 in flight: 13.3), half of it start and look-ups
-// of one wave of CTAs; 20 tokens 2.9.
+// a lane: 34 thousand tokens 11.3 us, 3.5 TB/s (4 in flight: 13.3), half of it start and look-ups
+// of two waves of CTAs; 16 tokens 2.9.
 template <int kLanes, bool kBf16>
 __global__ void __launch_bounds__(128)
     k_paged8_bounds(PagedGeom g, PagedBatchView b, uint8_t* bounds) {
