@@ -47,10 +47,14 @@ constexpr uint32_t kInfos = 4;
 // 2^15: down to 2^-25 of the largest they are normal fp16 numbers.
 constexpr float kLift = 11.f, kMost = 15.f;
 // A block's codes times its pages' shares of its scales lie 2^7 below fp16's largest: exact for
-// pages whose scales are down to 2^-22 of the block's.  A block whose pages differ by more
-// is wide: its codes stay as they are, and its rows take each page's scales.
+// pages whose scales are down to 2^-22 of the block's.  A row's reference takes the block's
+// scale of the values for that of its heaviest key, whose page may have a smaller one: the
+// weights of keys in other blocks then lie lower by as much.  Lifted, fp16 holds them down to
+// 2^-36 of the reference, so with values' scales down to 2^-11 of the block's nothing is
+// lost above 2^-25 of the row's largest weight times scale.  A block whose pages differ by
+// more is wide: its codes stay as they are, and its rows take each page's scales.
 constexpr int32_t kUp = 7;
-constexpr uint32_t kSpread = 22u, kWide = 1u << 31;
+constexpr uint32_t kSpreadK = 22u, kSpreadV = 11u, kWide = 1u << 31;
 constexpr float kLeast = 1e-37f;  // of a row's factor: -inf times it stays -inf
 // Keys whose weights are computed before the first half of them is handed over.
 constexpr int kEarly = 80;
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged8_chunk(PagedAttnArgs a) {
         bad = __ballot_sync(0xFFFFFFFFu, ids != -1 && !fine);
         k_top = __reduce_max_sync(0xFFFFFFFFu, fine ? ks : kScaleLow);
         v_top = __reduce_max_sync(0xFFFFFFFFu, fine ? vs : kScaleLow);
-        wide = __any_sync(0xFFFFFFFFu, fine && (k_top - ks > kSpread || v_top - vs > kSpread));
+        wide = __any_sync(0xFFFFFFFFu, fine && (k_top - ks > kSpreadK || v_top - vs > kSpreadV));
         return wide ? 0x3C003C00u
                     : fp16_power((int32_t)(ks - k_top) + kUp) |
                           fp16_power((int32_t)(vs - v_top) + kUp) << 16;

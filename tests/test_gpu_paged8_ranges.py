@@ -1,0 +1,42 @@
+"""Attention over 8-bit pages where scales and queries differ most: what the header says
+is lost is lost, and nothing else."""
+import math
+
+import pytest
+import torch
+
+from tests.gpu_util import DEV
+from tests.test_gpu_paged8 import E4M3, Setup, attend
+
+pytestmark = pytest.mark.gpu
+
+
+def code_of(x):
+    return int(torch.tensor(x).to(E4M3).view(torch.uint8))
+
+
+# ---------------------------------------------------------------- values' scales in a block
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("spread", [11, 12, 22])
+@pytest.mark.parametrize("n,L,window", [(40, 700, 0), (150, 700, 0), (200, 600, 300)])
+def test_a_large_scale_beside_the_heaviest_key(n, L, window, spread, dtype):
+    """The heaviest key (values of zero) shares its block with a page whose values' scale is
+    2^spread larger, which a row does not see or gives no weight to; the result is
+    the other keys', with weights of 2^-14 of the heaviest's.  (As many sequences and heads as
+    give a CTA a tile's blocks one after the other.)"""
+    s = Setup([n] * 30, [L] * 30, 2, 8, 64, 16, dtype, spread=0)
+    k, v = s.codes
+    heavy, large = 127, 6  # a position, a page: both of the first block
+    pages = s.table.long()
+    k[pages], v[pages] = 0, code_of(448.0)
+    for sc in s.scales:
+        sc[pages] = 127
+    k[pages[:, heavy // 16], heavy % 16, :, 0] = code_of(1.0)
+    v[pages[:, heavy // 16], heavy % 16] = 0
+    k[pages[:, large], :, :, 1] = code_of(256.0)
+    s.scales[1][pages[:, large]] = 127 + spread
+    s.q.zero_()
+    s.q[..., 0] = 14 * math.log(2.0)
+    s.q[..., 1] = -1.0
+    out, lse = attend(s, window=window, scale=1.0)
+    s.check(out, lse, window=window, scale=1.0)
