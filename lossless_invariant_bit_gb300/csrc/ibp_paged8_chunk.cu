@@ -55,7 +55,6 @@ constexpr float kLift = 11.f, kMost = 15.f;
 // more is wide: its codes stay as they are, and its rows take each page's scales.
 constexpr int32_t kUp = 7;
 constexpr uint32_t kSpreadK = 22u, kSpreadV = 11u, kWide = 1u << 31;
-constexpr float kLeast = 1e-37f;  // of a row's factor: -inf times it stays -inf
 // Keys whose weights are computed before the first half of them is handed over.
 constexpr int kEarly = 80;
 
@@ -166,7 +165,7 @@ __device__ __noinline__ Sums wide_block(uint32_t ts, uint32_t to, uint32_t D, co
       const uint32_t page = (uint32_t)key >> box_lg;
       const float2 p = pages[page];
       const bool see = key >= from && key < end && !(badp >> page & 1u);
-      const float v = see ? fmaf(__uint_as_float(x[j]), fmaxf(cr * p.x, kLeast), p.y) : -INFINITY;
+      const float v = see ? fmaf(__uint_as_float(x[j]), row_factor(cr, p.x), p.y) : -INFINITY;
       most = fmaxf(most, v);
       x[j] = __float_as_uint(v);
     }
@@ -633,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_paged8_chunk(PagedAttnArgs a) {
         // The weights need a reference, not the maximum: they are computed with the one
         // at hand while the maximum is found, and again in the rare block whose
         // maximum has outgrown it.
-        const float c = wide ? 1.f : fmaxf(cr * scale.x, kLeast);
+        const float c = wide ? 1.f : row_factor(cr, scale.x);
         const uint64_t c2 = pair2(c, c);
         uint64_t l0, l1, b2;
         auto weights = [&](const int j, uint32_t (&w2)[32]) {  // 4 keys

@@ -40,3 +40,18 @@ def test_a_large_scale_beside_the_heaviest_key(n, L, window, spread, dtype):
     s.q[..., 1] = -1.0
     out, lse = attend(s, window=window, scale=1.0)
     s.check(out, lse, window=window, scale=1.0)
+
+
+# ---------------------------------------------------------------- factors of the scores
+@pytest.mark.parametrize("n,L,wide", [(1, 200, False), (3, 200, True), (60, 300, False),
+                                      (60, 300, True), (300, 500, False), (300, 500, True)])
+def test_the_largest_queries_and_keys_of_zero(n, L, wide):
+    """Queries near 2^120 under keys' scales of 2^50: scores of zero stay zero."""
+    s = Setup([n], [L], 2, 2, 64, 16, torch.bfloat16, spread=0)
+    pages = s.table[0].long()
+    s.codes[0][pages] = 0
+    s.scales[0][pages] = 177
+    if wide:  # pages of one block that differ by more than a block's scale holds
+        s.scales[0][pages[::2]] = 77
+    s.q = (s.q.float() * 2.0 ** 120).bfloat16()
+    s.check(*attend(s))
