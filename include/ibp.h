@@ -524,7 +524,10 @@ IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc)
  *   attention  as over code * scale, in fp32 with weights and codes multiplied in fp16 (in
  *              bf16 where ibp_paged_workspace asks for more: then as over 16-bit pages);
  *              the scales are exact.  Weights times their values' scale that lie below 2^-25
- *              of a row's largest are lost
+ *              of a row's largest are lost.  bf16 queries become fp16 numbers times a power of
+ *              two for each row: a score is off by up to scale * 2^-39 * max |q| * sum |k| over
+ *              the channels (no more than fp32 sums are, but where the keys are zero or tiny in
+ *              the channels in which the row is large); not so as over 16-bit pages
  *   bounds     of code * scale, rounded to the 16-bit type
  * A scale outside its range is an error like a page id out of range, where it is needed. */
 IBP_API ibp_status ibp_paged_create_8bit(ibp_paged** out, const ibp_paged_desc* desc,

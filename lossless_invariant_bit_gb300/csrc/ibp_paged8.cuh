@@ -61,7 +61,7 @@ __device__ __forceinline__ uint32_t code_chunk(uint32_t row, uint32_t chunk) {
 }
 
 // bf16 queries for products in fp16: each row times a power of two that brings its largest
-// magnitude into [2^14, 2^15).
+// magnitude into [2^14, 2^15).  Half a step of fp16's smallest numbers, 2^-25, is 2^-39 of it.
 struct Lift {
   float up, down;
   uint8_t byte;  // down's exponent, as a scale's

@@ -18,7 +18,8 @@
 //                  c, its values' goes into the exponent, and the sum takes 2^-b of it.  m
 //                  refers to the largest c S + b, so W stays within fp16 however the
 //                  blocks' scales differ
-//   queries        fp16, or bf16 brought into its range by a power of two for each row
+//   queries        fp16, or bf16 brought into its range by a power of two for each row (what that
+//                  costs a score: ibp_paged8_step.cu)
 //
 // The products run in fp16, at the rate of bf16's: 8-bit products would need the queries and
 // the weights in two or three parts each to keep their bits, and take as long.

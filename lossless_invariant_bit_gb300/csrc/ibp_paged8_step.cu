@@ -16,7 +16,9 @@
 //     for two (every e4m3 number is an fp16 number); the products run in fp16 with fp32
 //     sums whatever the type of the queries.  bf16 queries are brought into fp16's range
 //     by a power of two for each row: 8 bits of each survive down to 2^-28 of the row's
-//     largest, below that they lose bits that no score can show (2^-39 of it is dropped).
+//     largest, below that they are off by up to 2^-39 of it.  A score is then off by up to
+//     scale 2^-39 max|q| sum|k|: below fp32's rounding of its sum, but where the keys are
+//     zero or tiny in the channels in which the row is large.
 //   - A page's scales never touch an element.  That of its keys multiplies the row's factor of
 //     the scores; that of its values goes into the exponent, w_j = exp2(s_j + b - m), where m is
 //     a reference at most 2^15 below the largest s_j + b: weights and values are then

@@ -5,8 +5,9 @@ import math
 import pytest
 import torch
 
+from lossless_invariant_bit_gb300 import ibp, paged
 from tests.gpu_util import DEV
-from tests.test_gpu_paged8 import E4M3, Setup, attend
+from tests.test_gpu_paged8 import E4M3, F64, Setup, attend
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,50 @@ def test_the_largest_queries_and_keys_of_zero(n, L, wide):
         s.scales[0][pages[::2]] = 77
     s.q = (s.q.float() * 2.0 ** 120).bfloat16()
     s.check(*attend(s))
+
+
+# ---------------------------------------------------------------- queries' range
+def a_query_of_two_channels(n, L, small, keys):
+    """q = (1, small) in two channels, keys zero in the first, `keys` x 1 to 4 in the second."""
+    s = Setup([n], [L], 4, 2, 128, 16, torch.bfloat16, spread=0)
+    pages = s.table[0].long()
+    s.codes[0][pages] = 0
+    few = torch.tensor([code_of(x) for x in (1.0, 1.5, 2.0, 3.0, 4.0)], dtype=torch.uint8,
+                       device=DEV)
+    pick = torch.randint(0, 5, s.codes[0][pages][..., 1].shape, generator=s.g, device=DEV)
+    x = s.codes[0][pages]
+    x[..., 1] = few[pick]
+    s.codes[0][pages] = x
+    s.scales[0][pages] = 127 + keys
+    s.q.zero_()
+    s.q[..., 0] = 1.0
+    s.q[..., 1] = small
+    return s
+
+
+def scores_of(s):
+    """Row 0's of the last token, and what the header allows each to be off by on codes."""
+    K, _ = s.of(0, 0)
+    q = s.q[-1, 0].to(F64)
+    x = K[:, 0] @ q
+    return x, 2.0 ** -39 * float(q.abs().max()) * K[:, 0].abs().sum(1)
+
+
+@pytest.mark.parametrize("small,keys", [(2.0 ** -33 * 1.2421875, 32), (2.0 ** -40, 40)])
+@pytest.mark.parametrize("n,L", [(1, 300), (4, 300), (500, 900)])
+def test_a_query_with_one_large_channel(n, L, small, keys, monkeypatch):
+    """A channel far below the row's largest that alone meets keys: over codes each score is off
+    by 2^-39 max |q| sum |k| at most, over pages made 16-bit ones it is exact."""
+    s = a_query_of_two_channels(n, L, small, keys)
+    x, off = scores_of(s)
+    want = float(torch.logsumexp(x, 0))
+    room = ibp.ibp_paged_workspace(s.cache.handle, s.batch.desc, 8) > ibp.PAGED_WORKSPACE_BYTES
+    assert room == (n == 500)
+    if room:
+        _, lse = attend(s, scale=1.0)
+        assert abs(float(lse[-1, 0]) - want) <= 2.0 ** -18
+        monkeypatch.setattr(paged, "_MOST_WORKSPACE", 0)
+    _, lse = attend(s, scale=1.0)
+    # the log of the sum moves by no more than the largest score does
+    assert abs(float(lse[-1, 0]) - want) <= float(off.max()) + 2.0 ** -18
+    assert s.cache.status() == 0
