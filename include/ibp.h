@@ -663,7 +663,8 @@ typedef struct {
  * A call that cannot be served as a whole (too few free pages, more new tokens than
  * n_tokens, a length or target outside [0, max_pages * page_tokens], a list longer than the
  * cache) sets IBP_ERANGE in the handle's status word and changes nothing, but that q_starts
- * becomes 0: its batch has no rows.  Calls on the same tables follow one another; they may
+ * becomes 0: its batch has no rows.  Calls on the same tables are for one stream, from several
+ * threads too (they are enqueued one after the other), or ordered by the caller; they may
  * be captured.  Errors: IBP_EINVAL, IBP_EALIGN, IBP_ECUDA. */
 IBP_API ibp_status ibp_paged_resize(const ibp_paged* cache, const ibp_paged_tables* tables,
                                     const int32_t* target, int32_t* q_starts, int64_t* slots,

@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "ibp.h"
 
@@ -202,6 +203,12 @@ struct ibp_paged {
 };
 
 namespace ibp {
+
+// The launches of one call hand something to each other through memory that calls may share:
+// attention its pieces through the workspace, a resize the list of free pages.  Calls that
+// share it (several threads on one stream) are enqueued one after the other: a lock for
+// each workspace, and for the tables.
+std::mutex& call_lock(const void* shared);
 
 // A handle on pages of 16-bit values, or of codes of one byte under the scales given;
 // the descriptor is checked.

@@ -3,7 +3,9 @@
 #pragma once
 
 #include "ibp_paged.cuh"
+#ifdef __CUDACC__
 #include "ibp_sm103.cuh"
+#endif
 
 namespace ibp {
 

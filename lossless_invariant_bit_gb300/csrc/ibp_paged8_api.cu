@@ -1,5 +1,7 @@
 // C-ABI of the paged K/V cache's additions: handles on pages held in 8 bits, and page
 // tables.
+#include <mutex>
+
 #include "ibp_internal.cuh"
 #include "ibp_paged8.cuh"
 
@@ -60,6 +62,7 @@ ibp_status ibp_paged_resize(const ibp_paged* c, const ibp_paged_tables* t, const
   a.n_tokens = n_tokens;
   a.n_pages = c->g.n_pages;
   a.page_lg = c->g.page_lg;
+  std::lock_guard<std::mutex> lock(ibp::call_lock(t->state));
   return ibp::launch_paged_resize(a, c->sm_count, reinterpret_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
              ? IBP_OK

@@ -65,21 +65,14 @@ void give_status(int device, int at) {
 
 }  // namespace
 
-// The launches of one attention call hand pieces to each other through its workspace, so
-// calls that share one (several threads on one stream) are enqueued one after the other:
-// a lock for each workspace, found by its address.
-namespace {
-
-constexpr size_t kLocks = 256;
-std::mutex g_call_mu[kLocks];
-
-std::mutex& call_lock(const void* workspace) {
-  uint64_t x = reinterpret_cast<uintptr_t>(workspace);
+// Found by the address, of 256 that are there.
+std::mutex& ibp::call_lock(const void* shared) {
+  constexpr size_t kLocks = 256;
+  static std::mutex mu[kLocks];
+  uint64_t x = reinterpret_cast<uintptr_t>(shared);
   x = (x >> 4) * 0x9E3779B97F4A7C15ull;  // (workspaces lie far apart: the upper bits tell)
-  return g_call_mu[x >> 56];
+  return mu[x >> 56];
 }
-
-}  // namespace
 
 namespace {
 
@@ -357,7 +350,7 @@ ibp_status ibp_paged_attention(const ibp_paged* c, const ibp_paged_batch* b, con
         !page_map(&wide_maps.v, d, wide.g.v, ibp::kBoxTokens, false))
       return IBP_ECUDA;
   }
-  std::lock_guard<std::mutex> lock(call_lock(workspace));
+  std::lock_guard<std::mutex> lock(ibp::call_lock(workspace));
   cudaError_t ce = staged ? run.stage(a, wide, c->sm_count, st) : cudaSuccess;
   if (ce == cudaSuccess && !few)
     ce = staged ? ibp::launch_paged_chunk(wide, wide_maps, c->sm_count, st)

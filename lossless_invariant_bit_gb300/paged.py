@@ -411,7 +411,9 @@ class PageTables:
     max_pages], kv_lens [n_seqs], and the free pages free_pages[:n_free], int32.
 
     Every sequence is empty at first and every page free; the tensors may be filled in
-    otherwise before a call."""
+    otherwise before a call.  Calls on the same tables are for one stream.  Several threads may
+    call there, one call follows the other; but the tensors, and with them the batch that
+    a call returned, are then the last call's."""
 
     def __init__(self, cache: PagedCache, n_seqs: int, max_pages: int):
         if n_seqs < 1 or max_pages < 1:
