@@ -164,7 +164,9 @@ class PagedCache:
                                  "[n_pages, kv_heads] on the pages' device")
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.n_pages, self.dtype, self.page_dtype, self.k, self.v = n_pages, dtype, held, k, v
-        self.k_scales, self.v_scales, self._codes = k_scales, v_scales, codes
+        self.k_scales, self.v_scales = k_scales, v_scales
+        # whether chunks may be long enough to make 16-bit pages of these
+        self._widens = codes and dtype is torch.bfloat16
         self.device, self._index = k.device, k.device.index
         self._bounds_shape = (n_pages, kv_heads, 2, head_dim)
         # a dimension of one element has no stride to speak of
@@ -321,7 +323,10 @@ class PagedCache:
                 raise ValueError("pages lists no pages")
         raw = _raw_stream(self._index)
         size = ibp.PAGED_WORKSPACE_BYTES
-        if self._codes and pages is None and batch.n_tokens > 64:
+        # The library says whether a batch's chunks make 16-bit pages; sequences of at most 16 rows
+        # of queries to a K/V head are no chunks.
+        if (self._widens and pages is None
+                and batch.desc.max_q_tokens * heads > 16 * self.kv_heads):
             want = ctypes.c_uint64(0)
             self._lib.ibp_paged_workspace(self.handle, batch.address, heads, ctypes.byref(want))
             if size < want.value <= _MOST_WORKSPACE:
