@@ -65,15 +65,10 @@ def _workspace(device: torch.device, raw: int) -> torch.Tensor:
 _MOST_WORKSPACE = 2 << 30
 
 
-def _large_workspace(device: torch.device, raw: int, bytes_: int) -> torch.Tensor:
-    """As _workspace, of at least as many bytes; the stream keeps the largest."""
-    if torch._C._cuda_isCurrentStreamCapturing():
-        return torch.empty(bytes_, dtype=torch.uint8, device=device)
-    ws = _workspaces.get((device.index, raw))
-    if ws is None or ws.numel() < bytes_:
-        ws = _workspaces[device.index, raw] = torch.empty(bytes_, dtype=torch.uint8,
-                                                          device=device)
-    return ws
+def _large_workspace(device: torch.device, bytes_: int) -> torch.Tensor:
+    """The call's alone: torch has it back, for what follows on the stream, when the call is
+    enqueued (the 3 us that this takes are beside a kernel of hundreds)."""
+    return torch.empty(bytes_, dtype=torch.uint8, device=device)
 
 
 def _as_stream(stream) -> torch.cuda.Stream:
@@ -334,7 +329,7 @@ class PagedCache:
         ws = None
         if size != ibp.PAGED_WORKSPACE_BYTES:
             try:
-                ws = _large_workspace(self.device, raw, size)
+                ws = _large_workspace(self.device, size)
             except torch.OutOfMemoryError:  # (the call does without)
                 size = ibp.PAGED_WORKSPACE_BYTES
         if ws is None:
