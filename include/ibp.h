@@ -522,12 +522,13 @@ IBP_API ibp_status ibp_paged_create(ibp_paged** out, const ibp_paged_desc* desc)
  *              largest scale does not hold becomes the largest code; infinities and NaN
  *              become NaN codes.  A page that new tokens go into belongs to one sequence
  *   attention  as over code * scale, in fp32 with weights and codes multiplied in fp16 (in
- *              bf16 where ibp_paged_workspace asks for more: then as over 16-bit pages);
+ *              bf16, as over 16-bit pages, where ibp_paged_workspace asks for more than
+ *              IBP_PAGED_WORKSPACE_BYTES and the call has it);
  *              the scales are exact.  Weights times their values' scale that lie below 2^-25
  *              of a row's largest are lost.  bf16 queries become fp16 numbers times a power of
  *              two for each row: a score is off by up to scale * 2^-39 * max |q| * sum |k| over
  *              the channels (no more than fp32 sums are, but where the keys are zero or tiny in
- *              the channels in which the row is large); not so as over 16-bit pages
+ *              the channels in which the row is large); both not so as over 16-bit pages
  *   bounds     of code * scale, rounded to the 16-bit type
  * A scale outside its range is an error like a page id out of range, where it is needed. */
 IBP_API ibp_status ibp_paged_create_8bit(ibp_paged** out, const ibp_paged_desc* desc,
@@ -598,7 +599,8 @@ IBP_API ibp_status ibp_paged_attention(const ibp_paged* cache, const ibp_paged_b
  * IBP_PAGED_WORKSPACE_BYTES, and for a handle on pages held in 8 bits, of type bf16, whose
  * chunks of new tokens are long, room for its pages as 16-bit ones, which are then made once
  * (n_seqs * max_pages pages: a table with columns that no sequence needs costs room).  With less
- * the result is computed from the codes, in more time.  Errors: IBP_EINVAL. */
+ * the result is computed from the codes, in more time, and with other roundings (weights to
+ * fp16, not to bf16).  Errors: IBP_EINVAL. */
 IBP_API ibp_status ibp_paged_workspace(const ibp_paged* cache, const ibp_paged_batch* batch,
                                        uint32_t q_heads, uint64_t* bytes);
 

@@ -113,6 +113,12 @@ class PagedCache:
     float8_e4m3fn: then a page's keys (values) of one head are codes under the scale in
     k_scales (v_scales) [n_pages, kv_heads], float8_e8m0fnu, which appends keep.
 
+    Long chunks of bfloat16 over 8-bit pages make 16-bit pages of them once, in a workspace of
+    up to `most_workspace` bytes (2 GiB), and round their weights to bfloat16 as over 16-bit
+    pages; where the batch's tables want more, or torch has no such memory left, they
+    take longer and the weights are rounded to float16.  With most_workspace=0 it is always so,
+    and a result does not depend on the memory that is free.
+
     Calls run on the current stream, or on `stream` (a torch stream or a
     cudaStream_t), on which their outputs and workspaces are then allocated too.
     The pages' device has to be the current one.  Several threads may call on one
@@ -124,8 +130,11 @@ class PagedCache:
                  v: Optional[torch.Tensor] = None, device=None,
                  page_dtype: Optional[torch.dtype] = None,
                  k_scales: Optional[torch.Tensor] = None,
-                 v_scales: Optional[torch.Tensor] = None):
+                 v_scales: Optional[torch.Tensor] = None,
+                 most_workspace: Optional[int] = None):
         self.handle = None
+        if most_workspace is not None and most_workspace < 0:
+            raise ValueError("most_workspace is not negative")
         if dtype not in _DTYPES:
             raise ValueError("a paged cache holds float16 or bfloat16")
         held = dtype if page_dtype is None else page_dtype
@@ -160,6 +169,7 @@ class PagedCache:
         self.kv_heads, self.head_dim, self.page_tokens = kv_heads, head_dim, page_tokens
         self.n_pages, self.dtype, self.page_dtype, self.k, self.v = n_pages, dtype, held, k, v
         self.k_scales, self.v_scales = k_scales, v_scales
+        self.most_workspace = most_workspace
         # whether chunks may be long enough to make 16-bit pages of these
         self._widens = codes and dtype is torch.bfloat16
         self.device, self._index = k.device, k.device.index
@@ -324,7 +334,8 @@ class PagedCache:
                 and batch.desc.max_q_tokens * heads > 16 * self.kv_heads):
             want = ctypes.c_uint64(0)
             self._lib.ibp_paged_workspace(self.handle, batch.address, heads, ctypes.byref(want))
-            if size < want.value <= _MOST_WORKSPACE:
+            most = _MOST_WORKSPACE if self.most_workspace is None else self.most_workspace
+            if size < want.value <= most:
                 size = want.value
         ws = None
         if size != ibp.PAGED_WORKSPACE_BYTES:

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from lossless_invariant_bit_gb300 import ibp
+from lossless_invariant_bit_gb300.paged import PagedCache
 from tests.gpu_util import DEV
 from tests.test_gpu_paged8 import BF16_WEIGHT, Setup, attend
 
@@ -32,3 +33,16 @@ def test_the_larger_workspace_is_given_back():
     held = torch.cuda.memory_allocated() - before
     assert held <= 3 * ibp.PAGED_WORKSPACE_BYTES + (1 << 20)
     s.check(*attend(s), weight=BF16_WEIGHT)
+
+
+def test_weights_over_codes_whatever_memory_is_free():
+    """most_workspace=0: weights are rounded to fp16, with room and without the same bits."""
+    s = Setup([900], [3000], 2, 2, 128, 32, torch.bfloat16)
+    s.check(*attend(s), weight=BF16_WEIGHT)
+    s.cache.most_workspace = 0
+    out, lse = attend(s)
+    s.check(out, lse)
+    c = PagedCache(2, 128, 32, s.n_pages, torch.bfloat16, k=s.cache.k, v=s.cache.v,
+                   page_dtype=torch.float8_e4m3fn, k_scales=s.cache.k_scales,
+                   v_scales=s.cache.v_scales, most_workspace=0)
+    assert torch.equal(c.attention(s.batch, s.q), out) and c.status() == 0

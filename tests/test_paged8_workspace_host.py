@@ -34,12 +34,12 @@ def asks(made, monkeypatch):  # noqa: F811
     return fake
 
 
-def attend(T, H, G, D, dtype, page_dtype=E4M3, pages=None):
+def attend(T, H, G, D, dtype, page_dtype=E4M3, pages=None, **more):
     shape = (5, 16, H, D)
     c = paged.PagedCache(H, D, 16, 5, dtype, k=Said(shape, page_dtype), v=Said(shape, page_dtype),
                          page_dtype=page_dtype,
                          **(dict(k_scales=Said((5, H), E8M0), v_scales=Said((5, H), E8M0))
-                            if page_dtype is E4M3 else {}))
+                            if page_dtype is E4M3 else {}), **more)
     b = paged.PagedBatch(Said((1, 4), I32), Said((1,), I32), Said((2,), I32), T, T)
     q = Said((T, H * G, D), dtype)
     c.attention(b, q, out=q, pages=pages)
@@ -67,3 +67,15 @@ def test_more_than_the_most_is_not_taken(asks):
     asks.wants = paged._MOST_WORKSPACE + 1
     attend(2048, 2, 8, 128, BF16)
     assert asks.called[1] == ("ibp_paged_attention", ibp.PAGED_WORKSPACE_BYTES)
+
+
+def test_the_user_says_how_much_it_may_be(asks):
+    """0: always the codes, with the rounding of their weights."""
+    asks.wants = ibp.PAGED_WORKSPACE_BYTES + 4096
+    for most, given in ((0, ibp.PAGED_WORKSPACE_BYTES), (asks.wants - 1, ibp.PAGED_WORKSPACE_BYTES),
+                        (asks.wants, asks.wants), (None, asks.wants)):
+        asks.called.clear()
+        attend(2048, 2, 8, 128, BF16, most_workspace=most)
+        assert asks.called[1] == ("ibp_paged_attention", given)
+    with pytest.raises(ValueError):
+        attend(2048, 2, 8, 128, BF16, most_workspace=-1)
