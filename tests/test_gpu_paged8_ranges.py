@@ -7,7 +7,7 @@ import torch
 
 from lossless_invariant_bit_gb300 import ibp, paged
 from tests.gpu_util import DEV
-from tests.test_gpu_paged8 import E4M3, F64, Setup, attend
+from tests.test_gpu_paged8 import BF16_WEIGHT, E4M3, F64, Setup, attend
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +103,17 @@ def test_a_query_with_one_large_channel(n, L, small, keys, monkeypatch):
     # the log of the sum moves by no more than the largest score does
     assert abs(float(lse[-1, 0]) - want) <= float(off.max()) + 2.0 ** -18
     assert s.cache.status() == 0
+
+
+# ---------------------------------------------------------------- 16-bit pages of all scales
+@pytest.mark.parametrize("q_lens,kv_lens,G,P", [([900], [1300], 2, 16), ([500, 700], [900, 1000], 4, 64)])
+def test_long_chunks_of_bf16_under_scales_of_the_whole_range(q_lens, kv_lens, G, P):
+    s = Setup(q_lens, kv_lens, G, 2, 128, P, torch.bfloat16, spread=0)
+    for w, spread in ((0, 12), (1, 49)):
+        live = s.scales[w] != 255
+        x = torch.randint(127 - spread, 127 + spread + 1, s.scales[w].shape, generator=s.g,
+                          device=DEV).to(torch.uint8)
+        s.scales[w].copy_(torch.where(live, x, s.scales[w]))
+    s.q *= 2.0 ** -8
+    assert ibp.ibp_paged_workspace(s.cache.handle, s.batch.desc, 2 * G) > ibp.PAGED_WORKSPACE_BYTES
+    s.check(*attend(s), weight=BF16_WEIGHT)
