@@ -7,14 +7,12 @@
 
 #include <atomic>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 #include <mutex>
 #include <thread>
 #include <vector>
 
-#include "ibp_paged8.cuh"
-#include "ibp_tma.cuh"
+#include "paged_fakes_host.h"
 
 namespace {
 
@@ -29,16 +27,9 @@ void note(const void* call) {
   usleep(200);  // the time of a launch, and room for the other thread
 }
 
-CUresult encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill) {
-  return CUDA_SUCCESS;
-}
-
 }  // namespace
 
 namespace ibp {
-EncodeTiledFn encode_tiled() { return &encode; }
 cudaError_t launch_paged_resize(const PagedTablesArgs& a, int, cudaStream_t) {
   note(a.q_starts);
   note(a.q_starts);
@@ -62,21 +53,6 @@ NOTHING(launch_paged_chunk_join, const PagedAttnArgs&, int, cudaStream_t)
 NOTHING(launch_paged8_chunk_join, const PagedAttnArgs&, int, cudaStream_t)
 NOTHING(launch_paged8_stage, const PagedAttnArgs&, const PagedAttnArgs&, int, cudaStream_t)
 }  // namespace ibp
-
-// the runtime, on host memory
-extern "C" {
-cudaError_t cudaMalloc(void** p, size_t n) { return (*p = malloc(n)) ? cudaSuccess : cudaErrorMemoryAllocation; }
-cudaError_t cudaFree(void* p) { return free(p), cudaSuccess; }
-cudaError_t cudaMemset(void* p, int v, size_t n) { return memset(p, v, n), cudaSuccess; }
-cudaError_t cudaMemsetAsync(void* p, int v, size_t n, cudaStream_t) { return memset(p, v, n), cudaSuccess; }
-cudaError_t cudaMemcpyAsync(void* d, const void* s, size_t n, cudaMemcpyKind, cudaStream_t) {
-  return memcpy(d, s, n), cudaSuccess;
-}
-cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
-cudaError_t cudaGetLastError(void) { return cudaSuccess; }
-cudaError_t cudaGetDevice(int* d) { return *d = 0, cudaSuccess; }
-cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { return *v = 152, cudaSuccess; }
-}
 
 int main(int argc, char** argv) {
   const bool shared = argc > 1 && !strcmp(argv[1], "threads");
