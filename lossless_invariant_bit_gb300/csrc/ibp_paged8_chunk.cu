@@ -28,8 +28,10 @@
 // bound by the conversions (every tile converts its keys again: about 3200 cycles a block of
 // 128 keys against 2830 of products), which is why long chunks of bf16 go to the 16-bit
 // pages' kernel, behind one conversion of their pages (k_paged8_stage).  24 sequences of up to
-// 333 new tokens, heads of 64, with a window: 65 us of the batch's 82, bound by the
-// exponentials as the 16-bit pages' kernel is there.  Codes by TMA into tiles of their own, read from
+// 333 new tokens, heads of 64, with a window: 65 us of the batch's 82; no unit is full: of 116
+// thousand cycles the rows' warps compute weights for 50 (2500 a block, exponentials 1050 of
+// them) and wait 25 to 33 for scores, of keys whose conversion takes 2870 a block; queries, results
+// and the run's start take 30.  Codes by TMA into tiles of their own, read from
 // there: 513 us, but 92 for 78 where a batch is mixed: the products' operands come through
 // the same memory.  Each page's scales in the rows' registers: 672.
 #include "ibp_paged8.cuh"

@@ -27,7 +27,7 @@ float8_e8m0fnu); every call is the same:
 The pages that sequences hold can be kept on the device:
 
     tables = cache.tables(n_seqs, max_pages)              # every page is free
-    batch, slots = tables.resize(target, n_tokens)        # lengths change: pages come and go
+    batch, slots = tables.resize(target, n_tokens, longest)  # lengths change: pages come and go
     cache.append(batch, k, v)                             # slots: the new tokens' rows
 """
 from __future__ import annotations
@@ -448,7 +448,8 @@ class PageTables:
                stream=None) -> Optional[Tuple[PagedBatch, torch.Tensor]]:
         """Sequence s gets target[s] tokens (int32 [n_seqs] on the device): pages come from the
         free ones or go back to them.  n_tokens: rows of the new tokens' arrays, at least
-        what sequences grow by together; of one at most max_q_tokens (n_tokens).  Returns the
+        what sequences grow by together; of one at most max_q_tokens (n_tokens: give it, 1 for a
+        step of single tokens, or attention takes each for a chunk and is slower).  Returns the
         batch of the new tokens, whose tensors are these tables' (another call changes them), and
         their slots (int64 [n_tokens]: page * page_tokens + place, rows of key_rows() and
         value_rows(); behind the last new token's they stay as they were); nothing when n_tokens
