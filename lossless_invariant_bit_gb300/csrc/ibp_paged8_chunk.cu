@@ -184,6 +184,8 @@ __device__ __noinline__ Sums wide_block(uint32_t ts, uint32_t to, uint32_t D, co
     s.l *= f;
     if (any) rescale(to, D, f);
   }
+  // the block's sum by itself: many equal weights added to a long sum are all rounded one way
+  float l[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
   for (int32_t q = 0; q < 128; q += 32) {
     uint32_t x[32];
@@ -191,9 +193,10 @@ __device__ __noinline__ Sums wide_block(uint32_t ts, uint32_t to, uint32_t D, co
     tmem_wait_ld(x);
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      s.l = fmaf(ex2(__uint_as_float(x[j]) - s.base), ex2(-pages[(uint32_t)(q + j) >> box_lg].y),
-                 s.l);
+      l[j & 3] = fmaf(ex2(__uint_as_float(x[j]) - s.base),
+                      ex2(-pages[(uint32_t)(q + j) >> box_lg].y), l[j & 3]);
   }
+  s.l += (l[0] + l[1]) + (l[2] + l[3]);
   return s;
 }
 

@@ -43,6 +43,19 @@ def test_a_large_scale_beside_the_heaviest_key(n, L, window, spread, dtype):
     s.check(out, lse, window=window, scale=1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_sums_of_many_equal_weights(dtype):
+    """Every second page's keys have scales 2^-24 of the others', and scores of about zero: 10000
+    equal weights, in blocks that take each page's scales.  (As many sequences and heads as
+    give a CTA a hundred blocks of a tile.)"""
+    s = Setup([130] * 10, [20000] * 10, 2, 8, 64, 16, dtype, spread=0)
+    pages = s.table.long()
+    s.scales[0][pages[:, ::2]] = 127 - 14
+    s.scales[0][pages[:, 1::2]] = 127 + 10
+    s.q *= 2.0 ** -17
+    s.check(*attend(s))
+
+
 # ---------------------------------------------------------------- factors of the scores
 @pytest.mark.parametrize("n,L,wide", [(1, 200, False), (3, 200, True), (60, 300, False),
                                       (60, 300, True), (300, 500, False), (300, 500, True)])
